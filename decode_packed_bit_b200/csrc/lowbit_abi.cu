@@ -60,6 +60,24 @@ lowbit_status q1m1_gemv_x_group_launch(const uint8_t *const *, const uint16_t *c
 bool q1m1_x_group_supported(int R, int M, int N, int K);
 lowbit_status q1m1_gemv_launch(const uint8_t *const *, const uint16_t *const *, const void *, float *const *,
                                int, int, int, cudaStream_t);
+size_t lora_workspace_bytes(int R, int M, int K, int rank);
+int lora_max_group();
+lowbit_status lora_launch(const uint16_t *, const int32_t *, const uint16_t *const *, const uint16_t *const *,
+                          const int32_t *, const float *, const float *const *, float *const *, int, int, int, int, int,
+                          int, void *, cudaStream_t);
+void rope_phases_host(lowbit_rope_scaling, int, double, double, double, double, double, int64_t *);
+lowbit_status rope_launch(const void *, int64_t, void *, int64_t, int, const void *, int64_t, void *, int64_t, int,
+                          lowbit_dtype, lowbit_dtype, const int32_t *, const int64_t *, int, int, int, int, float,
+                          cudaStream_t);
+int kv8_fault_flag();
+lowbit_status kv8_append_launch(const lowbit_kv8_cache &, const lowbit_kv8_batch &, const void *, int64_t, lowbit_dtype,
+                                const void *, int64_t, lowbit_dtype, cudaStream_t);
+lowbit_status kv8_read_launch(const lowbit_kv8_cache &, const lowbit_kv8_batch &, void *, void *, lowbit_dtype,
+                              cudaStream_t);
+int kv8_attn_fault_flag();
+size_t kv8_attn_workspace_bytes(const lowbit_kv8_cache &);
+lowbit_status kv8_attn_launch(const lowbit_kv8_cache &, const lowbit_kv8_batch &, const uint16_t *, int64_t, int, float,
+                              uint16_t *, int64_t, void *, cudaStream_t);
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int kQ1MaxM = 16;
@@ -109,8 +127,9 @@ int lowbit_version(void) { return 100; }
 int lowbit_fault_flags(void)
 {
     const int f4 = i4tc_fault_flag(), fs = q1stack_fault_flag(), fg = smg_fault_flag();
-    if (f4 < 0 || fs < 0 || fg < 0) return -1;
-    return (f4 ? 1 : 0) | (fs ? 4 : 0) | (fg ? 8 : 0);
+    const int fk = kv8_fault_flag(), fa = kv8_attn_fault_flag();
+    if (f4 < 0 || fs < 0 || fg < 0 || fk < 0 || fa < 0) return -1;
+    return (f4 ? 1 : 0) | (fs ? 4 : 0) | (fg ? 8 : 0) | (fk || fa ? 16 : 0);
 }
 
 lowbit_status lowbit_pack(lowbit_format fmt, const int8_t *codes, int64_t rows, int64_t cols,
@@ -480,6 +499,192 @@ lowbit_status lowbit_rmsnorm_bf16(const float *a, const float *b, int M, int D, 
     LB_CHECK(D % 8 == 0 && (int64_t)M * D < kMaxElems, LOWBIT_ERR_UNSUPPORTED_SHAPE);
     LB_CHECK(aligned16(a) && aligned16(out) && (b == nullptr || aligned16(b)), LOWBIT_ERR_MISALIGNED);
     return rmsnorm_launch(a, b, M, D, eps, out, as_stream(stream));
+}
+
+// ---------------------------------------------------------------------------
+// low-rank adapters
+// ---------------------------------------------------------------------------
+
+static lowbit_status lora_shape_ok(int R, int M, int N, int K, int rank)
+{
+    LB_CHECK(R >= 1 && R <= lora_max_group() && M >= 1 && N >= 1 && K >= 1 && rank >= 1, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(K % 64 == 0 && rank % 8 == 0 && rank <= 128 && N <= (1 << 30) && M <= (1 << 30),
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    LB_CHECK((int64_t)M * N < kMaxElems && (int64_t)M * K < kMaxElems, LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    return LOWBIT_OK;
+}
+
+size_t lowbit_lora_workspace_bytes(int R, int M, int N, int K, int rank)
+{
+    return lora_shape_ok(R, M, N, K, rank) == LOWBIT_OK ? lora_workspace_bytes(R, M, K, rank) : 0;
+}
+
+lowbit_status lowbit_lora_add_group(const uint16_t *x, const int32_t *ids, const uint16_t *const *a,
+                                    const uint16_t *const *b, const int32_t *ranks, const float *scales,
+                                    const float *const *base, float *const *y, int R, int M, int N, int K, int rank,
+                                    int n_adapters, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const lowbit_status s = lora_shape_ok(R, M, N, K, rank);
+    if (s != LOWBIT_OK) return s;
+    LB_CHECK(n_adapters >= 1 && x && ids && a && b && base && y && workspace, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK((int64_t)n_adapters * rank < kMaxElems / K && (int64_t)n_adapters * rank < kMaxElems / N,
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    LB_CHECK(aligned16(x) && aligned16(ids) && aligned16(workspace) && (!ranks || aligned16(ranks)) &&
+                 (!scales || aligned16(scales)),
+             LOWBIT_ERR_MISALIGNED);
+    for (int r = 0; r < R; ++r) {
+        LB_CHECK(a[r] && b[r] && base[r] && y[r], LOWBIT_ERR_INVALID_ARG);
+        LB_CHECK(aligned16(a[r]) && aligned16(b[r]) && aligned16(base[r]) && aligned16(y[r]), LOWBIT_ERR_MISALIGNED);
+    }
+    LB_CHECK(workspace_bytes >= lora_workspace_bytes(R, M, K, rank), LOWBIT_ERR_INVALID_ARG);
+    return lora_launch(x, ids, a, b, ranks, scales, base, y, R, M, N, K, rank, n_adapters, workspace,
+                       as_stream(stream));
+}
+
+lowbit_status lowbit_lora_add(const uint16_t *x, const int32_t *ids, const uint16_t *a, const uint16_t *b,
+                              const int32_t *ranks, const float *scales, const float *base, float *y, int M, int N,
+                              int K, int rank, int n_adapters, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return lowbit_lora_add_group(x, ids, &a, &b, ranks, scales, &base, &y, 1, M, N, K, rank, n_adapters, workspace,
+                                 workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// rotary positions
+// ---------------------------------------------------------------------------
+
+lowbit_status lowbit_rope_phases(lowbit_rope_scaling scaling, int rot, double base, double factor,
+                                 double trained_length, double slow, double fast, int64_t *phases)
+{
+    LB_CHECK(scaling == LOWBIT_ROPE_PLAIN || scaling == LOWBIT_ROPE_LINEAR || scaling == LOWBIT_ROPE_BASE ||
+                 scaling == LOWBIT_ROPE_BANDS,
+             LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(phases && rot >= 2 && base > 1.0 && base <= 1e300, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(rot % 2 == 0 && rot <= 1024, LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    if (scaling != LOWBIT_ROPE_PLAIN) LB_CHECK(factor >= 1.0 && factor <= 1e9, LOWBIT_ERR_INVALID_ARG);
+    if (scaling == LOWBIT_ROPE_BANDS)
+        LB_CHECK(trained_length > 0.0 && trained_length <= 1e18 && slow >= 0.0 && fast > slow && fast <= 1e18,
+                 LOWBIT_ERR_INVALID_ARG);
+    rope_phases_host(scaling, rot, base, factor, trained_length, slow, fast, phases);
+    return LOWBIT_OK;
+}
+
+lowbit_status lowbit_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int q_heads,
+                          const void *k, int64_t k_stride, void *k_out, int64_t k_out_stride, int kv_heads,
+                          lowbit_dtype in_type, lowbit_dtype out_type, const int32_t *positions,
+                          const int64_t *phases, int M, int head_dim, int rot, int interleaved, float magnitude,
+                          void *stream)
+{
+    LB_CHECK(M >= 1 && q_heads >= 0 && kv_heads >= 0 && q_heads <= 65536 && kv_heads <= 65536 &&
+                 q_heads + kv_heads >= 1 && positions && phases,
+             LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK((in_type == LOWBIT_F32 || in_type == LOWBIT_BF16) && (out_type == LOWBIT_F32 || out_type == LOWBIT_BF16),
+             LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(head_dim >= 8 && head_dim <= 1024 && head_dim % 8 == 0 && rot >= 2 && rot <= head_dim && rot % 2 == 0,
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    LB_CHECK(aligned16(positions) && aligned16(phases), LOWBIT_ERR_MISALIGNED);
+    const void *in[2] = {q, k};
+    void *out[2] = {q_out, k_out};
+    const int64_t is[2] = {q_stride, k_stride}, os[2] = {q_out_stride, k_out_stride};
+    const int heads[2] = {q_heads, kv_heads};
+    for (int i = 0; i < 2; ++i) {
+        if (heads[i] == 0) continue;
+        const int64_t row = (int64_t)heads[i] * head_dim;
+        LB_CHECK(in[i] && out[i] && is[i] >= row && os[i] >= row, LOWBIT_ERR_INVALID_ARG);
+        LB_CHECK(is[i] % 8 == 0 && os[i] % 8 == 0, LOWBIT_ERR_MISALIGNED);
+        LB_CHECK(is[i] < kMaxElems / M && os[i] < kMaxElems / M, LOWBIT_ERR_UNSUPPORTED_SHAPE);
+        LB_CHECK(aligned16(in[i]) && aligned16(out[i]), LOWBIT_ERR_MISALIGNED);
+        LB_CHECK(in[i] != out[i] || (in_type == out_type && is[i] == os[i]), LOWBIT_ERR_INVALID_ARG);
+    }
+    return rope_launch(q, q_stride, q_out, q_out_stride, q_heads, k, k_stride, k_out, k_out_stride, kv_heads, in_type,
+                       out_type, positions, phases, M, head_dim, rot, interleaved != 0, magnitude, as_stream(stream));
+}
+
+// ---------------------------------------------------------------------------
+// KV8 cache
+// ---------------------------------------------------------------------------
+
+static lowbit_status kv8_ok(const lowbit_kv8_cache *c, const lowbit_kv8_batch *b)
+{
+    LB_CHECK(c && b, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(c->n_pages >= 1 && c->n_heads >= 1 && b->n_seqs >= 0 && b->n_rows >= 0 && b->max_pages >= 1,
+             LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK((c->page_tokens == 32 || c->page_tokens == 64 || c->page_tokens == 128) &&
+                 (c->head_dim == 64 || c->head_dim == 128) && c->n_heads <= 1024,
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    LB_CHECK((int64_t)c->n_pages * c->n_heads < (int64_t(1) << 31) &&
+                 (int64_t)b->max_pages * c->page_tokens < (int64_t(1) << 31),
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    LB_CHECK(b->row_start || b->n_rows == b->n_seqs, LOWBIT_ERR_INVALID_ARG);
+    if (b->n_seqs == 0 || b->n_rows == 0) return LOWBIT_OK;
+    LB_CHECK(c->k && c->k_scales && c->v && c->v_scales && b->kv_len && b->page_table, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(aligned16(c->k) && aligned16(c->k_scales) && aligned16(c->v) && aligned16(c->v_scales) &&
+                 aligned16(b->kv_len) && aligned16(b->page_table) && (!b->row_start || aligned16(b->row_start)),
+             LOWBIT_ERR_MISALIGNED);
+    return LOWBIT_OK;
+}
+
+lowbit_status lowbit_kv8_append(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch, const void *k,
+                                int64_t k_stride, lowbit_dtype k_type, const void *v, int64_t v_stride,
+                                lowbit_dtype v_type, void *stream)
+{
+    const lowbit_status s = kv8_ok(cache, batch);
+    if (s != LOWBIT_OK) return s;
+    LB_CHECK((k_type == LOWBIT_F32 || k_type == LOWBIT_BF16) && (v_type == LOWBIT_F32 || v_type == LOWBIT_BF16),
+             LOWBIT_ERR_INVALID_ARG);
+    const int64_t row = (int64_t)cache->n_heads * cache->head_dim;
+    LB_CHECK(k_stride >= row && v_stride >= row, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(k_stride % 8 == 0 && v_stride % 8 == 0, LOWBIT_ERR_MISALIGNED);
+    if (batch->n_seqs == 0 || batch->n_rows == 0) return LOWBIT_OK;
+    LB_CHECK(k_stride < kMaxElems / batch->n_rows && v_stride < kMaxElems / batch->n_rows,
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    LB_CHECK(k && v, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(aligned16(k) && aligned16(v), LOWBIT_ERR_MISALIGNED);
+    return kv8_append_launch(*cache, *batch, k, k_stride, k_type, v, v_stride, v_type, as_stream(stream));
+}
+
+lowbit_status lowbit_kv8_read(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch, void *k_out, void *v_out,
+                              lowbit_dtype out_type, void *stream)
+{
+    const lowbit_status s = kv8_ok(cache, batch);
+    if (s != LOWBIT_OK) return s;
+    LB_CHECK(out_type == LOWBIT_F32 || out_type == LOWBIT_BF16, LOWBIT_ERR_INVALID_ARG);
+    if (batch->n_seqs == 0 || batch->n_rows == 0 || (!k_out && !v_out)) return LOWBIT_OK;
+    LB_CHECK((!k_out || aligned16(k_out)) && (!v_out || aligned16(v_out)), LOWBIT_ERR_MISALIGNED);
+    return kv8_read_launch(*cache, *batch, k_out, v_out, out_type, as_stream(stream));
+}
+
+static lowbit_status kv8_attn_ok(const lowbit_kv8_cache *c, const lowbit_kv8_batch *b, int q_heads)
+{
+    const lowbit_status s = kv8_ok(c, b);
+    if (s != LOWBIT_OK) return s;
+    LB_CHECK(q_heads >= 1 && q_heads % c->n_heads == 0, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(q_heads / c->n_heads <= 64 && (int64_t)b->n_rows * q_heads < (int64_t(1) << 31),
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    return LOWBIT_OK;
+}
+
+size_t lowbit_kv8_attention_workspace_bytes(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch, int q_heads)
+{
+    return kv8_attn_ok(cache, batch, q_heads) == LOWBIT_OK ? kv8_attn_workspace_bytes(*cache) : 0;
+}
+
+lowbit_status lowbit_kv8_attention(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch, const uint16_t *q,
+                                   int64_t q_stride, int q_heads, float scale, uint16_t *out, int64_t out_stride,
+                                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    const lowbit_status s = kv8_attn_ok(cache, batch, q_heads);
+    if (s != LOWBIT_OK) return s;
+    const int64_t row = (int64_t)q_heads * cache->head_dim;
+    LB_CHECK(scale == scale && scale - scale == 0.f && q_stride >= row && out_stride >= row, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(q_stride % 8 == 0 && out_stride % 8 == 0, LOWBIT_ERR_MISALIGNED);
+    if (batch->n_seqs == 0 || batch->n_rows == 0) return LOWBIT_OK;
+    LB_CHECK(q_stride < kMaxElems / batch->n_rows && out_stride < kMaxElems / batch->n_rows,
+             LOWBIT_ERR_UNSUPPORTED_SHAPE);
+    LB_CHECK(q && out && workspace, LOWBIT_ERR_INVALID_ARG);
+    LB_CHECK(aligned16(q) && aligned16(out) && aligned16(workspace), LOWBIT_ERR_MISALIGNED);
+    LB_CHECK(workspace_bytes >= kv8_attn_workspace_bytes(*cache), LOWBIT_ERR_INVALID_ARG);
+    return kv8_attn_launch(*cache, *batch, q, q_stride, q_heads, scale, out, out_stride, workspace, as_stream(stream));
 }
 
 }  // extern "C"

@@ -29,6 +29,7 @@ FORMATS = {"q1": LOWBIT_FMT_Q1_G128, "q2": LOWBIT_FMT_Q2, "int4": LOWBIT_FMT_INT
 
 # (name, restype, argtypes) of every symbol include/lowbit.h declares.
 P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+F64 = ctypes.c_double
 SYMBOLS = [
     ("lowbit_status_string", ctypes.c_char_p, [I32]),
     ("lowbit_version", I32, []),
@@ -55,6 +56,15 @@ SYMBOLS = [
     ("lowbit_rmsnorm_bf16", I32, [P, P, I32, I32, F32, P, P]),
     ("lowbit_q1g128_stack_workspace_bytes", SZ, [I32, I32, I32]),
     ("lowbit_q1g128_stack_step", I32, [P, P, I32, I32, I32, P, F32, P, SZ, P, P, P]),
+    ("lowbit_lora_workspace_bytes", SZ, [I32, I32, I32, I32, I32]),
+    ("lowbit_lora_add", I32, [P] * 8 + [I32, I32, I32, I32, I32, P, SZ, P]),
+    ("lowbit_lora_add_group", I32, [P] * 8 + [I32, I32, I32, I32, I32, I32, P, SZ, P]),
+    ("lowbit_rope_phases", I32, [I32, I32, F64, F64, F64, F64, F64, P]),
+    ("lowbit_rope", I32, [P, I64, P, I64, I32, P, I64, P, I64, I32, I32, I32, P, P, I32, I32, I32, I32, F32, P]),
+    ("lowbit_kv8_append", I32, [P, P, P, I64, I32, P, I64, I32, P]),
+    ("lowbit_kv8_read", I32, [P, P, P, P, I32, P]),
+    ("lowbit_kv8_attention_workspace_bytes", SZ, [P, P, I32]),
+    ("lowbit_kv8_attention", I32, [P, P, P, I64, I32, F32, P, I64, P, SZ, P]),
 ]
 
 _lib = None
@@ -315,3 +325,222 @@ def lowbit_q1g128_stack_step(w_bits, w_scales, x, hidden, ffn, workspace, eps=1e
                                           _ptr(record_inputs), _ptr(record_outputs), _stream(stream)),
            "lowbit_q1g128_stack_step")
 
+
+
+# -- low-rank adapters of many requests ---------------------------------------------
+#
+# The operands of these and of the following calls are checked here as far as the C
+# side cannot see them: element types, shapes, strides and the device.
+
+LOWBIT_F32 = 0
+LOWBIT_BF16 = 1
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
+
+
+def _dtypes():
+    import torch
+    return {torch.float32: LOWBIT_F32, torch.bfloat16: LOWBIT_BF16}
+
+
+def _dense(t, dtype, shape, what):
+    """t is a dense CUDA tensor of this type and shape on the current device."""
+    import torch
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}; expected the current CUDA device")
+
+
+def _rows(t, rows, heads, dim, what):
+    """Row stride of a [rows][heads][dim] tensor whose rows are dense (rows may lie apart)."""
+    import torch
+    if tuple(t.shape) != (rows, heads, dim) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{what}: expected shape {(rows, heads, dim)} with dense rows, got {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}; expected the current CUDA device")
+    return t.stride(0) if rows > 1 else heads * dim
+
+
+def _bits16(t):
+    import torch
+    return torch.bfloat16 if t.dtype is torch.bfloat16 else torch.int16
+
+
+def lowbit_lora_workspace_bytes(R: int, M: int, N: int, K: int, rank: int) -> int:
+    return int(lib().lowbit_lora_workspace_bytes(R, M, N, K, rank))
+
+
+def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, workspace=None, stream=None):
+    """y_r[m] = base_r[m] + scales[i] B_r,i (A_r,i x[m]) with i = ids[m] (any i outside the pool: y_r[m] = base_r[m]).
+
+    x bf16 [M][K], ids int32 [M]; a, b, base, ys: equal-length lists of bf16 [L][rank][K], bf16 [L][N][rank],
+    fp32 [M][N] and fp32 [M][N] (base_r may be y_r itself); ranks int32 [L] and scales fp32 [L], or None.
+    workspace: lowbit_lora_workspace_bytes(R, M, N, K, rank) bytes."""
+    import torch
+    R = len(a)
+    if not 1 <= R == len(b) == len(base) == len(ys):
+        raise ValueError("lowbit_lora_add_group: lists of different lengths")
+    M, K = x.shape
+    L, rank, _ = a[0].shape
+    N = b[0].shape[1]
+    _dense(x, _bits16(x), (M, K), "x")
+    _dense(ids, torch.int32, (M,), "ids")
+    for r in range(R):
+        _dense(a[r], _bits16(a[r]), (L, rank, K), "a")
+        _dense(b[r], _bits16(b[r]), (L, N, rank), "b")
+        _dense(base[r], torch.float32, (M, N), "base")
+        _dense(ys[r], torch.float32, (M, N), "y")
+    if ranks is not None:
+        _dense(ranks, torch.int32, (L,), "ranks")
+    if scales is not None:
+        _dense(scales, torch.float32, (L,), "scales")
+    pa, ka = _ptr_array(a)
+    pb, kb = _ptr_array(b)
+    pc, kc = _ptr_array(base)
+    py, ky = _ptr_array(ys)
+    _check(lib().lowbit_lora_add_group(_ptr(x), _ptr(ids), pa, pb, _ptr(ranks), _ptr(scales), pc, py, R, M, N, K, rank,
+                                       L, _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "lowbit_lora_add_group")
+
+
+def lowbit_lora_add(x, ids, a, b, base, y, ranks=None, scales=None, workspace=None, stream=None):
+    """One projection's adapters: see lowbit_lora_add_group."""
+    lowbit_lora_add_group(x, ids, [a], [b], [base], [y], ranks, scales, workspace, stream)
+
+
+# -- rotary positions ---------------------------------------------------------------
+
+def lowbit_rope_phases(rot: int, base: float = 10000.0, scaling="plain", factor: float = 1.0,
+                       trained_length: float = 0.0, slow: float = 1.0, fast: float = 32.0):
+    """The rot/2 phases (2^-64 turns per position) as an int64 CPU tensor; scaling "plain", "linear", "base" or "bands"."""
+    import torch
+    phases = torch.empty(max(rot, 0) // 2, dtype=torch.int64)
+    _check(lib().lowbit_rope_phases(ROPE_SCALINGS[scaling], rot, base, factor, trained_length, slow, fast,
+                                    _ptr(phases)), "lowbit_rope_phases")
+    return phases
+
+
+def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnitude=1.0, stream=None):
+    """q [M][q_heads][D] -> q_out and k [M][kv_heads][D] -> k_out (either pair may be None), fp32 or bf16, rows dense
+    and any stride (a multiple of 8) apart; positions int32 [M]; phases int64 [rot / 2].  In place where types match."""
+    import torch
+    ref, ref_out = (q, q_out) if q is not None else (k, k_out)
+    M, _, D = ref.shape
+    types = _dtypes()
+    half = phases.shape[0]
+    _dense(positions, torch.int32, (M,), "positions")
+    _dense(phases, torch.int64, (half,), "phases")
+    args = []
+    for name, i, o in (("q", q, q_out), ("k", k, k_out)):
+        if i is None:
+            args += [None, 0, None, 0, 0]
+            continue
+        if i.dtype is not ref.dtype or o.dtype is not ref_out.dtype:
+            raise ValueError("lowbit_rope: q and k have one input and one output type")
+        heads = i.shape[1]
+        args += [_ptr(i), _rows(i, M, heads, D, name), _ptr(o), _rows(o, M, heads, D, name + "_out"), heads]
+    _check(lib().lowbit_rope(*args, types[ref.dtype], types[ref_out.dtype], _ptr(positions), _ptr(phases), M, D,
+                             2 * half, 1 if interleaved else 0, float(magnitude), _stream(stream)), "lowbit_rope")
+
+
+# -- KV8 cache ----------------------------------------------------------------------
+
+class _KV8CacheC(ctypes.Structure):
+    _fields_ = [("k", P), ("k_scales", P), ("v", P), ("v_scales", P), ("n_pages", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _KV8BatchC(ctypes.Structure):
+    _fields_ = [("kv_len", P), ("page_table", P), ("row_start", P), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_rows", ctypes.c_int32)]
+
+
+class KV8Cache:
+    """The buffers of a KV8 cache: int8 codes k, v [n_pages][n_heads][page_tokens][head_dim] and fp32 scales
+    [n_pages][n_heads].  Holds them alive; a call reads or writes them in place."""
+
+    def __init__(self, k, k_scales, v, v_scales):
+        import torch
+        n_pages, heads, page, dim = k.shape
+        for name, t, dtype, shape in (("k", k, torch.int8, (n_pages, heads, page, dim)), ("v", v, torch.int8, k.shape),
+                                      ("k_scales", k_scales, torch.float32, (n_pages, heads)),
+                                      ("v_scales", v_scales, torch.float32, (n_pages, heads))):
+            _dense(t, dtype, shape, name)
+        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+        self.n_heads, self.page_tokens, self.head_dim, self.device = heads, page, dim, k.device
+        self._c = _KV8CacheC(k.data_ptr(), k_scales.data_ptr(), v.data_ptr(), v_scales.data_ptr(), n_pages, heads,
+                             page, dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_heads: int, page_tokens: int, head_dim: int, device="cuda"):
+        """A cache of zeros."""
+        import torch
+        shape = (n_pages, n_heads, page_tokens, head_dim)
+        return cls(*(f(s, dtype=d, device=device) for f, s, d in ((torch.zeros, shape, torch.int8),
+                   (torch.zeros, shape[:2], torch.float32), (torch.zeros, shape, torch.int8),
+                   (torch.zeros, shape[:2], torch.float32))))
+
+
+def _kv8_batch(cache, page_table, kv_len, row_start, rows):
+    import torch
+    B, width = page_table.shape
+    _dense(page_table, torch.int32, (B, width), "page_table")
+    _dense(kv_len, torch.int32, (B,), "kv_len")
+    if cache.device != page_table.device:
+        raise ValueError(f"page_table: on {page_table.device}, the cache on {cache.device}")
+    if row_start is not None:
+        _dense(row_start, torch.int32, (B + 1,), "row_start")
+    return _KV8BatchC(kv_len.data_ptr(), page_table.data_ptr(), None if row_start is None else row_start.data_ptr(), B,
+                      width, rows)
+
+
+def lowbit_kv8_append(cache: KV8Cache, page_table, kv_len, k, v, row_start=None, stream=None):
+    """Write k, v [rows][n_heads][head_dim] (fp32 or bf16 each, rows dense and any stride apart) as the sequences' last
+    tokens.  page_table int32 [B][max_pages], kv_len int32 [B] (the new tokens included), row_start int32 [B + 1], or
+    None for one row per sequence."""
+    rows = k.shape[0]
+    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows)
+    types = _dtypes()
+    ks = _rows(k, rows, cache.n_heads, cache.head_dim, "k")
+    vs = _rows(v, rows, cache.n_heads, cache.head_dim, "v")
+    _check(lib().lowbit_kv8_append(cache._ref, ctypes.byref(batch), _ptr(k), ks, types[k.dtype], _ptr(v), vs,
+                                   types[v.dtype], _stream(stream)), "lowbit_kv8_append")
+
+
+def lowbit_kv8_read(cache: KV8Cache, page_table, kv_len, k_out, v_out, row_start=None, stream=None):
+    """The values of the sequences' last tokens back from the cache: k_out, v_out [rows][n_heads][head_dim] (dense, one
+    type, fp32 or bf16; either may be None)."""
+    ref = k_out if k_out is not None else v_out
+    rows = ref.shape[0]
+    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            _dense(t, ref.dtype, (rows, cache.n_heads, cache.head_dim), name)
+    _check(lib().lowbit_kv8_read(cache._ref, ctypes.byref(batch), _ptr(k_out), _ptr(v_out), _dtypes()[ref.dtype],
+                                 _stream(stream)), "lowbit_kv8_read")
+
+
+def lowbit_kv8_attention_workspace_bytes(cache: KV8Cache, n_seqs: int, n_rows: int, q_heads: int) -> int:
+    """Bytes for calls with this many sequences and rows (zero-fill them once)."""
+    batch = _KV8BatchC(16, 16, 16, n_seqs, 1, n_rows)
+    return int(lib().lowbit_kv8_attention_workspace_bytes(cache._ref, ctypes.byref(batch), q_heads))
+
+
+def lowbit_kv8_attention(cache: KV8Cache, page_table, kv_len, q, out, scale, row_start=None, workspace=None,
+                         stream=None):
+    """out = softmax(scale q k^T) v of each row over its sequence's tokens up to the row's own position.
+
+    q, out bf16 [rows][q_heads][head_dim], rows dense and any stride (a multiple of 8) apart; page_table, kv_len and
+    row_start as for lowbit_kv8_append.  workspace: lowbit_kv8_attention_workspace_bytes(...) bytes, zero-filled before
+    their first use."""
+    import torch
+    rows, heads, dim = q.shape
+    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows)
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16:
+        raise ValueError(f"lowbit_kv8_attention: q and out are bfloat16, got {q.dtype} and {out.dtype}")
+    qs, os_ = _rows(q, rows, heads, cache.head_dim, "q"), _rows(out, rows, heads, cache.head_dim, "out")
+    _check(lib().lowbit_kv8_attention(cache._ref, ctypes.byref(batch), _ptr(q), qs, heads, float(scale), _ptr(out), os_,
+                                      _ptr(workspace), _nbytes(workspace), _stream(stream)), "lowbit_kv8_attention")

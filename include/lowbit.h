@@ -99,7 +99,8 @@ int lowbit_version(void);
  * tcgen05 GEMM ran out, bit 2 = a grid barrier of lowbit_q1g128_stack_step,
  * bit 3 = a wait on the shared activation ring of a small-batch kernel
  * (Q1_0_g128 at 2 <= M <= 16, INT4_G64 at 2 <= M <= 32; the results of such
- * a call are then not valid); -1 = the flags could not
+ * a call are then not valid), bit 4 = a length, page or row of a KV8 batch out
+ * of range (see lowbit_kv8_batch); -1 = the flags could not
  * be read.  This is a diagnostic call, not part of any product: it reads the
  * flags from device memory and therefore synchronises with the device (every
  * other entry point is asynchronous). */
@@ -423,6 +424,181 @@ lowbit_status lowbit_z80_generate(const uint8_t *const *w_packed, const int32_t 
  * ------------------------------------------------------------------------- */
 lowbit_status lowbit_rmsnorm_bf16(const float *a, const float *b, int M, int D, float eps,
                                   uint16_t *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * What a decoder needs beside the products: per-request adapters on a shared
+ * projection, rotary positions, and an 8-bit cache of keys and values with
+ * the attention that reads it.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of the operands that may be either. */
+typedef enum {
+    LOWBIT_F32 = 0,
+    LOWBIT_BF16 = 1
+} lowbit_dtype;
+
+/* Low-rank adapters of many requests beside a shared projection:
+ *     t[m][r] = sum_k a[i][r][k] * x[m][k]        r < ranks[i],  i = ids[m]
+ *     y[m][n] = base[m][n] + scales[i] * sum_r b[i][n][r] * t[m][r]
+ * and y[m] = base[m] for a row whose ids[m] is outside [0, n_adapters).
+ *
+ *   x      [M][K] bf16                  the projection's input
+ *   ids    [M] int32                    any order, any repetition
+ *   a      [n_adapters][rank][K] bf16   rows from ranks[i] on are not read
+ *   b      [n_adapters][N][rank] bf16   columns from ranks[i] on have no
+ *                                       effect, whatever they hold
+ *   ranks  [n_adapters] int32, or NULL (all equal rank); values outside
+ *          [0, rank] are clamped
+ *   scales [n_adapters] fp32, or NULL (all 1)
+ *   base   [M][N] fp32, the shared projection's output; may be y itself
+ *   y      [M][N] fp32
+ * Shapes: M >= 1, N >= 1, K >= 64 with K % 64 == 0, 8 <= rank <= 128 with
+ * rank % 8 == 0, n_adapters >= 1, M * N, M * K and the adapters' elements
+ * below 2^40.
+ * t is held in fp32 and meets b as the sum of three bf16 numbers, which
+ * carry all 24 bits of it; sums are fp32 in a fixed order, so the result is the same bits on every
+ * run and does not depend on which other rows are in the call's batch beyond
+ * the split that M chooses.
+ * Group form: R projections of one shape that read one x with one set of ids
+ * (HOST arrays of R device pointers, 1 <= R <= 16).
+ * workspace: lowbit_lora_workspace_bytes(R, M, N, K, rank) bytes; it needs no
+ * initialisation.  Calls that share one must be ordered on one stream. */
+size_t lowbit_lora_workspace_bytes(int R, int M, int N, int K, int rank);
+lowbit_status lowbit_lora_add(const uint16_t *x, const int32_t *ids, const uint16_t *a, const uint16_t *b,
+                              const int32_t *ranks, const float *scales, const float *base, float *y, int M,
+                              int N, int K, int rank, int n_adapters, void *workspace, size_t workspace_bytes,
+                              void *stream);
+lowbit_status lowbit_lora_add_group(const uint16_t *x, const int32_t *ids, const uint16_t *const *a,
+                                    const uint16_t *const *b, const int32_t *ranks, const float *scales,
+                                    const float *const *base, float *const *y, int R, int M, int N, int K,
+                                    int rank, int n_adapters, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* Rotary positions.  Of every head the first rot entries are turned in pairs:
+ * pair j (j < rot / 2) is (x[j], x[j + rot/2]), or (x[2j], x[2j+1]) when
+ * interleaved, and
+ *     (a, b) -> magnitude * (a cos w - b sin w, b cos w + a sin w),
+ *     w = 2 pi * ((positions[m] * phases[j]) mod 2^64) / 2^64;
+ * the other head_dim - rot entries are copied.  The product of position and
+ * phase wraps in integers, so the angle of a far position is as exact as that
+ * of a near one.  Sines and products are fp32, rounded once to the output type.
+ *
+ *   q, q_out  [M] rows of q_heads * head_dim elements of in_type / out_type,
+ *             rows q_stride / q_out_stride elements apart (multiples of 8,
+ *             at least a row); NULL with q_heads == 0
+ *   k, k_out  the same for kv_heads heads, so that one call turns both
+ *   positions [M] int32 (negative ones turn backwards)
+ *   phases    [rot / 2] int64 on the device: 2^-64 turns per position
+ * An output may be its input when types and strides are equal; other overlap
+ * is not allowed.  M >= 1, head_dim % 8 == 0, 8 <= head_dim <= 1024, rot even,
+ * 2 <= rot <= head_dim, q_heads + kv_heads >= 1.
+ *
+ * lowbit_rope_phases fills a HOST array of rot / 2 phases for the frequencies
+ * f_j = base^(-2j / rot) and one of the scalings for longer contexts:
+ *   LOWBIT_ROPE_PLAIN   f_j
+ *   LOWBIT_ROPE_LINEAR  f_j / factor (positions interpolated)
+ *   LOWBIT_ROPE_BASE    base' = base * factor^(rot / (rot - 2)): the slowest
+ *                       pair is factor times slower, the fastest unchanged
+ *   LOWBIT_ROPE_BANDS   by the turns u = trained_length * f_j / 2 pi that a pair
+ *                       makes over the trained length: f_j / factor where u <=
+ *                       slow, f_j where u >= fast, and between them c f_j +
+ *                       (1 - c) f_j / factor with c = (u - slow) / (fast - slow)
+ * (trained_length, slow and fast are read by the last only). */
+typedef enum {
+    LOWBIT_ROPE_PLAIN = 0,
+    LOWBIT_ROPE_LINEAR = 1,
+    LOWBIT_ROPE_BASE = 2,
+    LOWBIT_ROPE_BANDS = 3
+} lowbit_rope_scaling;
+lowbit_status lowbit_rope_phases(lowbit_rope_scaling scaling, int rot, double base, double factor,
+                                 double trained_length, double slow, double fast, int64_t *phases);
+lowbit_status lowbit_rope(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride, int q_heads,
+                          const void *k, int64_t k_stride, void *k_out, int64_t k_out_stride, int kv_heads,
+                          lowbit_dtype in_type, lowbit_dtype out_type, const int32_t *positions,
+                          const int64_t *phases, int M, int head_dim, int rot, int interleaved,
+                          float magnitude, void *stream);
+
+/* KV8 cache: keys and values as int8 codes in pages of page_tokens tokens,
+ * with one fp32 scale for each page and head; a value is code * scale.
+ *   k, v               [n_pages][n_heads][page_tokens][head_dim] int8
+ *   k_scales, v_scales [n_pages][n_heads] fp32
+ * page_tokens is 32, 64 or 128; head_dim is 64 or 128; n_heads <= 1024;
+ * n_pages * n_heads < 2^31.  The buffers may exceed 4 GB. */
+typedef struct {
+    int8_t *k;
+    float *k_scales;
+    int8_t *v;
+    float *v_scales;
+    int32_t n_pages, n_heads, page_tokens, head_dim;
+} lowbit_kv8_cache;
+
+/* Sequences and rows of a call.  Token t of sequence b lies in slot t %
+ * page_tokens of page page_table[b][t / page_tokens].  The call's rows belong
+ * to the sequences' last tokens: rows [row_start[b], row_start[b+1]) are the
+ * positions kv_len[b] - n_b .. kv_len[b] - 1 (n_b their number).
+ *   kv_len     [n_seqs] int32: tokens in the cache, the call's rows included
+ *   page_table [n_seqs][max_pages] int32; entries past a sequence's last
+ *              page are not read
+ *   row_start  [n_seqs + 1] int32, starting anywhere >= 0 and not falling;
+ *              or NULL: one row per sequence, row b (n_rows == n_seqs)
+ *   n_rows     rows of the operands; rows that belong to no sequence are not
+ *              read and their outputs not written
+ * All three arrays are device memory, read by the kernels: a captured graph
+ * follows what they hold at each replay.  Lengths and pages are checked there:
+ * kv_len is clamped to [0, max_pages * page_tokens], a page outside
+ * [0, n_pages) counts as absent (not written, not attended to, read as
+ * zeros), rows outside [0, n_rows) are skipped; each sets bit 4 (value 16) of
+ * lowbit_fault_flags().  A row whose position is negative (n_b > kv_len[b]) has no
+ * place: it is not written, reads as zeros and attends to nothing.
+ * n_seqs, n_rows >= 0 (0: no-op), max_pages >= 1, max_pages * page_tokens < 2^31. */
+typedef struct {
+    const int32_t *kv_len;
+    const int32_t *page_table;
+    const int32_t *row_start;
+    int32_t n_seqs, max_pages, n_rows;
+} lowbit_kv8_batch;
+
+/* Write new keys and values (k, v: n_rows rows of n_heads * head_dim elements,
+ * k_stride / v_stride elements apart, multiples of 8).  For each page and head
+ * that gets new tokens:
+ *     s' = max(s, fp32(max |new| / 127)), s taken as 0 unless the page already
+ *          holds older tokens of the sequence
+ *     an older token's code c becomes rint(c * s / s'); a new value's code is
+ *     rint(x / s'), both rounded exactly, ties to even (0 where s' = 0);
+ * the slots after the last token are left as they were.  NaN counts as 0 and
+ * infinities as the largest float.  A page's scale grows while the page fills,
+ * and each growth rounds its older codes once more (half a step of the new
+ * scale at most).  The result is the same bits on every run.  A page may get
+ * tokens of one sequence per call only. */
+lowbit_status lowbit_kv8_append(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch, const void *k,
+                                int64_t k_stride, lowbit_dtype k_type, const void *v, int64_t v_stride,
+                                lowbit_dtype v_type, void *stream);
+
+/* The values of the rows' positions back from the cache (the inverse of
+ * lowbit_kv8_append): k_out, v_out [n_rows][n_heads][head_dim] of out_type,
+ * dense; either may be NULL.  code * scale in fp32, rounded to out_type. */
+lowbit_status lowbit_kv8_read(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch, void *k_out,
+                              void *v_out, lowbit_dtype out_type, void *stream);
+
+/* Attention of the rows over their sequences' cached tokens:
+ *     out[r][j] = sum_t softmax_t(scale * q[r][j] . k[t][h]) v[t][h],
+ *     h = j / (q_heads / n_heads),
+ * over the tokens t <= the row's position (causal; a row without a place sees
+ * none and gives zeros).
+ *   q    n_rows rows of q_heads * head_dim bf16, q_stride elements apart
+ *   out  n_rows rows of q_heads * head_dim bf16, out_stride elements apart
+ *        (strides multiples of 8)
+ * q_heads a multiple of n_heads, at most 64 query heads per head of the cache.
+ * A non-finite q makes its row and head NaN.
+ * workspace: lowbit_kv8_attention_workspace_bytes(cache, batch, q_heads) bytes,
+ * zero-filled before its first use (calls leave what they need zeroed).  Calls
+ * that share one must be ordered on one stream; that holds for replays of
+ * captured graphs too. */
+size_t lowbit_kv8_attention_workspace_bytes(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch,
+                                            int q_heads);
+lowbit_status lowbit_kv8_attention(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch,
+                                   const uint16_t *q, int64_t q_stride, int q_heads, float scale, uint16_t *out,
+                                   int64_t out_stride, void *workspace, size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
