@@ -1,20 +1,25 @@
 // lora.cu -- low-rank adapters of many requests beside a shared projection:
 //     t[m] = A_i x[m],  y[m] = base[m] + s_i B_i t[m],  i = ids[m].
 //
-// Two launches.  The first forms t (fp32) for 16-row blocks and slices of K:
-// a warp takes the distinct adapters of its block one after the other, and
-// each lane's 16-byte loads of x and A are mma.sync m16n8k16 fragments as they
-// lie in memory (the k order inside a fragment is free as long as both operands
-// share it).  Only the rows of the adapter at hand are stored, so what another
-// adapter holds (infinities among it) cannot reach them.  The second adds s_i B_i t to base: t is
-// summed over the slices in order, scaled and split into three bf16 numbers,
-// which carry its 24 bits (two would leave an error of 2^-18 of t beside fp32
-// outputs); a warp holds the split of its 16 rows in registers and walks
-// over columns, 16 at a time, with B's 16-byte loads as fragments again.
+// Two launches.  The first forms t (fp32): a CTA takes rows, an adapter and a
+// slice of K; its warps cut the slice between them and add up through shared
+// memory in order.  Each lane's 16-byte loads of x and A are mma.sync m16n8k16
+// fragments as they lie in memory (the k order inside a fragment is free as
+// long as both operands share it).  The tensor core's accumulation cuts off a
+// little with each step, so a warp moves its sums to fp32 adds every 256 k.
+// The second launch adds s_i B_i t to base: t is summed over the slices in
+// order, scaled and split into three bf16 numbers, which carry its 24 bits (two
+// would leave an error of 2^-18 of t beside fp32 outputs); a warp holds the
+// split of its rows in registers and walks over columns, 16 at a time, with B's
+// loads as fragments again and the next step's loads under way.  All it needs
+// but t was there before the first launch began, so it loads ids, base and the
+// first of B before it waits for t.  Only rows of the adapter at hand are stored,
+// so what another adapter holds (infinities among it) cannot reach them.
 //
-// Rows stay in the caller's order: nothing is sorted, and a block costs one
-// pass over the weights of each adapter in it.  For decode batches that is the
-// bytes that have to be read anyway; prompts have one or two adapters a block.
+// Which rows a CTA takes: up to kLoraFewRows rows (decode), all rows of one
+// adapter, gathered, so that each adapter's weights are read once; beyond that
+// (prompts, where neighbours share an adapter) blocks of 16 or 32 rows in the
+// caller's order, with a pass for each adapter in the block.  Nothing is sorted.
 // Bound by the adapters' bytes for decode, by base and y (8 bytes an output)
 // for prompts.
 #include <algorithm>
@@ -27,6 +32,7 @@ constexpr int kLoraMaxGroup = 16;
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraMaxSlices = 64;
+constexpr int kLoraFewRows = kLoraThreads;  // one id per thread
 
 struct LoraArgs {
     const uint16_t *x;
@@ -38,7 +44,6 @@ struct LoraArgs {
     float *t;  // [R][slices][M][rank]
     int M, N, K, rank, L;
     int slices, kslice;  // slices of kslice k (a multiple of 32)
-    int parts;           // warps that share a block's adapters
     int cols;            // columns per CTA of the second launch
 };
 
@@ -50,216 +55,514 @@ __device__ __forceinline__ void lora_mma(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Of a block's 16 ids (lane r < 16 holds row r's, -1 for none): the lanes that
-// hold the first row of each distinct adapter.
+// Of a block's ids (lane r holds row r's, -1 for none): the lanes that hold the
+// first row of each distinct adapter.
 __device__ __forceinline__ unsigned lora_distinct(int id, int lane)
 {
     const unsigned same = __match_any_sync(0xffffffffu, id);
-    const bool first = lane < 16 && id >= 0 && (same & ((1u << lane) - 1) & 0xFFFFu) == 0;
-    return __ballot_sync(0xffffffffu, first);
+    return __ballot_sync(0xffffffffu, id >= 0 && (same & ((1u << lane) - 1)) == 0);
 }
 
+// Past L1: the second launch reads them before it waits for the first.
 __device__ __forceinline__ int lora_id(const LoraArgs &a, int64_t m)
 {
     if (m >= a.M) return -1;
-    const int id = __ldg(a.ids + m);
+    const int id = __ldcg(a.ids + m);
     return (unsigned)id < (unsigned)a.L ? id : -1;
 }
 
 __device__ __forceinline__ int lora_rank(const LoraArgs &a, int id)
 {
-    return a.ranks ? min(max(__ldg(a.ranks + id), 0), a.rank) : a.rank;
+    if (id < 0) return 0;
+    return a.ranks ? min(max(__ldcg(a.ranks + id), 0), a.rank) : a.rank;
 }
 
-// One warp: (row block, slice of K, projection, share of the block's adapters).
-template <int NT>  // rank / 8, rounded up to 2, 4, 8 or 16
-__global__ void __launch_bounds__(kLoraThreads) k_lora_shrink(const LoraArgs a)
+template <int NT, int RB>
+struct LoraShrink {
+    static constexpr int kLd = NT * 8 + 2;                                 // floats per row of a warp's sums
+    static constexpr int kBytes = kLoraWarps * RB * 16 * kLd * 4;
+};
+
+// A warp's sums over [k0, k1) of the products of 16 RB rows of x (xp: the rows
+// this lane loads, null for none) with `rank` rows of A, into shared memory.
+template <int NT, int RB>
+__device__ __forceinline__ void lora_dot(float *mine, const uint16_t *const (&xp)[RB][2], const uint16_t *w, int rank, int K,
+                                         int k0, int k1, int g)
 {
-    pdl_wait_primary();
-    pdl_launch_dependents();  // after the wait: the next launch may then read what came before this one
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int64_t task = (int64_t)blockIdx.x * kLoraWarps + (threadIdx.x >> 5);
-    const int part = (int)(task % a.parts), slice = (int)(task / a.parts % a.slices);
-    const int64_t block = task / ((int64_t)a.parts * a.slices);
-    if (block * 16 >= a.M) return;
-    const int target = blockIdx.y;
-    const int id = lora_id(a, lane < 16 ? block * 16 + lane : a.M);
-    unsigned todo = lora_distinct(id, lane);
-    const int id_lo = __shfl_sync(0xffffffffu, id, g), id_hi = __shfl_sync(0xffffffffu, id, g + 8);
-    const int k0 = slice * a.kslice, k1 = min(a.K, k0 + a.kslice);
-    const int64_t m_lo = block * 16 + g, m_hi = m_lo + 8;
-    const uint16_t *x_lo = a.x + min(m_lo, (int64_t)a.M - 1) * a.K, *x_hi = a.x + min(m_hi, (int64_t)a.M - 1) * a.K;
-    float *tp = a.t + ((int64_t)target * a.slices + slice) * a.M * a.rank;
-    for (int nth = 0; todo; ++nth) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        if (nth % a.parts != part) continue;
-        const int i = __shfl_sync(0xffffffffu, id, src);
-        const int rank = lora_rank(a, i);
-        const bool lo = id_lo == i, hi = id_hi == i;
-        float acc[NT][4];
+    constexpr int LD = LoraShrink<NT, RB>::kLd;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    int kc = k0;
+    do {
+        float acc[RB][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
-        const uint16_t *w = a.a[target] + ((int64_t)i * a.rank + g) * a.K;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-        for (int k = k0 + t * 8; k < k1; k += 32) {
-            const uint4 xl = lo ? __ldg(reinterpret_cast<const uint4 *>(x_lo + k)) : zero;
-            const uint4 xh = hi ? __ldg(reinterpret_cast<const uint4 *>(x_hi + k)) : zero;
-            uint4 wv[NT];
+        for (int b = 0; b < RB; ++b)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                wv[n] = n * 8 + g < rank ? __ldg(reinterpret_cast<const uint4 *>(w + (int64_t)n * 8 * a.K + k)) : zero;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                lora_mma(acc[n], xl.x, xh.x, xl.y, xh.y, wv[n].x, wv[n].y);
-                lora_mma(acc[n], xl.z, xh.z, xl.w, xh.w, wv[n].z, wv[n].w);
-            }
+                for (int c = 0; c < 4; ++c) acc[b][n][c] = 0.f;
+        const int ke = min(k1, kc + 256);
+#pragma unroll(NT *RB <= 4 ? 4 : 2)
+        for (int k = kc; k < ke; k += 32) {
+            uint4 wv[NT], x[RB][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                wv[n] = n * 8 + g < rank ? __ldg(reinterpret_cast<const uint4 *>(w + (int64_t)n * 8 * K + k)) : zero;
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    x[b][h] = xp[b][h] ? __ldg(reinterpret_cast<const uint4 *>(xp[b][h] + k)) : zero;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    lora_mma(acc[b][n], x[b][0].x, x[b][1].x, x[b][0].y, x[b][1].y, wv[n].x, wv[n].y);
+                    lora_mma(acc[b][n], x[b][0].z, x[b][1].z, x[b][0].w, x[b][1].w, wv[n].z, wv[n].w);
+                }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = n * 8 + 2 * t;
-            if (r < a.rank) {
-                if (lo) *reinterpret_cast<float2 *>(tp + m_lo * a.rank + r) = make_float2(acc[n][0], acc[n][1]);
-                if (hi) *reinterpret_cast<float2 *>(tp + m_hi * a.rank + r) = make_float2(acc[n][2], acc[n][3]);
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2 *p = reinterpret_cast<float2 *>(mine + (b * 16 + h * 8) * LD + n * 8);
+                    float2 s = make_float2(acc[b][n][2 * h], acc[b][n][2 * h + 1]);
+                    if (kc > k0) {
+                        s.x += p->x;
+                        s.y += p->y;
+                    }
+                    *p = s;
+                }
+        kc += 256;
+    } while (kc < k1);
+}
+
+// The sum over the CTA's warps of entries r, r + 1 of a row.
+template <int NT, int RB>
+__device__ __forceinline__ float2 lora_warps_sum(const float *red, int row, int r)
+{
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < kLoraWarps; ++q) {
+        const float2 v = *reinterpret_cast<const float2 *>(red + (q * RB * 16 + row) * LoraShrink<NT, RB>::kLd + r);
+        s.x += v.x;
+        s.y += v.y;
+    }
+    return s;
+}
+
+// This warp's part of a slice of K.
+__device__ __forceinline__ int2 lora_range(const LoraArgs &a, int slice, int warp)
+{
+    const int s0 = slice * a.kslice, s1 = min(a.K, s0 + a.kslice);
+    const int sub = ((s1 - s0 + kLoraWarps - 1) / kLoraWarps + 31) / 32 * 32;
+    const int k0 = min(s1, s0 + warp * sub);
+    return make_int2(k0, min(s1, k0 + sub));
+}
+
+// The rows of row m's adapter, in order, when m is the first of them: their
+// number, and rows[] filled; 0 for the others and for rows without an adapter.
+// Called by all threads of a CTA, M <= kLoraFewRows.
+struct LoraRows {
+    int id, n, rank;
+};
+__device__ __forceinline__ LoraRows lora_gather(const LoraArgs &a, int m, int *rows, int *warp_n)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int mine = lora_id(a, tid), id = lora_id(a, m);
+    const bool same = tid < a.M && mine == id && id >= 0;
+    const bool later = __syncthreads_or(same && tid < m);
+    const unsigned vote = __ballot_sync(0xffffffffu, same);
+    if (lane == 0) warp_n[warp] = __popc(vote);
+    __syncthreads();
+    int at = 0, n = 0;
+#pragma unroll
+    for (int w = 0; w < kLoraWarps; ++w) {
+        if (w < warp) at += warp_n[w];
+        n += warp_n[w];
+    }
+    if (same) rows[at + __popc(vote & ((1u << lane) - 1))] = tid;
+    __syncthreads();
+    return LoraRows{id, later ? 0 : n, lora_rank(a, id)};
+}
+
+// Few rows: grid (rows x slices, projections); the CTA of an adapter's first
+// row takes all its rows, the others leave.
+template <int NT>
+__global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_few(const LoraArgs a)
+{
+    using S = LoraShrink<NT, 1>;
+    extern __shared__ __align__(16) float red[];
+    __shared__ int rows[kLoraFewRows], warp_n[kLoraWarps];
+    pdl_wait_primary();
+    pdl_launch_dependents();  // after the wait: the next launch may read whatever came before this one
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int slice = blockIdx.x % a.slices, m = blockIdx.x / a.slices, target = blockIdx.y;
+    const LoraRows own = lora_gather(a, m, rows, warp_n);
+    if (own.n == 0) return;
+    const int2 k = lora_range(a, slice, warp);
+    const uint16_t *w = a.a[target] + ((int64_t)own.id * a.rank + g) * a.K + t * 8;
+    float *tp = a.t + ((int64_t)target * a.slices + slice) * a.M * a.rank;
+    const int half = a.rank / 2;
+    for (int r0 = 0; r0 < own.n; r0 += 16) {
+        const uint16_t *xp[1][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            xp[0][h] = r0 + h * 8 + g < own.n ? a.x + (int64_t)rows[r0 + h * 8 + g] * a.K + t * 8 : nullptr;
+        lora_dot<NT, 1>(red + (warp * 16 + g) * S::kLd + 2 * t, xp, w, own.rank, a.K, k.x, k.y, g);
+        __syncthreads();
+        for (int e = threadIdx.x; e < min(16, own.n - r0) * half; e += kLoraThreads) {
+            const int row = e / half, r = e % half * 2;
+            *reinterpret_cast<float2 *>(tp + (int64_t)rows[r0 + row] * a.rank + r) = lora_warps_sum<NT, 1>(red, row, r);
+        }
+        __syncthreads();
+    }
+}
+
+// Many rows: grid (blocks of 16 RB rows x slices, projections).
+// NT: rank / 8, rounded up to 2, 4, 8 or 16.
+template <int NT, int RB>
+__global__ void __launch_bounds__(kLoraThreads) k_lora_shrink(const LoraArgs a)
+{
+    using S = LoraShrink<NT, RB>;
+    extern __shared__ __align__(16) float red[];
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int slice = blockIdx.x % a.slices, target = blockIdx.y;
+    const int64_t m0 = (int64_t)(blockIdx.x / a.slices) * (16 * RB);
+    const int id = lora_id(a, lane < 16 * RB ? m0 + lane : a.M);
+    const int my_rank = lora_rank(a, id);
+    const int2 k = lora_range(a, slice, warp);
+    float *tp = a.t + ((int64_t)target * a.slices + slice) * a.M * a.rank;
+    const int half = a.rank / 2;
+    for (unsigned todo = lora_distinct(id, lane); todo; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1;
+        const int i = __shfl_sync(0xffffffffu, id, src), rank = __shfl_sync(0xffffffffu, my_rank, src);
+        const uint16_t *xp[RB][2];
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = b * 16 + h * 8 + g;
+                xp[b][h] = __shfl_sync(0xffffffffu, id, r) == i ? a.x + (m0 + r) * a.K + t * 8 : nullptr;
             }
+        lora_dot<NT, RB>(red + (warp * RB * 16 + g) * S::kLd + 2 * t, xp,
+                         a.a[target] + ((int64_t)i * a.rank + g) * a.K + t * 8, rank, a.K, k.x, k.y, g);
+        __syncthreads();
+        for (int e = threadIdx.x; e < RB * 16 * half; e += kLoraThreads) {
+            const int row = e / half, r = e % half * 2;
+            if (lora_id(a, m0 + row) == i)
+                *reinterpret_cast<float2 *>(tp + (m0 + row) * a.rank + r) = lora_warps_sum<NT, RB>(red, row, r);
+        }
+        __syncthreads();
+    }
+}
+
+// Four columns of a row of base or y; VEC: rows are 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ float4 lora_load4(const float *p, int left)
+{
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (VEC) {
+        if (left > 0) v = __ldcg(reinterpret_cast<const float4 *>(p));
+    } else {
+        if (left > 0) v.x = __ldcg(p);
+        if (left > 1) v.y = __ldcg(p + 1);
+        if (left > 2) v.z = __ldcg(p + 2);
+        if (left > 3) v.w = __ldcg(p + 3);
+    }
+    return v;
+}
+template <bool VEC>
+__device__ __forceinline__ void lora_store4(float *p, int left, const float4 &v)
+{
+    if (VEC) {
+        if (left > 0) *reinterpret_cast<float4 *>(p) = v;
+    } else {
+        if (left > 0) p[0] = v.x;
+        if (left > 1) p[1] = v.y;
+        if (left > 2) p[2] = v.z;
+        if (left > 3) p[3] = v.w;
+    }
+}
+
+// B's fragments for 16 columns from n0: column q of tile j is n0 + 4 (q / 2) +
+// 2 j + q % 2, so that a thread's results are four consecutive columns, n0 +
+// 4 t .., of its rows.
+template <int KT>
+__device__ __forceinline__ void lora_load_b(const LoraArgs &a, const uint16_t *wb, int n0, int i, int rank, int g, int t,
+                                            uint2 (&bw)[2][KT])
+{
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int col = n0 + 4 * (g >> 1) + 2 * j + (g & 1);
+        const uint16_t *w = wb + ((int64_t)i * a.N + min(col, a.N - 1)) * a.rank + 4 * t;
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+            bw[j][k] = k * 16 + 4 * t < rank ? __ldcg(reinterpret_cast<const uint2 *>(w + k * 16)) : make_uint2(0u, 0u);
+    }
+}
+
+// Clears the entries from the rank on, which may hold anything (whole groups of
+// four were not loaded).
+template <int KT>
+__device__ __forceinline__ void lora_clear_b(int rank, int t, uint2 (&bw)[2][KT])
+{
+    if ((rank & 3) == 0) return;
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        const int left = rank - (k * 16 + 4 * t);
+        const uint32_t mx = left == 1 ? 0xFFFFu : ~0u, my = left < 3 ? 0u : left == 3 ? 0xFFFFu : ~0u;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            bw[j][k].x &= mx;
+            bw[j][k].y &= my;
         }
     }
 }
 
-// Grid: (16-row blocks, column ranges, projections): neighbours share B.
-template <int KT, bool VEC>  // KT: rank / 16, rounded up to 1, 2, 4 or 8; VEC: rows of y are 16-byte aligned
-__global__ void __launch_bounds__(kLoraThreads) k_lora_expand(const LoraArgs a)
+// Four entries of t of row m, adapter i: slices in order, scaled, 0 from the
+// rank on.
+__device__ __forceinline__ float4 lora_t4(const LoraArgs &a, int target, int64_t m, int i, int rank, int r)
 {
-    constexpr int LD = KT * 16 + 4;  // floats per row of t in shared memory
-    __shared__ __align__(16) float ts[16 * LD];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    const int target = blockIdx.z;
-    const int64_t m0 = (int64_t)blockIdx.x * 16;
-    const int id = lora_id(a, lane < 16 ? m0 + lane : a.M);
-    const unsigned distinct = lora_distinct(id, lane);
-    const int id_lo = __shfl_sync(0xffffffffu, id, g), id_hi = __shfl_sync(0xffffffffu, id, g + 8);
-    // t of the block's rows, slices in order, scaled; 0 past an adapter's rank
-    if (distinct)
-        for (int e = threadIdx.x; e < 16 * KT * 4; e += kLoraThreads) {
-            const int row = e / (KT * 4), r = e % (KT * 4) * 4;
-            const int i = lora_id(a, m0 + row);
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i >= 0 && r < a.rank) {
-                const float *p = a.t + ((int64_t)target * a.slices * a.M + m0 + row) * a.rank + r;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r >= rank) return s;
+    const float *p = a.t + ((int64_t)target * a.slices * a.M + m) * a.rank + r;
 #pragma unroll 4
-                for (int q = 0; q < a.slices; ++q) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p + (int64_t)q * a.M * a.rank);
-                    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-                }
-                const float f = a.scales ? __ldg(a.scales + i) : 1.f;
-                const int rank = lora_rank(a, i) - r;
-                s.x = rank > 0 ? s.x * f : 0.f;
-                s.y = rank > 1 ? s.y * f : 0.f;
-                s.z = rank > 2 ? s.z * f : 0.f;
-                s.w = rank > 3 ? s.w * f : 0.f;
-            }
-            *reinterpret_cast<float4 *>(ts + row * LD + r) = s;
+    for (int q = 0; q < a.slices; ++q) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (int64_t)q * a.M * a.rank));
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    const float f = a.scales ? __ldcg(a.scales + i) : 1.f;
+    s.x *= f;
+    s.y = rank - r > 1 ? s.y * f : 0.f;
+    s.z = rank - r > 2 ? s.z * f : 0.f;
+    s.w = rank - r > 3 ? s.w * f : 0.f;
+    return s;
+}
+
+// The three bf16 numbers of four values as fragment words: out[s][w * 2].
+__device__ __forceinline__ void lora_split(const float4 &v, uint32_t (&f)[3][4], int h)
+{
+    float p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint32_t u;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(p[2 * w + 1]), "f"(p[2 * w]));
+            f[s][w * 2 + h] = u;
+            p[2 * w] -= __uint_as_float(u << 16);
+            p[2 * w + 1] -= __uint_as_float(u & 0xFFFF0000u);
         }
-    __syncthreads();
-    // three bf16 numbers per value: fragment words {row g, g + 8} x {4 t + 0..1, 2..3}
-    uint32_t f[KT][3][4];
-    if (distinct) {
+}
+
+template <int KT>
+__device__ __forceinline__ void lora_mul(const uint32_t (&f)[KT][3][4], const uint2 (&bw)[2][KT], float4 &lo, float4 &hi)
+{
+    float acc[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[j][c] = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
-            for (int hi = 0; hi < 2; ++hi) {
-                const float4 v = *reinterpret_cast<const float4 *>(ts + (g + 8 * hi) * LD + k * 16 + 4 * t);
-                float p[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int s = 0; s < 3; ++s)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        uint32_t u;
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(p[2 * w + 1]), "f"(p[2 * w]));
-                        f[k][s][w * 2 + hi] = u;
-                        p[2 * w] -= __uint_as_float(u << 16);
-                        p[2 * w + 1] -= __uint_as_float(u & 0xFFFF0000u);
-                    }
-            }
+            for (int s = 0; s < 3; ++s)
+                lora_mma(acc[j], f[k][s][0], f[k][s][1], f[k][s][2], f[k][s][3], bw[j][k].x, bw[j][k].y);
     }
+    lo = make_float4(acc[0][0], acc[0][1], acc[1][0], acc[1][1]);
+    hi = make_float4(acc[0][2], acc[0][3], acc[1][2], acc[1][3]);
+}
+
+__device__ __forceinline__ void lora_acc(float4 &o, const float4 &v)
+{
+    o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+}
+
+// Few rows: grid (rows, column ranges, projections); the CTA of an adapter's
+// first row takes all its rows, 16 at a time; a row without an adapter is copied.
+// KT: rank / 16, rounded up to 1, 2, 4 or 8.
+template <int KT, bool VEC>
+__global__ void __launch_bounds__(kLoraThreads, KT <= 4 ? 2 : 1) k_lora_expand_few(const LoraArgs a)
+{
+    __shared__ int rows[kLoraFewRows], warp_n[kLoraWarps];
+    __shared__ uint4 frag[KT * 3 * 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    pdl_launch_dependents();
+    const int target = blockIdx.z;
+    const LoraRows own = lora_gather(a, blockIdx.x, rows, warp_n);
     const float *base = a.base[target];
     float *y = a.y[target];
-    const int64_t r_lo = m0 + g, r_hi = r_lo + 8;
+    const int c0 = blockIdx.y * a.cols, n_end = min(a.N, c0 + a.cols);
+    if (own.n == 0) {
+        pdl_wait_primary();
+        if (own.id < 0 && y != base)
+            for (int n = c0 + threadIdx.x; n < n_end; n += kLoraThreads)
+                y[(int64_t)blockIdx.x * a.N + n] = base[(int64_t)blockIdx.x * a.N + n];
+        return;
+    }
+    constexpr int kStep = kLoraWarps * 16;
+    for (int r0 = 0; r0 < own.n; r0 += 16) {
+        int64_t at[2];  // offsets of this thread's rows, -1 for none
+#pragma unroll
+        for (int h = 0; h < 2; ++h) at[h] = r0 + h * 8 + g < own.n ? (int64_t)rows[r0 + h * 8 + g] * a.N : -1;
+        int n0 = c0 + warp * 16;
+        float4 nbase[2];
+        uint2 nb[2][KT];
+        auto prefetch = [&](int n0) {
+            lora_load_b<KT>(a, a.b[target], n0, own.id, own.rank, g, t, nb);
+            const int n = n0 + 4 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                nbase[h] = lora_load4<VEC>(base + (at[h] < 0 ? 0 : at[h]) + n, at[h] < 0 ? 0 : a.N - n);
+        };
+        if (n0 < n_end) prefetch(n0);
+        if (r0 == 0)
+            pdl_wait_primary();
+        else
+            __syncthreads();  // frag is free again
+        for (int e = threadIdx.x; e < KT * 32; e += kLoraThreads) {
+            const int k = e / 32, eg = (e & 31) >> 2, et = e & 3;
+            uint32_t f[3][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r0 + h * 8 + eg < own.n)
+                    v = lora_t4(a, target, rows[r0 + h * 8 + eg], own.id, own.rank, k * 16 + 4 * et);
+                lora_split(v, f, h);
+            }
+#pragma unroll
+            for (int s = 0; s < 3; ++s) frag[(k * 3 + s) * 32 + (e & 31)] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+        }
+        __syncthreads();
+        uint32_t f[KT][3][4];
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int s = 0; s < 3; ++s) {
+                const uint4 u = frag[(k * 3 + s) * 32 + lane];
+                f[k][s][0] = u.x; f[k][s][1] = u.y; f[k][s][2] = u.z; f[k][s][3] = u.w;
+            }
+        for (; n0 < n_end; n0 += kStep) {
+            float4 o[2] = {nbase[0], nbase[1]}, v[2];
+            uint2 bw[2][KT];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < KT; ++k) bw[j][k] = nb[j][k];
+            if (n0 + kStep < n_end) prefetch(n0 + kStep);
+            lora_clear_b<KT>(own.rank, t, bw);
+            lora_mul<KT>(f, bw, v[0], v[1]);
+            const int n = n0 + 4 * t;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                lora_acc(o[h], v[h]);
+                if (at[h] >= 0) lora_store4<VEC>(y + at[h] + n, a.N - n, o[h]);
+            }
+        }
+    }
+}
+
+// Many rows: grid (blocks of 16 RB rows, column ranges, projections):
+// neighbours share B.
+template <int KT, int RB, bool VEC>
+__global__ void __launch_bounds__(kLoraThreads, KT <= 4 ? 2 : 1) k_lora_expand(const LoraArgs a)
+{
+    constexpr int LD = KT * 16 + 4;  // floats per row of t in shared memory
+    __shared__ __align__(16) float ts[RB * 16 * LD];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    pdl_launch_dependents();
+    const int target = blockIdx.z;
+    const int64_t m0 = (int64_t)blockIdx.x * (16 * RB);
+    const int id = lora_id(a, lane < 16 * RB ? m0 + lane : a.M);
+    const int my_rank = lora_rank(a, id);
+    const unsigned distinct = lora_distinct(id, lane);
+    const float *base = a.base[target];
+    float *y = a.y[target];
     const int n_end = min(a.N, (int)(blockIdx.y + 1) * a.cols);
-    for (int n0 = blockIdx.y * a.cols + warp * 16; n0 < n_end; n0 += kLoraWarps * 16) {
-        // column q of block j is n0 + 4 (q / 2) + 2 j + q % 2, so that a thread
-        // holds four consecutive columns, n0 + 4 t .., of its two rows
+    constexpr int kStep = kLoraWarps * 16;
+    auto load_base = [&](int n0, float4 (&o)[RB][2]) {
         const int n = n0 + 4 * t;
-        float4 o_lo = make_float4(0.f, 0.f, 0.f, 0.f), o_hi = o_lo;
-        if (VEC) {
-            if (n < a.N) {
-                if (r_lo < a.M) o_lo = *reinterpret_cast<const float4 *>(base + r_lo * a.N + n);
-                if (r_hi < a.M) o_hi = *reinterpret_cast<const float4 *>(base + r_hi * a.N + n);
-            }
-        } else {
-            float *pl = &o_lo.x, *ph = &o_hi.x;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < a.N) {
-                    if (r_lo < a.M) pl[i] = base[r_lo * a.N + n + i];
-                    if (r_hi < a.M) ph[i] = base[r_hi * a.N + n + i];
-                }
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t r = m0 + b * 16 + h * 8 + g;
+                o[b][h] = lora_load4<VEC>(base + min(r, (int64_t)a.M - 1) * a.N + n, r < a.M ? a.N - n : 0);
+            }
+    };
+    int n0 = blockIdx.y * a.cols + warp * 16;
+    float4 nbase[RB][2];
+    uint2 nb[2][KT];
+    int src = (__ffs(distinct) - 1) & 31;
+    int ni = __shfl_sync(0xffffffffu, id, src), nrank = __shfl_sync(0xffffffffu, my_rank, src);
+    if (n0 < n_end) {
+        load_base(n0, nbase);
+        if (distinct) lora_load_b<KT>(a, a.b[target], n0, ni, nrank, g, t, nb);
+    }
+    pdl_wait_primary();
+    if (distinct)
+        for (int e = threadIdx.x; e < RB * 16 * KT * 4; e += kLoraThreads) {
+            const int row = e / (KT * 4), r = e % (KT * 4) * 4, i = lora_id(a, m0 + row);
+            *reinterpret_cast<float4 *>(ts + row * LD + r) = lora_t4(a, target, m0 + row, i, lora_rank(a, i), r);
         }
-        for (unsigned todo = distinct; todo; todo &= todo - 1) {
-            const int i = __shfl_sync(0xffffffffu, id, __ffs(todo) - 1);
-            const int rank = lora_rank(a, i);
-            const uint16_t *w = a.b[target] + (int64_t)i * a.N * a.rank + 4 * t;
-            float acc[2][4];
+    __syncthreads();
+    uint32_t f[RB][KT][3][4];
+    int row_id[RB][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+    for (int b = 0; b < RB; ++b)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) acc[j][c] = 0.f;
-                const int col = n0 + 4 * (g >> 1) + 2 * j + (g & 1);
-                uint2 bw[KT];
+        for (int h = 0; h < 2; ++h) {
+            row_id[b][h] = __shfl_sync(0xffffffffu, id, b * 16 + h * 8 + g);
 #pragma unroll
-                for (int k = 0; k < KT; ++k) {
-                    // entries from the adapter's rank on are cleared: they may hold anything
-                    const int left = rank - (k * 16 + 4 * t);
-                    bw[k] = make_uint2(0u, 0u);
-                    if (left > 0 && col < a.N)
-                        bw[k] = __ldg(reinterpret_cast<const uint2 *>(w + (int64_t)col * a.rank + k * 16));
-                    if (left < 4) {
-                        if (left < 2) bw[k].y = 0; else if (left < 4) bw[k].y &= left < 3 ? 0u : 0xFFFFu;
-                        if (left == 1) bw[k].x &= 0xFFFFu;
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < KT; ++k)
-#pragma unroll
-                    for (int s = 0; s < 3; ++s)
-                        lora_mma(acc[j], f[k][s][0], f[k][s][1], f[k][s][2], f[k][s][3], bw[k].x, bw[k].y);
-            }
-            if (id_lo == i) {
-                o_lo.x += acc[0][0]; o_lo.y += acc[0][1]; o_lo.z += acc[1][0]; o_lo.w += acc[1][1];
-            }
-            if (id_hi == i) {
-                o_hi.x += acc[0][2]; o_hi.y += acc[0][3]; o_hi.z += acc[1][2]; o_hi.w += acc[1][3];
+            for (int k = 0; k < KT; ++k) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (distinct) v = *reinterpret_cast<const float4 *>(ts + (b * 16 + h * 8 + g) * LD + k * 16 + 4 * t);
+                lora_split(v, f[b][k], h);
             }
         }
-        if (VEC) {
-            if (n < a.N) {
-                if (r_lo < a.M) *reinterpret_cast<float4 *>(y + r_lo * a.N + n) = o_lo;
-                if (r_hi < a.M) *reinterpret_cast<float4 *>(y + r_hi * a.N + n) = o_hi;
-            }
-        } else {
-            const float *pl = &o_lo.x, *ph = &o_hi.x;
+    for (; n0 < n_end; n0 += kStep) {
+        float4 o[RB][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (n + i < a.N) {
-                    if (r_lo < a.M) y[r_lo * a.N + n + i] = pl[i];
-                    if (r_hi < a.M) y[r_hi * a.N + n + i] = ph[i];
-                }
+        for (int b = 0; b < RB; ++b) {
+            o[b][0] = nbase[b][0];
+            o[b][1] = nbase[b][1];
         }
+        const bool more = n0 + kStep < n_end;
+        if (more) load_base(n0 + kStep, nbase);
+        for (unsigned todo = distinct; todo;) {
+            const int i = ni, rank = nrank;
+            uint2 bw[2][KT];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < KT; ++k) bw[j][k] = nb[j][k];
+            todo &= todo - 1;
+            src = __ffs(todo ? todo : distinct) - 1;
+            ni = __shfl_sync(0xffffffffu, id, src);
+            nrank = __shfl_sync(0xffffffffu, my_rank, src);
+            if (todo || more) lora_load_b<KT>(a, a.b[target], todo ? n0 : n0 + kStep, ni, nrank, g, t, nb);
+            lora_clear_b<KT>(rank, t, bw);
+#pragma unroll
+            for (int b = 0; b < RB; ++b) {
+                float4 v[2];
+                lora_mul<KT>(f[b], bw, v[0], v[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (row_id[b][h] == i) lora_acc(o[b][h], v[h]);
+            }
+        }
+        const int n = n0 + 4 * t;
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t r = m0 + b * 16 + h * 8 + g;
+                if (r < a.M) lora_store4<VEC>(y + r * a.N + n, a.N - n, o[b][h]);
+            }
     }
 }
 
@@ -268,20 +571,22 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_expand(const LoraArgs a)
 // ---------------------------------------------------------------------------
 
 struct LoraPlan {
-    int slices, kslice, parts;
+    bool few;
+    int rb, slices, kslice;
 };
 
-// Warps of the first launch: enough to fill the GPU (about 16 an SM), first by
-// sharing a block's adapters, then by slices of K, of at least 128 k each.
-static LoraPlan lora_plan(int R, int M, int K)
+// rb: rows per block / 16; 32 rows (each weight loaded for twice the rows) where
+// their fragments leave registers for two CTAs per SM.  Slices of K: about two
+// CTAs per SM in the first launch, of at least 64 k for each warp; a decode
+// batch counts as M / 2 adapters.
+static LoraPlan lora_plan(int R, int M, int K, int rank)
 {
-    const int blocks = (M + 15) / 16;
     LoraPlan p;
-    const int64_t want = 148 * 16;
-    p.parts = (int)std::min<int64_t>(std::min(16, M), std::max<int64_t>(1, want / ((int64_t)blocks * R)));
-    const int64_t s = std::max<int64_t>(1, want / ((int64_t)blocks * R * p.parts));
-    const int most = std::min(kLoraMaxSlices, (K + 127) / 128);
-    p.slices = (int)std::min<int64_t>(s, most);
+    p.few = M <= kLoraFewRows;
+    p.rb = rank <= 32 ? 2 : 1;
+    const int64_t groups = p.few ? (M + 1) / 2 : (M + 16 * p.rb - 1) / (16 * p.rb), want = 2 * 148;
+    const int most = std::max(1, K / (64 * kLoraWarps));
+    p.slices = (int)std::min<int64_t>(std::max<int64_t>(1, want / (groups * R)), std::min(most, kLoraMaxSlices));
     p.kslice = ((K + p.slices - 1) / p.slices + 31) / 32 * 32;
     p.slices = (K + p.kslice - 1) / p.kslice;
     return p;
@@ -289,16 +594,40 @@ static LoraPlan lora_plan(int R, int M, int K)
 
 size_t lora_workspace_bytes(int R, int M, int K, int rank)
 {
-    return align256((size_t)R * lora_plan(R, M, K).slices * M * rank * sizeof(float));
+    return align256((size_t)R * lora_plan(R, M, K, rank).slices * M * rank * sizeof(float));
 }
 
 int lora_max_group() { return kLoraMaxGroup; }
+
+template <typename... KArgs>
+static cudaError_t lora_start(void (*kern)(KArgs...), dim3 grid, int smem, const LoraArgs &g, cudaStream_t st)
+{
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, grid, dim3(kLoraThreads), smem, st, g);
+}
+
+template <int KT>  // rank / 16, rounded up to 1, 2, 4 or 8
+static cudaError_t lora_run(const LoraPlan &p, dim3 gs, dim3 ge, const LoraArgs &g, cudaStream_t st)
+{
+    constexpr int NT = 2 * KT, RB = KT <= 2 ? 2 : 1;
+    cudaError_t e = p.few ? lora_start(k_lora_shrink_few<NT>, gs, LoraShrink<NT, 1>::kBytes, g, st)
+                          : lora_start(k_lora_shrink<NT, RB>, gs, LoraShrink<NT, RB>::kBytes, g, st);
+    if (e != cudaSuccess) return e;
+    if (g.N % 4 == 0)
+        return p.few ? lora_start(k_lora_expand_few<KT, true>, ge, 0, g, st)
+                     : lora_start(k_lora_expand<KT, RB, true>, ge, 0, g, st);
+    return p.few ? lora_start(k_lora_expand_few<KT, false>, ge, 0, g, st)
+                 : lora_start(k_lora_expand<KT, RB, false>, ge, 0, g, st);
+}
 
 lowbit_status lora_launch(const uint16_t *x, const int32_t *ids, const uint16_t *const *a, const uint16_t *const *b,
                           const int32_t *ranks, const float *scales, const float *const *base, float *const *y, int R,
                           int M, int N, int K, int rank, int L, void *workspace, cudaStream_t st)
 {
-    const LoraPlan p = lora_plan(R, M, K);
+    const LoraPlan p = lora_plan(R, M, K, rank);
     LoraArgs g = {};
     g.x = x; g.ids = ids; g.ranks = ranks; g.scales = scales;
     for (int r = 0; r < R; ++r) {
@@ -306,26 +635,18 @@ lowbit_status lora_launch(const uint16_t *x, const int32_t *ids, const uint16_t 
     }
     g.t = static_cast<float *>(workspace);
     g.M = M; g.N = N; g.K = K; g.rank = rank; g.L = L;
-    g.slices = p.slices; g.kslice = p.kslice; g.parts = p.parts;
-    const int64_t blocks = (M + 15) / 16;
-    const int64_t tasks = blocks * p.slices * p.parts;
-    void (*shrink)(const LoraArgs) = rank <= 16 ? k_lora_shrink<2> : rank <= 32 ? k_lora_shrink<4>
-                                     : rank <= 64 ? k_lora_shrink<8> : k_lora_shrink<16>;
-    cudaError_t e = launch_pdl(shrink, dim3((unsigned)((tasks + kLoraWarps - 1) / kLoraWarps), R), dim3(kLoraThreads),
-                               0, st, g);
-    if (e != cudaSuccess) return LOWBIT_ERR_CUDA;
-    // columns per CTA: whole rounds of the CTA's warps, as many as leave about
-    // four CTAs per SM
+    g.slices = p.slices; g.kslice = p.kslice;
+    const int64_t groups = p.few ? M : ((int64_t)M + 16 * p.rb - 1) / (16 * p.rb);
+    // columns per CTA of the second launch: whole rounds of the CTA's warps, as
+    // many as leave about four CTAs per SM
     const int round = kLoraWarps * 16;
-    const int64_t ranges = std::max<int64_t>(1, 4 * 148 / (blocks * R));
+    const int64_t ranges = std::max<int64_t>(1, 4 * 148 / ((p.few ? (groups + 1) / 2 : groups) * R));
     g.cols = (int)((((int64_t)N + ranges - 1) / ranges + round - 1) / round * round);
-    const bool vec = N % 4 == 0;
-    void (*expand)(const LoraArgs) =
-        rank <= 16   ? (vec ? k_lora_expand<1, true> : k_lora_expand<1, false>)
-        : rank <= 32 ? (vec ? k_lora_expand<2, true> : k_lora_expand<2, false>)
-        : rank <= 64 ? (vec ? k_lora_expand<4, true> : k_lora_expand<4, false>)
-                     : (vec ? k_lora_expand<8, true> : k_lora_expand<8, false>);
-    e = launch_pdl(expand, dim3((unsigned)blocks, (unsigned)((N + g.cols - 1) / g.cols), R), dim3(kLoraThreads), 0, st, g);
+    const dim3 gs((unsigned)(groups * p.slices), R), ge((unsigned)groups, (unsigned)((N + g.cols - 1) / g.cols), R);
+    const cudaError_t e = rank <= 16   ? lora_run<1>(p, gs, ge, g, st)
+                          : rank <= 32 ? lora_run<2>(p, gs, ge, g, st)
+                          : rank <= 64 ? lora_run<4>(p, gs, ge, g, st)
+                                       : lora_run<8>(p, gs, ge, g, st);
     return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 

@@ -330,42 +330,64 @@ def lowbit_q1g128_stack_step(w_bits, w_scales, x, hidden, ffn, workspace, eps=1e
 # -- low-rank adapters of many requests ---------------------------------------------
 #
 # The operands of these and of the following calls are checked here as far as the C
-# side cannot see them: element types, shapes, strides and the device.
+# side cannot see them: element types, shapes, strides and the device.  A decode step
+# makes many such calls in a row, so the checks are kept to what a tensor answers
+# without building objects, and plain integers go to ctypes.
 
 LOWBIT_F32 = 0
 LOWBIT_BF16 = 1
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
+_types = {}  # torch dtypes of the operands that may be either -> lowbit_dtype
 
 
-def _dtypes():
+def _device() -> int:
+    """The current CUDA device; every operand has to be there."""
     import torch
-    return {torch.float32: LOWBIT_F32, torch.bfloat16: LOWBIT_BF16}
+    if not _types:
+        _types.update({torch.float32: LOWBIT_F32, torch.bfloat16: LOWBIT_BF16})
+    return torch.cuda.current_device()
 
 
-def _dense(t, dtype, shape, what):
-    """t is a dense CUDA tensor of this type and shape on the current device."""
+def _raw_stream(stream, dev):
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse(t, what, expected):
+    raise ValueError(f"{what}: expected {expected}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _dense(t, dtype, shape, what, dev):
+    """The address of t: a dense tensor of this type and shape on device dev."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, what, f"a contiguous {dtype} tensor of shape {shape} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _bits16(t, shape, what, dev):
+    """The same for bf16 values, as such or as int16 bit patterns."""
     import torch
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: on {t.device}; expected the current CUDA device")
+    return _dense(t, torch.int16 if t.dtype is torch.int16 else torch.bfloat16, shape, what, dev)
 
 
-def _rows(t, rows, heads, dim, what):
-    """Row stride of a [rows][heads][dim] tensor whose rows are dense (rows may lie apart)."""
-    import torch
-    if tuple(t.shape) != (rows, heads, dim) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"{what}: expected shape {(rows, heads, dim)} with dense rows, got {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what}: on {t.device}; expected the current CUDA device")
-    return t.stride(0) if rows > 1 else heads * dim
+def _rows(t, dtype, shape, what, dev):
+    """Address and row stride of a [rows][heads][dim] tensor whose rows are dense and may lie apart."""
+    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dtype is not dtype or t.shape != shape or s2 != 1 or (s1 != shape[2] and shape[1] > 1) or t.get_device() != dev:
+        _refuse(t, what, f"a {dtype} tensor of shape {shape} with dense rows on cuda:{dev}")
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _bits16(t):
-    import torch
-    return torch.bfloat16 if t.dtype is torch.bfloat16 else torch.int16
+def _either(t, what):
+    if t.dtype not in _types:
+        _refuse(t, what, "float32 or bfloat16")
+    return _types[t.dtype]
+
+
+def _ptrs(values):
+    return (ctypes.c_void_p * len(values))(*values)
 
 
 def lowbit_lora_workspace_bytes(R: int, M: int, N: int, K: int, rank: int) -> int:
@@ -379,30 +401,22 @@ def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, works
     fp32 [M][N] and fp32 [M][N] (base_r may be y_r itself); ranks int32 [L] and scales fp32 [L], or None.
     workspace: lowbit_lora_workspace_bytes(R, M, N, K, rank) bytes."""
     import torch
+    dev, f32 = _device(), torch.float32
     R = len(a)
     if not 1 <= R == len(b) == len(base) == len(ys):
         raise ValueError("lowbit_lora_add_group: lists of different lengths")
     M, K = x.shape
     L, rank, _ = a[0].shape
     N = b[0].shape[1]
-    _dense(x, _bits16(x), (M, K), "x")
-    _dense(ids, torch.int32, (M,), "ids")
-    for r in range(R):
-        _dense(a[r], _bits16(a[r]), (L, rank, K), "a")
-        _dense(b[r], _bits16(b[r]), (L, N, rank), "b")
-        _dense(base[r], torch.float32, (M, N), "base")
-        _dense(ys[r], torch.float32, (M, N), "y")
-    if ranks is not None:
-        _dense(ranks, torch.int32, (L,), "ranks")
-    if scales is not None:
-        _dense(scales, torch.float32, (L,), "scales")
-    pa, ka = _ptr_array(a)
-    pb, kb = _ptr_array(b)
-    pc, kc = _ptr_array(base)
-    py, ky = _ptr_array(ys)
-    _check(lib().lowbit_lora_add_group(_ptr(x), _ptr(ids), pa, pb, _ptr(ranks), _ptr(scales), pc, py, R, M, N, K, rank,
-                                       L, _ptr(workspace), _nbytes(workspace), _stream(stream)),
-           "lowbit_lora_add_group")
+    sa, sb, sy, sl = (L, rank, K), (L, N, rank), (M, N), (L,)
+    _check(lib().lowbit_lora_add_group(
+        _bits16(x, (M, K), "x", dev), _dense(ids, torch.int32, (M,), "ids", dev),
+        _ptrs([_bits16(t, sa, "a", dev) for t in a]), _ptrs([_bits16(t, sb, "b", dev) for t in b]),
+        None if ranks is None else _dense(ranks, torch.int32, sl, "ranks", dev),
+        None if scales is None else _dense(scales, f32, sl, "scales", dev),
+        _ptrs([_dense(t, f32, sy, "base", dev) for t in base]), _ptrs([_dense(t, f32, sy, "y", dev) for t in ys]),
+        R, M, N, K, rank, L, None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
+        _raw_stream(stream, dev)), "lowbit_lora_add_group")
 
 
 def lowbit_lora_add(x, ids, a, b, base, y, ranks=None, scales=None, workspace=None, stream=None):
@@ -426,23 +440,25 @@ def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnit
     """q [M][q_heads][D] -> q_out and k [M][kv_heads][D] -> k_out (either pair may be None), fp32 or bf16, rows dense
     and any stride (a multiple of 8) apart; positions int32 [M]; phases int64 [rot / 2].  In place where types match."""
     import torch
+    dev = _device()
     ref, ref_out = (q, q_out) if q is not None else (k, k_out)
     M, _, D = ref.shape
-    types = _dtypes()
     half = phases.shape[0]
-    _dense(positions, torch.int32, (M,), "positions")
-    _dense(phases, torch.int64, (half,), "phases")
-    args = []
-    for name, i, o in (("q", q, q_out), ("k", k, k_out)):
-        if i is None:
-            args += [None, 0, None, 0, 0]
-            continue
-        if i.dtype is not ref.dtype or o.dtype is not ref_out.dtype:
-            raise ValueError("lowbit_rope: q and k have one input and one output type")
-        heads = i.shape[1]
-        args += [_ptr(i), _rows(i, M, heads, D, name), _ptr(o), _rows(o, M, heads, D, name + "_out"), heads]
-    _check(lib().lowbit_rope(*args, types[ref.dtype], types[ref_out.dtype], _ptr(positions), _ptr(phases), M, D,
-                             2 * half, 1 if interleaved else 0, float(magnitude), _stream(stream)), "lowbit_rope")
+    ti, to = _either(ref, "input"), _either(ref_out, "output")
+    qp = qo = kp = ko = None
+    qs = qos = qh = ks = kos = kh = 0
+    if q is not None:
+        qh = q.shape[1]
+        qp, qs = _rows(q, ref.dtype, (M, qh, D), "q", dev)
+        qo, qos = _rows(q_out, ref_out.dtype, (M, qh, D), "q_out", dev)
+    if k is not None:
+        kh = k.shape[1]
+        kp, ks = _rows(k, ref.dtype, (M, kh, D), "k", dev)
+        ko, kos = _rows(k_out, ref_out.dtype, (M, kh, D), "k_out", dev)
+    _check(lib().lowbit_rope(qp, qs, qo, qos, qh, kp, ks, ko, kos, kh, ti, to,
+                             _dense(positions, torch.int32, (M,), "positions", dev),
+                             _dense(phases, torch.int64, (half,), "phases", dev), M, D, 2 * half,
+                             1 if interleaved else 0, magnitude, _raw_stream(stream, dev)), "lowbit_rope")
 
 
 # -- KV8 cache ----------------------------------------------------------------------
@@ -463,64 +479,67 @@ class KV8Cache:
 
     def __init__(self, k, k_scales, v, v_scales):
         import torch
+        dev = _device()
         n_pages, heads, page, dim = k.shape
-        for name, t, dtype, shape in (("k", k, torch.int8, (n_pages, heads, page, dim)), ("v", v, torch.int8, k.shape),
-                                      ("k_scales", k_scales, torch.float32, (n_pages, heads)),
-                                      ("v_scales", v_scales, torch.float32, (n_pages, heads))):
-            _dense(t, dtype, shape, name)
-        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
-        self.n_heads, self.page_tokens, self.head_dim, self.device = heads, page, dim, k.device
-        self._c = _KV8CacheC(k.data_ptr(), k_scales.data_ptr(), v.data_ptr(), v_scales.data_ptr(), n_pages, heads,
-                             page, dim)
+        self._c = _KV8CacheC(_dense(k, torch.int8, (n_pages, heads, page, dim), "k", dev),
+                             _dense(k_scales, torch.float32, (n_pages, heads), "k_scales", dev),
+                             _dense(v, torch.int8, (n_pages, heads, page, dim), "v", dev),
+                             _dense(v_scales, torch.float32, (n_pages, heads), "v_scales", dev), n_pages, heads, page,
+                             dim)
         self._ref = ctypes.byref(self._c)
+        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+        self.n_pages, self.n_heads, self.page_tokens, self.head_dim, self.device = n_pages, heads, page, dim, dev
 
     @classmethod
     def empty(cls, n_pages: int, n_heads: int, page_tokens: int, head_dim: int, device="cuda"):
         """A cache of zeros."""
         import torch
         shape = (n_pages, n_heads, page_tokens, head_dim)
-        return cls(*(f(s, dtype=d, device=device) for f, s, d in ((torch.zeros, shape, torch.int8),
-                   (torch.zeros, shape[:2], torch.float32), (torch.zeros, shape, torch.int8),
-                   (torch.zeros, shape[:2], torch.float32))))
+
+        def zeros(s, dtype):
+            return torch.zeros(s, dtype=dtype, device=device)
+
+        return cls(zeros(shape, torch.int8), zeros(shape[:2], torch.float32), zeros(shape, torch.int8),
+                   zeros(shape[:2], torch.float32))
 
 
-def _kv8_batch(cache, page_table, kv_len, row_start, rows):
+def _kv8_batch(cache, page_table, kv_len, row_start, rows, dev):
     import torch
+    i32 = torch.int32
     B, width = page_table.shape
-    _dense(page_table, torch.int32, (B, width), "page_table")
-    _dense(kv_len, torch.int32, (B,), "kv_len")
-    if cache.device != page_table.device:
-        raise ValueError(f"page_table: on {page_table.device}, the cache on {cache.device}")
-    if row_start is not None:
-        _dense(row_start, torch.int32, (B + 1,), "row_start")
-    return _KV8BatchC(kv_len.data_ptr(), page_table.data_ptr(), None if row_start is None else row_start.data_ptr(), B,
-                      width, rows)
+    if cache.device != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
+    return _KV8BatchC(_dense(kv_len, i32, (B,), "kv_len", dev), _dense(page_table, i32, (B, width), "page_table", dev),
+                      None if row_start is None else _dense(row_start, i32, (B + 1,), "row_start", dev), B, width, rows)
 
 
 def lowbit_kv8_append(cache: KV8Cache, page_table, kv_len, k, v, row_start=None, stream=None):
     """Write k, v [rows][n_heads][head_dim] (fp32 or bf16 each, rows dense and any stride apart) as the sequences' last
     tokens.  page_table int32 [B][max_pages], kv_len int32 [B] (the new tokens included), row_start int32 [B + 1], or
     None for one row per sequence."""
+    dev = _device()
     rows = k.shape[0]
-    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows)
-    types = _dtypes()
-    ks = _rows(k, rows, cache.n_heads, cache.head_dim, "k")
-    vs = _rows(v, rows, cache.n_heads, cache.head_dim, "v")
-    _check(lib().lowbit_kv8_append(cache._ref, ctypes.byref(batch), _ptr(k), ks, types[k.dtype], _ptr(v), vs,
-                                   types[v.dtype], _stream(stream)), "lowbit_kv8_append")
+    shape = (rows, cache.n_heads, cache.head_dim)
+    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
+    tk, tv = _either(k, "k"), _either(v, "v")
+    kp, ks = _rows(k, k.dtype, shape, "k", dev)
+    vp, vs = _rows(v, v.dtype, shape, "v", dev)
+    _check(lib().lowbit_kv8_append(cache._ref, ctypes.byref(batch), kp, ks, tk, vp, vs, tv, _raw_stream(stream, dev)),
+           "lowbit_kv8_append")
 
 
 def lowbit_kv8_read(cache: KV8Cache, page_table, kv_len, k_out, v_out, row_start=None, stream=None):
     """The values of the sequences' last tokens back from the cache: k_out, v_out [rows][n_heads][head_dim] (dense, one
     type, fp32 or bf16; either may be None)."""
+    dev = _device()
     ref = k_out if k_out is not None else v_out
     rows = ref.shape[0]
-    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None:
-            _dense(t, ref.dtype, (rows, cache.n_heads, cache.head_dim), name)
-    _check(lib().lowbit_kv8_read(cache._ref, ctypes.byref(batch), _ptr(k_out), _ptr(v_out), _dtypes()[ref.dtype],
-                                 _stream(stream)), "lowbit_kv8_read")
+    shape = (rows, cache.n_heads, cache.head_dim)
+    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
+    _check(lib().lowbit_kv8_read(cache._ref, ctypes.byref(batch),
+                                 None if k_out is None else _dense(k_out, ref.dtype, shape, "k_out", dev),
+                                 None if v_out is None else _dense(v_out, ref.dtype, shape, "v_out", dev),
+                                 _either(ref, "output"), _raw_stream(stream, dev)), "lowbit_kv8_read")
 
 
 def lowbit_kv8_attention_workspace_bytes(cache: KV8Cache, n_seqs: int, n_rows: int, q_heads: int) -> int:
@@ -537,10 +556,12 @@ def lowbit_kv8_attention(cache: KV8Cache, page_table, kv_len, q, out, scale, row
     row_start as for lowbit_kv8_append.  workspace: lowbit_kv8_attention_workspace_bytes(...) bytes, zero-filled before
     their first use."""
     import torch
-    rows, heads, dim = q.shape
-    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows)
-    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16:
-        raise ValueError(f"lowbit_kv8_attention: q and out are bfloat16, got {q.dtype} and {out.dtype}")
-    qs, os_ = _rows(q, rows, heads, cache.head_dim, "q"), _rows(out, rows, heads, cache.head_dim, "out")
-    _check(lib().lowbit_kv8_attention(cache._ref, ctypes.byref(batch), _ptr(q), qs, heads, float(scale), _ptr(out), os_,
-                                      _ptr(workspace), _nbytes(workspace), _stream(stream)), "lowbit_kv8_attention")
+    dev = _device()
+    rows, heads, _ = q.shape
+    shape = (rows, heads, cache.head_dim)
+    batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
+    qp, qs = _rows(q, torch.bfloat16, shape, "q", dev)
+    op, os_ = _rows(out, torch.bfloat16, shape, "out", dev)
+    _check(lib().lowbit_kv8_attention(cache._ref, ctypes.byref(batch), qp, qs, heads, scale, op, os_,
+                                      None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
+                                      _raw_stream(stream, dev)), "lowbit_kv8_attention")
