@@ -10,10 +10,10 @@
 // The second launch adds s_i B_i t to base: t is summed over the slices in
 // order, scaled and split into three bf16 numbers, which carry its 24 bits (two
 // would leave an error of 2^-18 of t beside fp32 outputs); a warp holds the
-// split of its rows in registers and walks over columns, 16 at a time, with B's
-// loads as fragments again and the next step's loads under way.  All it needs
-// but t was there before the first launch began, so it loads ids, base and the
-// first of B before it waits for t.  Only rows of the adapter at hand are stored,
+// split of its rows in registers and walks over columns, 16 at a time, with base
+// and B copied some steps ahead into a ring of its own (cp.async).  All it needs
+// but t was there before the first launch began, so those copies start before
+// it waits for t.  Only rows of the adapter at hand are stored,
 // so what another adapter holds (infinities among it) cannot reach them.
 //
 // Which rows a CTA takes: up to kLoraFewRows rows (decode), all rows of one
@@ -260,19 +260,68 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink(const LoraArgs a)
     }
 }
 
-// Four columns of a row of base or y; VEC: rows are 16-byte aligned.
-template <bool VEC>
+__device__ __forceinline__ void lora_cp16(unsigned dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A warp's ring: per stage 16 columns of base for 16 RB rows, then of B.  B's
+// column c lies in row (c / 2 % 2) * 8 + c / 4 * 2 + c % 2, which is tile j = c / 2 % 2,
+// fragment column g, so that a thread's results are four consecutive columns of
+// its rows; rows 32 or 96 bytes apart mod 128 keep the fragment loads (8 bytes a
+// lane, four rows a phase) free of bank conflicts.
+template <int KT, int RB>
+struct LoraRing {
+    static constexpr int kPitch = KT == 1 ? 32 : KT == 2 ? 96 : KT * 32 + 32;
+    static constexpr int kBase = RB * 16 * 64;
+    static constexpr int kStage = kBase + 16 * kPitch;
+    static constexpr int kStages = KT >= 4 || RB == 2 ? 3 : 4;
+    static constexpr int kBytes = kLoraWarps * kStages * kStage;
+    static constexpr int kCtas = KT == 1 && RB == 1 ? 4 : KT <= 4 ? 2 : 1;  // per SM, by registers and ring
+    static_assert(kBytes * kCtas <= 220 * 1024, "rings of an SM's CTAs");
+};
+
+template <int KT, int RB>
+__device__ __forceinline__ void lora_copy_b(const LoraArgs &a, unsigned dst, const uint16_t *b, int n0, int i, int rank,
+                                            int lane)
+{
+    const int per = a.rank / 8;
+    const uint16_t *src = b + ((int64_t)i * a.N + n0) * a.rank;
+    for (int e = lane; e < 16 * per; e += 32) {
+        const int c = e / per, ch = e % per;
+        if (n0 + c < a.N && ch * 8 < rank)
+            lora_cp16(dst + ((c >> 1 & 1) * 8 + (c >> 2) * 2 + (c & 1)) * LoraRing<KT, RB>::kPitch + ch * 16, src + e * 8);
+    }
+}
+
+// B's fragments of a stage.  The entries from the adapter's rank on are cleared:
+// they may hold anything.
+template <int KT, int RB>
+__device__ __forceinline__ void lora_read_b(unsigned src, int rank, int g, int t, uint2 (&bw)[2][KT])
+{
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+        const int left = rank - (k * 16 + 4 * t);
+        const uint32_t mx = left <= 0 ? 0u : left == 1 ? 0xFFFFu : ~0u, my = left < 3 ? 0u : left == 3 ? 0xFFFFu : ~0u;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                         : "=r"(bw[j][k].x), "=r"(bw[j][k].y)
+                         : "r"(src + (j * 8 + g) * LoraRing<KT, RB>::kPitch + k * 32 + t * 8));
+            bw[j][k].x &= mx;
+            bw[j][k].y &= my;
+        }
+    }
+}
+
+// Four columns of a row of base or y where rows are not 16-byte aligned.
 __device__ __forceinline__ float4 lora_load4(const float *p, int left)
 {
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (VEC) {
-        if (left > 0) v = __ldcg(reinterpret_cast<const float4 *>(p));
-    } else {
-        if (left > 0) v.x = __ldcg(p);
-        if (left > 1) v.y = __ldcg(p + 1);
-        if (left > 2) v.z = __ldcg(p + 2);
-        if (left > 3) v.w = __ldcg(p + 3);
-    }
+    if (left > 0) v.x = __ldcg(p);
+    if (left > 1) v.y = __ldcg(p + 1);
+    if (left > 2) v.z = __ldcg(p + 2);
+    if (left > 3) v.w = __ldcg(p + 3);
     return v;
 }
 template <bool VEC>
@@ -285,41 +334,6 @@ __device__ __forceinline__ void lora_store4(float *p, int left, const float4 &v)
         if (left > 1) p[1] = v.y;
         if (left > 2) p[2] = v.z;
         if (left > 3) p[3] = v.w;
-    }
-}
-
-// B's fragments for 16 columns from n0: column q of tile j is n0 + 4 (q / 2) +
-// 2 j + q % 2, so that a thread's results are four consecutive columns, n0 +
-// 4 t .., of its rows.
-template <int KT>
-__device__ __forceinline__ void lora_load_b(const LoraArgs &a, const uint16_t *wb, int n0, int i, int rank, int g, int t,
-                                            uint2 (&bw)[2][KT])
-{
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int col = n0 + 4 * (g >> 1) + 2 * j + (g & 1);
-        const uint16_t *w = wb + ((int64_t)i * a.N + min(col, a.N - 1)) * a.rank + 4 * t;
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-            bw[j][k] = k * 16 + 4 * t < rank ? __ldcg(reinterpret_cast<const uint2 *>(w + k * 16)) : make_uint2(0u, 0u);
-    }
-}
-
-// Clears the entries from the rank on, which may hold anything (whole groups of
-// four were not loaded).
-template <int KT>
-__device__ __forceinline__ void lora_clear_b(int rank, int t, uint2 (&bw)[2][KT])
-{
-    if ((rank & 3) == 0) return;
-#pragma unroll
-    for (int k = 0; k < KT; ++k) {
-        const int left = rank - (k * 16 + 4 * t);
-        const uint32_t mx = left == 1 ? 0xFFFFu : ~0u, my = left < 3 ? 0u : left == 3 ? 0xFFFFu : ~0u;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            bw[j][k].x &= mx;
-            bw[j][k].y &= my;
-        }
     }
 }
 
@@ -384,17 +398,21 @@ __device__ __forceinline__ void lora_acc(float4 &o, const float4 &v)
 
 // Few rows: grid (rows, column ranges, projections); the CTA of an adapter's
 // first row takes all its rows, 16 at a time; a row without an adapter is copied.
-// KT: rank / 16, rounded up to 1, 2, 4 or 8.
+// KT: rank / 16, rounded up to 1, 2, 4 or 8; VEC: rows of y are 16-byte aligned.
 template <int KT, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads, KT <= 4 ? 2 : 1) k_lora_expand_few(const LoraArgs a)
+__global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_expand_few(const LoraArgs a)
 {
+    using S = LoraRing<KT, 1>;
+    extern __shared__ __align__(128) uint8_t ring_mem[];
     __shared__ int rows[kLoraFewRows], warp_n[kLoraWarps];
     __shared__ uint4 frag[KT * 3 * 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const unsigned ring = (unsigned)__cvta_generic_to_shared(ring_mem) + warp * S::kStages * S::kStage;
     pdl_launch_dependents();
     const int target = blockIdx.z;
     const LoraRows own = lora_gather(a, blockIdx.x, rows, warp_n);
     const float *base = a.base[target];
+    const uint16_t *b = a.b[target];
     float *y = a.y[target];
     const int c0 = blockIdx.y * a.cols, n_end = min(a.N, c0 + a.cols);
     if (own.n == 0) {
@@ -409,17 +427,24 @@ __global__ void __launch_bounds__(kLoraThreads, KT <= 4 ? 2 : 1) k_lora_expand_f
         int64_t at[2];  // offsets of this thread's rows, -1 for none
 #pragma unroll
         for (int h = 0; h < 2; ++h) at[h] = r0 + h * 8 + g < own.n ? (int64_t)rows[r0 + h * 8 + g] * a.N : -1;
-        int n0 = c0 + warp * 16;
-        float4 nbase[2];
-        uint2 nb[2][KT];
-        auto prefetch = [&](int n0) {
-            lora_load_b<KT>(a, a.b[target], n0, own.id, own.rank, g, t, nb);
-            const int n = n0 + 4 * t;
+        int n0 = c0 + warp * 16, ahead = n0, put = 0, get = 0;
+        auto issue = [&]() {
+            if (ahead < n_end) {
+                const unsigned st = ring + put * S::kStage;
+                if (VEC)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                nbase[h] = lora_load4<VEC>(base + (at[h] < 0 ? 0 : at[h]) + n, at[h] < 0 ? 0 : a.N - n);
+                    for (int h = 0; h < 2; ++h) {  // row h * 8 + g, columns 4 t ..
+                        if (at[h] >= 0 && ahead + 4 * t < a.N)
+                            lora_cp16(st + (h * 8 + g) * 64 + t * 16, base + at[h] + ahead + 4 * t);
+                    }
+                lora_copy_b<KT, 1>(a, st + S::kBase, b, ahead, own.id, own.rank, lane);
+                ahead += kStep;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            put = put + 1 == S::kStages ? 0 : put + 1;
         };
-        if (n0 < n_end) prefetch(n0);
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; ++s) issue();
         if (r0 == 0)
             pdl_wait_primary();
         else
@@ -447,62 +472,79 @@ __global__ void __launch_bounds__(kLoraThreads, KT <= 4 ? 2 : 1) k_lora_expand_f
                 f[k][s][0] = u.x; f[k][s][1] = u.y; f[k][s][2] = u.z; f[k][s][3] = u.w;
             }
         for (; n0 < n_end; n0 += kStep) {
-            float4 o[2] = {nbase[0], nbase[1]}, v[2];
-            uint2 bw[2][KT];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int k = 0; k < KT; ++k) bw[j][k] = nb[j][k];
-            if (n0 + kStep < n_end) prefetch(n0 + kStep);
-            lora_clear_b<KT>(own.rank, t, bw);
-            lora_mul<KT>(f, bw, v[0], v[1]);
+            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+            __syncwarp();
+            issue();  // into the stage read last
+            const unsigned st = ring + get * S::kStage;
+            get = get + 1 == S::kStages ? 0 : get + 1;
             const int n = n0 + 4 * t;
+            float4 o[2], v[2];
+            uint2 bw[2][KT];
+            lora_read_b<KT, 1>(st + S::kBase, own.rank, g, t, bw);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (VEC)
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(o[h].x), "=f"(o[h].y), "=f"(o[h].z), "=f"(o[h].w)
+                                 : "r"(st + (h * 8 + g) * 64 + t * 16));
+                else
+                    o[h] = lora_load4(base + (at[h] < 0 ? 0 : at[h]) + n, at[h] < 0 ? 0 : a.N - n);
+            }
+            lora_mul<KT>(f, bw, v[0], v[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 lora_acc(o[h], v[h]);
                 if (at[h] >= 0) lora_store4<VEC>(y + at[h] + n, a.N - n, o[h]);
             }
+            __syncwarp();  // every lane has read the stage
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Many rows: grid (blocks of 16 RB rows, column ranges, projections):
-// neighbours share B.
+// neighbours share B.  The ring holds base and the first adapter's B; those of
+// a block's further adapters are few and loaded in place.
 template <int KT, int RB, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads, KT <= 4 ? 2 : 1) k_lora_expand(const LoraArgs a)
+__global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, RB>::kCtas) k_lora_expand(const LoraArgs a)
 {
+    using S = LoraRing<KT, RB>;
     constexpr int LD = KT * 16 + 4;  // floats per row of t in shared memory
+    extern __shared__ __align__(128) uint8_t ring_mem[];
     __shared__ __align__(16) float ts[RB * 16 * LD];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const unsigned ring = (unsigned)__cvta_generic_to_shared(ring_mem) + warp * S::kStages * S::kStage;
     pdl_launch_dependents();
     const int target = blockIdx.z;
     const int64_t m0 = (int64_t)blockIdx.x * (16 * RB);
     const int id = lora_id(a, lane < 16 * RB ? m0 + lane : a.M);
     const int my_rank = lora_rank(a, id);
     const unsigned distinct = lora_distinct(id, lane);
+    const int first = (__ffs(distinct) - 1) & 31;
+    const int id0 = __shfl_sync(0xffffffffu, id, first), rank0 = __shfl_sync(0xffffffffu, my_rank, first);
     const float *base = a.base[target];
+    const uint16_t *b = a.b[target];
     float *y = a.y[target];
     const int n_end = min(a.N, (int)(blockIdx.y + 1) * a.cols);
     constexpr int kStep = kLoraWarps * 16;
-    auto load_base = [&](int n0, float4 (&o)[RB][2]) {
-        const int n = n0 + 4 * t;
+    int n0 = blockIdx.y * a.cols + warp * 16, ahead = n0, put = 0, get = 0;
+    auto issue = [&]() {
+        if (ahead < n_end) {
+            const unsigned st = ring + put * S::kStage;
+            if (VEC && ahead + 4 * t < a.N)
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t r = m0 + b * 16 + h * 8 + g;
-                o[b][h] = lora_load4<VEC>(base + min(r, (int64_t)a.M - 1) * a.N + n, r < a.M ? a.N - n : 0);
-            }
+                for (int q = 0; q < 2 * RB; ++q) {
+                    const int64_t r = m0 + q * 8 + g;
+                    if (r < a.M) lora_cp16(st + (q * 8 + g) * 64 + t * 16, base + r * a.N + ahead + 4 * t);
+                }
+            if (distinct) lora_copy_b<KT, RB>(a, st + S::kBase, b, ahead, id0, rank0, lane);
+            ahead += kStep;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        put = put + 1 == S::kStages ? 0 : put + 1;
     };
-    int n0 = blockIdx.y * a.cols + warp * 16;
-    float4 nbase[RB][2];
-    uint2 nb[2][KT];
-    int src = (__ffs(distinct) - 1) & 31;
-    int ni = __shfl_sync(0xffffffffu, id, src), nrank = __shfl_sync(0xffffffffu, my_rank, src);
-    if (n0 < n_end) {
-        load_base(n0, nbase);
-        if (distinct) lora_load_b<KT>(a, a.b[target], n0, ni, nrank, g, t, nb);
-    }
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) issue();
     pdl_wait_primary();
     if (distinct)
         for (int e = threadIdx.x; e < RB * 16 * KT * 4; e += kLoraThreads) {
@@ -513,57 +555,70 @@ __global__ void __launch_bounds__(kLoraThreads, KT <= 4 ? 2 : 1) k_lora_expand(c
     uint32_t f[RB][KT][3][4];
     int row_id[RB][2];
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+    for (int q = 0; q < RB; ++q)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            row_id[b][h] = __shfl_sync(0xffffffffu, id, b * 16 + h * 8 + g);
+            row_id[q][h] = __shfl_sync(0xffffffffu, id, q * 16 + h * 8 + g);
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (distinct) v = *reinterpret_cast<const float4 *>(ts + (b * 16 + h * 8 + g) * LD + k * 16 + 4 * t);
-                lora_split(v, f[b][k], h);
+                if (distinct) v = *reinterpret_cast<const float4 *>(ts + (q * 16 + h * 8 + g) * LD + k * 16 + 4 * t);
+                lora_split(v, f[q][k], h);
             }
         }
     for (; n0 < n_end; n0 += kStep) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+        __syncwarp();
+        issue();  // into the stage read last
+        const unsigned st = ring + get * S::kStage;
+        get = get + 1 == S::kStages ? 0 : get + 1;
+        const int n = n0 + 4 * t;
         float4 o[RB][2];
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            o[b][0] = nbase[b][0];
-            o[b][1] = nbase[b][1];
-        }
-        const bool more = n0 + kStep < n_end;
-        if (more) load_base(n0 + kStep, nbase);
-        for (unsigned todo = distinct; todo;) {
-            const int i = ni, rank = nrank;
-            uint2 bw[2][KT];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int k = 0; k < KT; ++k) bw[j][k] = nb[j][k];
-            todo &= todo - 1;
-            src = __ffs(todo ? todo : distinct) - 1;
-            ni = __shfl_sync(0xffffffffu, id, src);
-            nrank = __shfl_sync(0xffffffffu, my_rank, src);
-            if (todo || more) lora_load_b<KT>(a, a.b[target], todo ? n0 : n0 + kStep, ni, nrank, g, t, nb);
-            lora_clear_b<KT>(rank, t, bw);
-#pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                float4 v[2];
-                lora_mul<KT>(f[b], bw, v[0], v[1]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (row_id[b][h] == i) lora_acc(o[b][h], v[h]);
-            }
-        }
-        const int n = n0 + 4 * t;
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
+        for (int q = 0; q < RB; ++q)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t r = m0 + b * 16 + h * 8 + g;
-                if (r < a.M) lora_store4<VEC>(y + r * a.N + n, a.N - n, o[b][h]);
+                const int64_t r = m0 + q * 16 + h * 8 + g;
+                if (VEC)
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(o[q][h].x), "=f"(o[q][h].y), "=f"(o[q][h].z), "=f"(o[q][h].w)
+                                 : "r"(st + (q * 16 + h * 8 + g) * 64 + t * 16));
+                else
+                    o[q][h] = lora_load4(base + min(r, (int64_t)a.M - 1) * a.N + n, r < a.M ? a.N - n : 0);
             }
+        int i = id0, rank = rank0;
+        for (unsigned todo = distinct; todo;) {
+            uint2 bw[2][KT];
+            lora_read_b<KT, RB>(st + S::kBase, rank, g, t, bw);
+#pragma unroll
+            for (int q = 0; q < RB; ++q) {
+                float4 v[2];
+                lora_mul<KT>(f[q], bw, v[0], v[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (row_id[q][h] == i) lora_acc(o[q][h], v[h]);
+            }
+            todo &= todo - 1;
+            if (todo) {  // the next adapter's B takes the first one's place in the stage
+                const int src = __ffs(todo) - 1;
+                i = __shfl_sync(0xffffffffu, id, src);
+                rank = __shfl_sync(0xffffffffu, my_rank, src);
+                __syncwarp();
+                lora_copy_b<KT, RB>(a, st + S::kBase, b, n0, i, rank, lane);
+                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < RB; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t r = m0 + q * 16 + h * 8 + g;
+                if (r < a.M) lora_store4<VEC>(y + r * a.N + n, a.N - n, o[q][h]);
+            }
+        __syncwarp();  // every lane has read the stage
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -602,7 +657,7 @@ int lora_max_group() { return kLoraMaxGroup; }
 template <typename... KArgs>
 static cudaError_t lora_start(void (*kern)(KArgs...), dim3 grid, int smem, const LoraArgs &g, cudaStream_t st)
 {
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {  // with the static arrays beside it, beyond the default 48 KB
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
@@ -617,10 +672,10 @@ static cudaError_t lora_run(const LoraPlan &p, dim3 gs, dim3 ge, const LoraArgs 
                           : lora_start(k_lora_shrink<NT, RB>, gs, LoraShrink<NT, RB>::kBytes, g, st);
     if (e != cudaSuccess) return e;
     if (g.N % 4 == 0)
-        return p.few ? lora_start(k_lora_expand_few<KT, true>, ge, 0, g, st)
-                     : lora_start(k_lora_expand<KT, RB, true>, ge, 0, g, st);
-    return p.few ? lora_start(k_lora_expand_few<KT, false>, ge, 0, g, st)
-                 : lora_start(k_lora_expand<KT, RB, false>, ge, 0, g, st);
+        return p.few ? lora_start(k_lora_expand_few<KT, true>, ge, LoraRing<KT, 1>::kBytes, g, st)
+                     : lora_start(k_lora_expand<KT, RB, true>, ge, LoraRing<KT, RB>::kBytes, g, st);
+    return p.few ? lora_start(k_lora_expand_few<KT, false>, ge, LoraRing<KT, 1>::kBytes, g, st)
+                 : lora_start(k_lora_expand<KT, RB, false>, ge, LoraRing<KT, RB>::kBytes, g, st);
 }
 
 lowbit_status lora_launch(const uint16_t *x, const int32_t *ids, const uint16_t *const *a, const uint16_t *const *b,
@@ -637,11 +692,13 @@ lowbit_status lora_launch(const uint16_t *x, const int32_t *ids, const uint16_t 
     g.M = M; g.N = N; g.K = K; g.rank = rank; g.L = L;
     g.slices = p.slices; g.kslice = p.kslice;
     const int64_t groups = p.few ? M : ((int64_t)M + 16 * p.rb - 1) / (16 * p.rb);
-    // columns per CTA of the second launch: whole rounds of the CTA's warps, as
-    // many as leave about four CTAs per SM
-    const int round = kLoraWarps * 16;
-    const int64_t ranges = std::max<int64_t>(1, 4 * 148 / ((p.few ? (groups + 1) / 2 : groups) * R));
-    g.cols = (int)((((int64_t)N + ranges - 1) / ranges + round - 1) / round * round);
+    // Columns per CTA of the second launch, in rounds of the CTA's warps: as few as
+    // fill the SMs at once, at most eight (CTAs with more adapters or a higher rank
+    // take longer; with 43 rounds each, half of the SMs' time was spent waiting for
+    // the last of them).
+    const int64_t rounds = (N + kLoraWarps * 16 - 1) / (kLoraWarps * 16), slots = (rank <= 16 && p.few ? 4 : rank <= 64 ? 2 : 1) * 148;
+    const int64_t each = (rounds * (p.few ? (groups + 1) / 2 : groups) * R + slots - 1) / slots;
+    g.cols = (int)std::min<int64_t>(std::max<int64_t>(each, 1), 8) * kLoraWarps * 16;
     const dim3 gs((unsigned)(groups * p.slices), R), ge((unsigned)groups, (unsigned)((N + g.cols - 1) / g.cols), R);
     const cudaError_t e = rank <= 16   ? lora_run<1>(p, gs, ge, g, st)
                           : rank <= 32 ? lora_run<2>(p, gs, ge, g, st)
