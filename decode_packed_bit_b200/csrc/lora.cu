@@ -281,36 +281,84 @@ struct LoraRing {
     static_assert(kBytes * kCtas <= 220 * 1024, "rings of an SM's CTAs");
 };
 
+// Where this lane's pieces (16 bytes) of 16 columns of B go in a stage; the
+// pieces themselves lie one after the other in memory, lane by lane.  Bit q of
+// the mask: piece q exists and holds entries below the adapter's rank; col: its
+// column.
 template <int KT, int RB>
-__device__ __forceinline__ void lora_copy_b(const LoraArgs &a, unsigned dst, const uint16_t *b, int n0, int i, int rank,
-                                            int lane)
-{
-    const int per = a.rank / 8;
-    const uint16_t *src = b + ((int64_t)i * a.N + n0) * a.rank;
-    for (int e = lane; e < 16 * per; e += 32) {
-        const int c = e / per, ch = e % per;
-        if (n0 + c < a.N && ch * 8 < rank)
-            lora_cp16(dst + ((c >> 1 & 1) * 8 + (c >> 2) * 2 + (c & 1)) * LoraRing<KT, RB>::kPitch + ch * 16, src + e * 8);
+struct LoraPieces {
+    unsigned dst[KT], mask;
+    int col[KT];
+    __device__ __forceinline__ void set(int rank, int pool_rank, int lane)
+    {
+        const int per = pool_rank / 8;
+        mask = 0;
+#pragma unroll
+        for (int q = 0; q < KT; ++q) {
+            const int e = lane + 32 * q, c = e / per, ch = e % per;
+            if (c < 16 && ch * 8 < rank) mask |= 1u << q;
+            col[q] = c;
+            dst[q] = ((c >> 1 & 1) * 8 + (c >> 2) * 2 + (c & 1)) * LoraRing<KT, RB>::kPitch + ch * 16;
+        }
     }
-}
+    // src: this lane's first piece of the 16 columns; left: columns there are
+    __device__ __forceinline__ void copy(unsigned to, const uint16_t *src, int left) const
+    {
+#pragma unroll
+        for (int q = 0; q < KT; ++q)
+            if ((mask >> q & 1) && col[q] < left) lora_cp16(to + dst[q], src + q * 256);
+    }
+};
 
-// B's fragments of a stage.  The entries from the adapter's rank on are cleared:
-// they may hold anything.
+// acc += the block's rows of t (f: three bf16 numbers each) times a stage's 16
+// columns of B.  Steps of 16 entries beyond the adapter's rank are left out (with
+// one or two steps the branch costs more than it saves: 94 against 85 us for
+// 4096 rows of rank 32), and in the step that it ends in the entries from the rank on are cleared: they
+// may hold anything.
 template <int KT, int RB>
-__device__ __forceinline__ void lora_read_b(unsigned src, int rank, int g, int t, uint2 (&bw)[2][KT])
+__device__ __forceinline__ void lora_mul(const uint32_t (&f)[RB][KT][3][4], unsigned src, int rank, int g, int t,
+                                         float (&acc)[RB][2][4])
 {
+#pragma unroll
+    for (int q = 0; q < RB; ++q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[q][j][c] = 0.f;
+    const unsigned at = src + g * LoraRing<KT, RB>::kPitch + t * 8;
+    uint2 bw[KT][2];
+    auto load = [&](int k) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                         : "=r"(bw[k][j].x), "=r"(bw[k][j].y)
+                         : "r"(at + j * 8 * LoraRing<KT, RB>::kPitch + k * 32));
+    };
+    if (KT <= 2)
+#pragma unroll
+        for (int k = 0; k < KT; ++k) load(k);
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
-        const int left = rank - (k * 16 + 4 * t);
-        const uint32_t mx = left <= 0 ? 0u : left == 1 ? 0xFFFFu : ~0u, my = left < 3 ? 0u : left == 3 ? 0xFFFFu : ~0u;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                         : "=r"(bw[j][k].x), "=r"(bw[j][k].y)
-                         : "r"(src + (j * 8 + g) * LoraRing<KT, RB>::kPitch + k * 32 + t * 8));
-            bw[j][k].x &= mx;
-            bw[j][k].y &= my;
+        if (KT > 2) {
+            if (k * 16 >= rank) break;
+            load(k);
         }
+        if (k * 16 + 16 > rank) {
+            const int left = rank - (k * 16 + 4 * t);
+            const uint32_t mx = left <= 0 ? 0u : left == 1 ? 0xFFFFu : ~0u, my = left < 3 ? 0u : left == 3 ? 0xFFFFu : ~0u;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                bw[k][j].x &= mx;
+                bw[k][j].y &= my;
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int q = 0; q < RB; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    lora_mma(acc[q][j], f[q][k][s][0], f[q][k][s][1], f[q][k][s][2], f[q][k][s][3], bw[k][j].x, bw[k][j].y);
     }
 }
 
@@ -373,27 +421,10 @@ __device__ __forceinline__ void lora_split(const float4 &v, uint32_t (&f)[3][4],
         }
 }
 
-template <int KT>
-__device__ __forceinline__ void lora_mul(const uint32_t (&f)[KT][3][4], const uint2 (&bw)[2][KT], float4 &lo, float4 &hi)
+// A thread's four columns of tiles 0 and 1: rows g (h = 0) and g + 8 (h = 1).
+__device__ __forceinline__ void lora_acc(float4 &o, const float (&acc)[2][4], int h)
 {
-    float acc[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[j][c] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KT; ++k)
-#pragma unroll
-            for (int s = 0; s < 3; ++s)
-                lora_mma(acc[j], f[k][s][0], f[k][s][1], f[k][s][2], f[k][s][3], bw[j][k].x, bw[j][k].y);
-    }
-    lo = make_float4(acc[0][0], acc[0][1], acc[1][0], acc[1][1]);
-    hi = make_float4(acc[0][2], acc[0][3], acc[1][2], acc[1][3]);
-}
-
-__device__ __forceinline__ void lora_acc(float4 &o, const float4 &v)
-{
-    o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+    o.x += acc[0][2 * h]; o.y += acc[0][2 * h + 1]; o.z += acc[1][2 * h]; o.w += acc[1][2 * h + 1];
 }
 
 // Few rows: grid (rows, column ranges, projections); the CTA of an adapter's
@@ -412,7 +443,6 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
     const int target = blockIdx.z;
     const LoraRows own = lora_gather(a, blockIdx.x, rows, warp_n);
     const float *base = a.base[target];
-    const uint16_t *b = a.b[target];
     float *y = a.y[target];
     const int c0 = blockIdx.y * a.cols, n_end = min(a.N, c0 + a.cols);
     if (own.n == 0) {
@@ -423,6 +453,9 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
         return;
     }
     constexpr int kStep = kLoraWarps * 16;
+    LoraPieces<KT, 1> pieces;
+    pieces.set(own.rank, a.rank, lane);
+    const uint16_t *b = a.b[target] + (int64_t)own.id * a.N * a.rank + lane * 8;
     for (int r0 = 0; r0 < own.n; r0 += 16) {
         int64_t at[2];  // offsets of this thread's rows, -1 for none
 #pragma unroll
@@ -437,7 +470,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
                         if (at[h] >= 0 && ahead + 4 * t < a.N)
                             lora_cp16(st + (h * 8 + g) * 64 + t * 16, base + at[h] + ahead + 4 * t);
                     }
-                lora_copy_b<KT, 1>(a, st + S::kBase, b, ahead, own.id, own.rank, lane);
+                pieces.copy(st + S::kBase, b + (int64_t)ahead * a.rank, a.N - ahead);
                 ahead += kStep;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -463,13 +496,13 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
             for (int s = 0; s < 3; ++s) frag[(k * 3 + s) * 32 + (e & 31)] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
         }
         __syncthreads();
-        uint32_t f[KT][3][4];
+        uint32_t f[1][KT][3][4];
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int s = 0; s < 3; ++s) {
                 const uint4 u = frag[(k * 3 + s) * 32 + lane];
-                f[k][s][0] = u.x; f[k][s][1] = u.y; f[k][s][2] = u.z; f[k][s][3] = u.w;
+                f[0][k][s][0] = u.x; f[0][k][s][1] = u.y; f[0][k][s][2] = u.z; f[0][k][s][3] = u.w;
             }
         for (; n0 < n_end; n0 += kStep) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
@@ -478,9 +511,9 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
             const unsigned st = ring + get * S::kStage;
             get = get + 1 == S::kStages ? 0 : get + 1;
             const int n = n0 + 4 * t;
-            float4 o[2], v[2];
-            uint2 bw[2][KT];
-            lora_read_b<KT, 1>(st + S::kBase, own.rank, g, t, bw);
+            float4 o[2];
+            float acc[1][2][4];
+            lora_mul<KT, 1>(f, st + S::kBase, own.rank, g, t, acc);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (VEC)
@@ -490,10 +523,9 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
                 else
                     o[h] = lora_load4(base + (at[h] < 0 ? 0 : at[h]) + n, at[h] < 0 ? 0 : a.N - n);
             }
-            lora_mul<KT>(f, bw, v[0], v[1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                lora_acc(o[h], v[h]);
+                lora_acc(o[h], acc[0], h);
                 if (at[h] >= 0) lora_store4<VEC>(y + at[h] + n, a.N - n, o[h]);
             }
             __syncwarp();  // every lane has read the stage
@@ -523,8 +555,10 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, RB>::kCtas) k_lora_
     const int first = (__ffs(distinct) - 1) & 31;
     const int id0 = __shfl_sync(0xffffffffu, id, first), rank0 = __shfl_sync(0xffffffffu, my_rank, first);
     const float *base = a.base[target];
-    const uint16_t *b = a.b[target];
     float *y = a.y[target];
+    LoraPieces<KT, RB> pieces;
+    pieces.set(rank0, a.rank, lane);
+    const uint16_t *b = a.b[target] + lane * 8, *b0 = b + (int64_t)max(id0, 0) * a.N * a.rank;
     const int n_end = min(a.N, (int)(blockIdx.y + 1) * a.cols);
     constexpr int kStep = kLoraWarps * 16;
     int n0 = blockIdx.y * a.cols + warp * 16, ahead = n0, put = 0, get = 0;
@@ -537,7 +571,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, RB>::kCtas) k_lora_
                     const int64_t r = m0 + q * 8 + g;
                     if (r < a.M) lora_cp16(st + (q * 8 + g) * 64 + t * 16, base + r * a.N + ahead + 4 * t);
                 }
-            if (distinct) lora_copy_b<KT, RB>(a, st + S::kBase, b, ahead, id0, rank0, lane);
+            if (distinct) pieces.copy(st + S::kBase, b0 + (int64_t)ahead * a.rank, a.N - ahead);
             ahead += kStep;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -588,23 +622,22 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, RB>::kCtas) k_lora_
             }
         int i = id0, rank = rank0;
         for (unsigned todo = distinct; todo;) {
-            uint2 bw[2][KT];
-            lora_read_b<KT, RB>(st + S::kBase, rank, g, t, bw);
+            float acc[RB][2][4];
+            lora_mul<KT, RB>(f, st + S::kBase, rank, g, t, acc);
 #pragma unroll
-            for (int q = 0; q < RB; ++q) {
-                float4 v[2];
-                lora_mul<KT>(f[q], bw, v[0], v[1]);
+            for (int q = 0; q < RB; ++q)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (row_id[q][h] == i) lora_acc(o[q][h], v[h]);
-            }
+                    if (row_id[q][h] == i) lora_acc(o[q][h], acc[q], h);
             todo &= todo - 1;
             if (todo) {  // the next adapter's B takes the first one's place in the stage
                 const int src = __ffs(todo) - 1;
                 i = __shfl_sync(0xffffffffu, id, src);
                 rank = __shfl_sync(0xffffffffu, my_rank, src);
                 __syncwarp();
-                lora_copy_b<KT, RB>(a, st + S::kBase, b, n0, i, rank, lane);
+                LoraPieces<KT, RB> its;
+                its.set(rank, a.rank, lane);
+                its.copy(st + S::kBase, b + ((int64_t)i * a.N + n0) * a.rank, a.N - n0);
                 asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
                 __syncwarp();
             }
