@@ -21,8 +21,9 @@
 // tokens come in tiles of 32.  All tiles of all units, in order, are cut into
 // equal ranges, one per CTA (one CTA per SM); lengths are read on the device,
 // so a captured graph follows them.  The warps of a CTA take a range's tiles in
-// turn, each with its own cp.async ring, and join their partial sums through
-// shared memory at the end of a unit; a unit cut between CTAs is joined in
+// turn, each with its own cp.async ring of key and value halves of tiles, which
+// runs on across the ends of units, and join their partial sums through shared
+// memory at the end of a unit; a unit cut between CTAs is joined in
 // CTA order by the last of them to arrive (a counter in the workspace, left
 // zeroed), so the result does not depend on timing.
 #include <algorithm>
@@ -42,7 +43,7 @@ int kv8_attn_fault_flag()
     return (int)v;
 }
 
-constexpr int kAtWarps = 8;
+constexpr int kAtWarps = 12;  // 168 registers a thread; with 8 warps the chains of a tile's steps showed
 constexpr int kAtThreads = kAtWarps * 32;
 constexpr int kAtTile = 32;  // tokens
 constexpr int kAtMaxRT = 2;
@@ -55,6 +56,7 @@ struct Kv8Attn {
     uint16_t *out;
     int64_t q_stride, out_stride;
     int G;            // query heads per cache head
+    int page_log2;
     float scale_log2; // scale * log2(e)
     unsigned *counters;   // [CTAs], zero between calls
     float *part_ml;       // [2 CTAs][rows][2]
@@ -63,15 +65,19 @@ struct Kv8Attn {
 
 template <int D, int RT>
 struct AttnShape {
-    static constexpr int kStageBytes = 2 * kAtTile * D;
-    static constexpr int kMergeBytes = kAtWarps * RT * 8 * D * 4;
-    static constexpr int kStages = std::min(6, (int)((226 * 1024 - kMergeBytes - 2 * kAtWarps * RT * 32) / (kAtWarps * (kStageBytes + 8))));
-    static constexpr int kRing = kAtWarps * kStages * kStageBytes;
-    static constexpr int kScales = kRing;                                    // [warp][stage][2] fp32
-    static constexpr int kMerge = kScales + kAtWarps * kStages * 8;
-    static constexpr int kStats = kMerge + kMergeBytes;                      // [2][warp][rows] fp32
-    static constexpr int kBytes = kStats + 2 * kAtWarps * RT * 8 * 4;
-    static_assert(kStages >= 2 && kBytes <= 226 * 1024 + 512, "attention ring does not fit");
+    static constexpr int kHalf = kAtTile * D;        // bytes of a tile's keys, or of its values
+    static constexpr int kRows = RT * 8;
+    static constexpr int kMergeBytes = kAtWarps * 8 * D * 4;  // eight rows at a time
+    static constexpr int kFixed = kMergeBytes + 2 * 2 * kAtWarps * kRows * 4 + RT * D * 16 + 2 * kRows * 4;
+    static constexpr int kHalves = std::min(6, (int)((226 * 1024 - kFixed) / (kAtWarps * (kHalf + 4))));
+    static constexpr int kRing = kAtWarps * kHalves * kHalf;
+    static constexpr int kQ = kRing;                                       // q fragments, [RT][D / 32][32] x 16 bytes
+    static constexpr int kMerge = kQ + RT * D * 16;
+    static constexpr int kStats = kMerge + kMergeBytes;                    // [2][m, l][warp][rows] fp32
+    static constexpr int kRowInfo = kStats + 2 * 2 * kAtWarps * kRows * 4; // [rows] factor, [rows] limit
+    static constexpr int kScales = kRowInfo + 2 * kRows * 4;               // [warp][half] fp32
+    static constexpr int kBytes = kScales + kAtWarps * kHalves * 4;
+    static_assert(kHalves >= 3 && kBytes <= 226 * 1024 + 512, "attention ring does not fit");
 };
 
 __device__ __forceinline__ void at_cp16(unsigned dst, const void *src)
@@ -119,7 +125,7 @@ __device__ __forceinline__ float at_ref(float m) { return m == -INFINITY ? 0.f :
 // sequence b.  Tiles from `seen` on are visible to no row of the unit.
 struct AttnWalk {
     int64_t left;  // tiles of the range from this segment's start on
-    int b, u, units, tiles, ta, tb, seen;
+    int b, u, units, tiles, ta, tb, seen, h;
     Kv8Seq s;
     int rts;  // row tiles of the sequence
 };
@@ -140,8 +146,9 @@ template <int RT>
 __device__ __forceinline__ void at_segment(AttnWalk &w, const Kv8Attn &a)
 {
     w.tb = (int)min((int64_t)w.tiles, w.ta + w.left);
+    w.h = w.u / w.rts;
     // what the unit's last row sees
-    const int last = min(w.s.n - 1, ((w.u % w.rts + 1) * RT * 8 - 1) / a.G);
+    const int last = min(w.s.n - 1, ((w.u - w.h * w.rts + 1) * RT * 8 - 1) / a.G);
     const int vis = min(max(w.s.len - w.s.n + last + 1, 0), w.s.len);
     w.seen = (vis + kAtTile - 1) / kAtTile;
 }
@@ -172,9 +179,9 @@ template <int D, int RT>
 __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
 {
     using S = AttnShape<D, RT>;
-    constexpr int ROWS = RT * 8, NJ = D / 8, NS = S::kStages, KS = D / 32;
+    constexpr int ROWS = RT * 8, NJ = D / 8, NH = S::kHalves, KS = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t sh_sum[kAtThreads / 32];
+    __shared__ int64_t sh_sum[kAtWarps], sh_units[kAtWarps];
     __shared__ int64_t sh_off;
     __shared__ int sh_b, sh_last;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -184,153 +191,187 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
     // ---- this CTA's range of the batch's tiles ----
     const int per = (a.v.n_seqs + kAtThreads - 1) / kAtThreads;
     const int s0 = min(tid * per, a.v.n_seqs), s1 = min(s0 + per, a.v.n_seqs);
-    auto seq_work = [&](int b) -> int64_t {
+    auto seq_work = [&](int b, int64_t &units) -> int64_t {
         AttnWalk w;
         at_sequence<RT>(w, a, b);
+        units += w.units;
         return (int64_t)w.units * w.tiles;
     };
-    int64_t mine = 0;
-    for (int b = s0; b < s1; ++b) mine += seq_work(b);
+    int64_t mine = 0, units = 0;
+    for (int b = s0; b < s1; ++b) mine += seq_work(b, units);
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        units += __shfl_xor_sync(0xffffffffu, units, o);
         if (lane >= o) incl += x;
     }
-    if (lane == 31) sh_sum[warp] = incl;
+    if (lane == 31) {
+        sh_sum[warp] = incl;
+        sh_units[warp] = units;
+    }
     __syncthreads();
     int64_t total = 0, before = 0;
+    units = 0;
 #pragma unroll
-    for (int w = 0; w < kAtThreads / 32; ++w) {
+    for (int w = 0; w < kAtWarps; ++w) {
         if (w < warp) before += sh_sum[w];
         total += sh_sum[w];
+        units += sh_units[w];
     }
     if (total == 0) return;
-    // enough CTAs that a range has a tile for each warp
-    const int64_t C = min((int64_t)gridDim.x, (total + kAtWarps - 1) / kAtWarps);
+    // CTAs: one per unit where units are short (no joining between CTAs), else
+    // enough that a range has three tiles for each warp
+    const int64_t C = min(min((int64_t)gridDim.x, total), max(units, (total + 3 * kAtWarps - 1) / (3 * kAtWarps)));
     if (blockIdx.x >= C) return;
     const int64_t w0 = blockIdx.x * total / C, w1 = (blockIdx.x + 1) * total / C;
     {
         const int64_t excl = before + incl - mine;
         if (w0 >= excl && w0 < excl + mine) {
-            int64_t off = w0 - excl;
+            int64_t off = w0 - excl, u = 0;
             int b = s0;
-            for (int64_t x; off >= (x = seq_work(b)); ++b) off -= x;
+            for (int64_t x; off >= (x = seq_work(b, u)); ++b) off -= x;
             sh_b = b;
             sh_off = off;
         }
     }
     __syncthreads();
-    AttnWalk ld;
-    ld.left = w1 - w0;
-    at_sequence<RT>(ld, a, sh_b);
-    ld.u = (int)(sh_off / ld.tiles);
-    ld.ta = (int)(sh_off % ld.tiles);
-    at_segment<RT>(ld, a);
-    AttnWalk cw = ld;
+    AttnWalk cw;
+    cw.left = w1 - w0;
+    at_sequence<RT>(cw, a, sh_b);
+    cw.u = (int)(sh_off / cw.tiles);
+    cw.ta = (int)(sh_off % cw.tiles);
+    at_segment<RT>(cw, a);
     int64_t wpos = w0;  // of cw's segment
 
     // ---- this warp's ring ----
-    const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + warp * NS * S::kStageBytes;
-    const unsigned scal = (unsigned)__cvta_generic_to_shared(smem) + S::kScales + warp * NS * 8;
+    const unsigned smem0 = (unsigned)__cvta_generic_to_shared(smem);
+    const unsigned ring = smem0 + warp * NH * S::kHalf, scal = smem0 + S::kScales + warp * NH * 4;
+    // 16-byte slots of 128-byte lines, permuted so that the fragment loads below
+    // meet eight different ones; lane l copies pieces l, l + 32, ...
+    constexpr int CH = D / 16;
+    const int prow = lane / CH, pch = lane % CH;
+    const unsigned kdst = D == 128 ? prow * 128 + ((pch ^ (4 * (prow & 1))) << 4) : (prow >> 1) * 128 + (((prow & 1) * 4 + pch) << 4);
+    const unsigned vdst = D == 128 ? prow * 128 + (pch << 4) : (prow >> 1) * 128 + (((prow & 1) * 4 + pch) << 4);
+    AttnWalk ld = cw;
     int ld_tile = ld.ta + warp, ld_slot = 0;
-    bool ld_more = true;
-    // Copies this warp's next tile (nothing at the end of the range).  A tile
-    // without a valid page leaves scale 0 and stale codes behind; `present`
-    // tells the consumer.
-    unsigned present = 0;  // one bit per slot
+    bool ld_more = true, ld_value = false;
+    int64_t ld_at = 0;   // byte offset of the tile, this lane's first piece
+    int64_t ld_ph = -1;  // its page and head, -1 for an absent page
+    unsigned present = 0;  // one bit per slot: keys that are there
+    // Copies the next half of a tile (nothing at the end of the range).
     auto issue = [&]() {
-        while (ld_more && ld_tile >= min(ld.tb, ld.seen)) {
-            ld_more = at_next<RT>(ld, a);
-            ld_tile = ld.ta + warp;
-        }
-        if (ld_more) {
-            const int tok = ld_tile * kAtTile;
-            const int page = kv8_page(a.v, ld.b, tok / a.v.P, &g_at_fault);
-            present &= ~(1u << ld_slot);
-            if (page >= 0) {
-                present |= 1u << ld_slot;
-                const int64_t ph = (int64_t)page * a.v.H + ld.u / ld.rts;
-                const int64_t at = (ph * a.v.P + tok % a.v.P) * D;
-                const unsigned st = ring + ld_slot * S::kStageBytes;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const int e = i * 32 + lane, row = e / (D / 16), ch = e % (D / 16);
-                    // 16-byte slots of a 128-byte line, permuted so that the
-                    // fragment loads below meet eight different ones
-                    const int line = D == 128 ? row : row >> 1, slot = D == 128 ? ch : (row & 1) * 4 + ch;
-                    const int kx = D == 128 ? 4 * (row & 1) : 0, vx = 2 * ((row >> 2) & 3);
-                    at_cp16(st + line * 128 + ((slot ^ kx) << 4), a.k + at + e * 16);
-                    at_cp16(st + kAtTile * D + line * 128 + ((slot ^ vx) << 4), a.vv + at + e * 16);
-                }
-                if (lane < 2) at_cp4(scal + ld_slot * 8 + lane * 4, (lane ? a.vs : a.ks) + ph);
+        if (!ld_value) {
+            while (ld_more && ld_tile >= min(ld.tb, ld.seen)) {
+                ld_more = at_next<RT>(ld, a);
+                ld_tile = ld.ta + warp;
             }
-            ld_tile += kAtWarps;
+            ld_ph = -1;
+            if (ld_more) {
+                const int tok = ld_tile * kAtTile;
+                const int page = kv8_page(a.v, ld.b, tok >> a.page_log2, &g_at_fault);
+                if (page >= 0) {
+                    ld_ph = (int64_t)page * a.v.H + ld.h;
+                    ld_at = ((ld_ph << a.page_log2) + (tok & (a.v.P - 1))) * D + lane * 16;
+                }
+                ld_tile += kAtWarps;
+            }
+            present = ld_ph >= 0 ? present | (1u << ld_slot) : present & ~(1u << ld_slot);
+        }
+        if (ld_ph >= 0) {
+            const int8_t *src = (ld_value ? a.vv : a.k) + ld_at;
+            const unsigned st = ring + ld_slot * S::kHalf;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                // rows advance by 32 / CH: 4 (D = 128) or 8 (two lines by two)
+                if (ld_value) {
+                    const unsigned x = D == 128 ? (unsigned)(2 * (i & 3)) << 4 : (unsigned)(2 * ((2 * i + (prow >> 2)) & 3)) << 4;
+                    at_cp16(st + i * 512 + (vdst ^ x), src + i * 512);
+                } else {
+                    at_cp16(st + i * 512 + kdst, src + i * 512);
+                }
+            }
+            if (lane == 0) at_cp4(scal + ld_slot * 4, (ld_value ? a.vs : a.ks) + ld_ph);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        ld_slot = ld_slot + 1 == NS ? 0 : ld_slot + 1;
+        ld_value = !ld_value;
+        ld_slot = ld_slot + 1 == NH ? 0 : ld_slot + 1;
     };
 #pragma unroll 1
-    for (int i = 0; i < NS - 1; ++i) issue();
+    for (int i = 0; i < NH - 1; ++i) issue();
     int slot = 0;
 
+    // ---- q of a unit's rows as two int8 limbs, in fragment order ----
+    // Thread x < ROWS D / 8 takes 8 entries of row x / (D / 8); a segment's q is
+    // loaded while the segment before it is worked on.
+    constexpr int QT = D / 8;  // threads per row
+    const int qrow = tid / QT, qpart = tid % QT;
+    uint4 qraw = make_uint4(0, 0, 0, 0);
+    auto load_q = [&](const AttnWalk &w) {
+        qraw = make_uint4(0, 0, 0, 0);
+        const int r = w.u % w.rts * ROWS + qrow, i = r / a.G;
+        if (qrow < ROWS && i < w.s.n)
+            qraw = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.r0 + i) * a.q_stride +
+                                                         (int64_t)(w.h * a.G + r % a.G) * D + qpart * 8));
+    };
+    float *row_f = reinterpret_cast<float *>(smem + S::kRowInfo);
+    int *row_lim = reinterpret_cast<int *>(row_f + ROWS);
+    auto store_q = [&](const AttnWalk &w) {
+        if (tid >= ROWS * QT) return;
+        const int r = w.u % w.rts * ROWS + qrow, i = r / a.G;
+        // rows past the sequence's see what is there, as zeros
+        const int lim = i < w.s.n ? min(max(w.s.len - w.s.n + i + 1, 0), w.s.len) : w.s.len;
+        const uint32_t raw[4] = {qraw.x, qraw.y, qraw.z, qraw.w};
+        float f[8];
+        float top = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            f[y] = __uint_as_float(y & 1 ? raw[y / 2] & 0xFFFF0000u : raw[y / 2] << 16);
+            top = fmaxf(top, fabsf(f[y]));
+            bad |= !(fabsf(f[y]) <= FLT_MAX);
+        }
+        const unsigned group = QT == 16 ? 0xFFFFu << (lane & 16) : 0xFFu << (lane & 24);
+#pragma unroll
+        for (int o = 1; o < QT; o <<= 1) top = fmaxf(top, __shfl_xor_sync(group, top, o));
+        bad = (__ballot_sync(group, bad) & group) != 0;
+        const float inv = top >= 0x1p-100f && !bad ? 32512.f / top : 0.f;
+        uint32_t limb[4] = {0, 0, 0, 0};  // hi and lo of entries 0-3, of 4-7
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const int v = __float2int_rn(f[y] * inv), vh = (v + 128) >> 8;
+            limb[y / 4 * 2] |= (uint32_t)(vh & 0xFF) << (8 * (y & 3));
+            limb[y / 4 * 2 + 1] |= (uint32_t)((v - vh * 256) & 0xFF) << (8 * (y & 3));
+        }
+        // entries 8 qpart ..: 16-byte chunk qpart / 2 of a key, which lane t =
+        // chunk % 4 of fragments 2 (chunk / 4) and the next one holds
+        const int ch = qpart >> 1, frag = 2 * (ch >> 2) + (qpart & 1);
+        reinterpret_cast<uint4 *>(smem + S::kQ)[((qrow >> 3) * KS + frag) * 32 + (qrow & 7) * 4 + (ch & 3)] =
+            make_uint4(limb[0], limb[1], limb[2], limb[3]);
+        if (qpart == 0) {
+            row_f[qrow] = bad && lim > 0 ? NAN : top * (1.f / 32512.f) * a.scale_log2;
+            row_lim[qrow] = lim;
+        }
+    };
+    load_q(cw);
+    store_q(cw);
+    __syncthreads();
+
     float *merge = reinterpret_cast<float *>(smem + S::kMerge);
-    float *stat_m = reinterpret_cast<float *>(smem + S::kStats), *stat_l = stat_m + kAtWarps * ROWS;
+    int parity = 0;
 
     while (true) {
-        const int h = cw.u / cw.rts, row0 = cw.u % cw.rts * ROWS;
-        // ---- q of the unit's rows as two int8 limbs ----
-        uint32_t qf[RT][KS][4];
+        AttnWalk nw = cw;
+        const bool more = at_next<RT>(nw, a);
+        if (more) load_q(nw);
+        const int h = cw.h, row0 = cw.u % cw.rts * ROWS;
         float rowf[RT];
-        int lim[RT];
-        int lim_min = INT_MAX;
+        int lim[RT], lim_min = INT_MAX;
 #pragma unroll
         for (int m = 0; m < RT; ++m) {
-            const int r = row0 + m * 8 + g, i = r / a.G;
-            const bool valid = i < cw.s.n;
-            lim[m] = valid ? min(max(cw.s.len - cw.s.n + i + 1, 0), cw.s.len) : cw.s.len;
+            rowf[m] = row_f[m * 8 + g];
+            lim[m] = row_lim[m * 8 + g];
             lim_min = min(lim_min, lim[m]);
-            float f[D / 4];
-            const uint16_t *qp = a.q + (int64_t)(cw.s.r0 + i) * a.q_stride + (int64_t)(h * a.G + r % a.G) * D;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (valid) u = __ldg(reinterpret_cast<const uint4 *>(qp + c * 64 + t * 16 + x * 8));
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        f[c * 16 + x * 8 + 2 * y] = __uint_as_float(w[y] << 16);
-                        f[c * 16 + x * 8 + 2 * y + 1] = __uint_as_float(w[y] & 0xFFFF0000u);
-                    }
-                }
-            float top = 0.f;
-            bool bad = false;
-#pragma unroll
-            for (int x = 0; x < D / 4; ++x) {
-                top = fmaxf(top, fabsf(f[x]));
-                bad |= !(fabsf(f[x]) <= FLT_MAX);
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 1) != 0;
-            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 2) != 0;
-            const float inv = top >= 0x1p-100f && !bad ? 32512.f / top : 0.f;
-            rowf[m] = bad && lim[m] > 0 ? NAN : top * (1.f / 32512.f) * a.scale_log2;
-#pragma unroll
-            for (int w = 0; w < D / 16; ++w) {
-                uint32_t hi = 0, lo = 0;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int v = __float2int_rn(f[4 * w + y] * inv), vh = (v + 128) >> 8;
-                    hi |= (uint32_t)(vh & 0xFF) << (8 * y);
-                    lo |= (uint32_t)((v - vh * 256) & 0xFF) << (8 * y);
-                }
-                // word w of this thread's entries: fragment pair w / 2
-                qf[m][w / 2][(w & 1) * 2] = hi;
-                qf[m][w / 2][(w & 1) * 2 + 1] = lo;
-            }
         }
         lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
@@ -344,42 +385,53 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
         }
 
         for (int tile = cw.ta + warp; tile < min(cw.tb, cw.seen); tile += kAtWarps) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(NH - 2) : "memory");
             __syncwarp();
+            const bool there = (present >> slot) & 1;
             issue();  // into the slot read last, while this one is worked on
-            const unsigned st = ring + slot * S::kStageBytes;
-            if ((present >> slot) & 1) {
-                float sc[2];
-                asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(sc[0]), "=f"(sc[1]) : "r"(scal + slot * 8));
+            uint32_t pf[RT][4];
+            float fac[RT], al[RT];
+            bool same = true;
+            if (there) {
+                const unsigned st = ring + slot * S::kHalf;
+                float ks;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks) : "r"(scal + slot * 4));
                 // scores: column n of block j is token 16 (j / 2) + 4 (n / 2) +
                 // 2 (j % 2) + n % 2, so that a thread's scores are those of the
                 // tokens its probability fragment holds
                 int acc[RT][4][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int m = 0; m < RT; ++m)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) acc[m][j][x] = 0;
-                    const int tr = 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1);
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t qf[RT][2][4];
+#pragma unroll
+                    for (int m = 0; m < RT; ++m)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint4 u = at_lds16(smem0 + S::kQ + ((m * KS + 2 * c + y) * 32 + lane) * 16);
+                            qf[m][y][0] = u.x; qf[m][y][1] = u.y; qf[m][y][2] = u.z; qf[m][y][3] = u.w;
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int tr = 16 * (j >> 1) + 4 * (g >> 1) + 2 * (j & 1) + (g & 1);
                         const int sl = D == 128 ? ((t + 4 * c) ^ (4 * (g & 1))) : (g & 1) * 4 + t;
                         const uint4 x = at_lds16(st + (D == 128 ? tr : tr >> 1) * 128 + (sl << 4));
 #pragma unroll
                         for (int m = 0; m < RT; ++m) {
-                            at_mma_ss(acc[m][j], qf[m][2 * c], x.x, x.y);
-                            at_mma_ss(acc[m][j], qf[m][2 * c + 1], x.z, x.w);
+                            at_mma_ss(acc[m][j], qf[m][0], x.x, x.y);
+                            at_mma_ss(acc[m][j], qf[m][1], x.z, x.w);
                         }
                     }
                 }
-                uint32_t pf[RT][4];
-                float al[RT], fac[RT];
-                bool same = true;
                 const bool masked = (tile + 1) * kAtTile > lim_min;
 #pragma unroll
                 for (int m = 0; m < RT; ++m) {
-                    const float f = rowf[m] * sc[0];
+                    const float f = rowf[m] * ks;
                     float s[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {  // token 16 (x / 4) + 4 t + x % 4
@@ -414,24 +466,33 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
                     const float mn = fmaxf(mx[m], tm), rn = at_ref(mn);
                     al[m] = at_exp2(mx[m] - rn);
                     // 0 * rowf: a NaN row stays one where masked tokens hide it
-                    const float w = at_exp2(tm - rn) * (1.f / 65280.f) + 0.f * rowf[m];
-                    fac[m] = w * sc[1];
-                    l[m] = l[m] * al[m] + (float)sum * w;
+                    fac[m] = at_exp2(tm - rn) * (1.f / 65280.f) + 0.f * rowf[m];
+                    l[m] = l[m] * al[m] + (float)sum * fac[m];
                     same = same && mx[m] == mn;
                     mx[m] = mn;
                 }
-                // rows whose maximum stands keep their sums as they are
-                if (!__all_sync(0xffffffffu, same)) {
+            }
+            // rows whose maximum stands keep their sums as they are
+            if (!__all_sync(0xffffffffu, same)) {
 #pragma unroll
-                    for (int m = 0; m < RT; ++m)
+                for (int m = 0; m < RT; ++m)
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
-                            o[m][j][0] *= al[m];
-                            o[m][j][1] *= al[m];
-                        }
-                }
+                    for (int j = 0; j < NJ; ++j) {
+                        o[m][j][0] *= al[m];
+                        o[m][j][1] *= al[m];
+                    }
+            }
+            slot = slot + 1 == NH ? 0 : slot + 1;
+            asm volatile("cp.async.wait_group %0;" ::"n"(NH - 2) : "memory");
+            __syncwarp();
+            issue();
+            if (there) {
+                const unsigned vb = ring + slot * S::kHalf;
+                float vs;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(scal + slot * 4));
+#pragma unroll
+                for (int m = 0; m < RT; ++m) fac[m] *= vs;
                 // products with v: column n of block j is entry (D / 8) n + j
-                const unsigned vb = st + kAtTile * D;
                 constexpr int VW = D / 32;  // words of a token's entries per thread
                 uint32_t x[2][4][VW];
 #pragma unroll
@@ -473,11 +534,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
                         }
                 }
             }
-            __syncwarp();  // every lane has read the slot
-            slot = slot + 1 == NS ? 0 : slot + 1;
+            slot = slot + 1 == NH ? 0 : slot + 1;
         }
 
         // ---- join the warps' sums ----
+        // (statistics alternate between two places: the next segment's may be
+        // written while this one's are still read)
+        float *stat_m = reinterpret_cast<float *>(smem + S::kStats) + parity * 2 * kAtWarps * ROWS;
+        float *stat_l = stat_m + kAtWarps * ROWS;
+        parity ^= 1;
 #pragma unroll
         for (int m = 0; m < RT; ++m) {
             l[m] += __shfl_xor_sync(0xffffffffu, l[m], 1);
@@ -488,54 +553,57 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
             }
         }
         __syncthreads();
-#pragma unroll
-        for (int m = 0; m < RT; ++m) {
-            const int row = m * 8 + g;
-            float top = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, stat_m[w * ROWS + row]);
-            const float f = at_exp2(mx[m] - at_ref(top));
-            float4 *dst = reinterpret_cast<float4 *>(merge + (warp * ROWS + row) * D + t * (D / 4));
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                // entries 4 i .. 4 i + 3 of the thread's D / 4 consecutive ones
-                const int e = i / (D / 32), j = 4 * (i % (D / 32));
-                const int sw = D == 128 ? (row & 1) * 4 + t : (row & 1) * 2 + (t >> 1);
-                dst[i ^ sw] = make_float4(o[m][j][e] * f, o[m][j + 1][e] * f, o[m][j + 2][e] * f, o[m][j + 3][e] * f);
-            }
-        }
-        __syncthreads();
         const bool whole = cw.ta == 0 && cw.tb == cw.tiles;
         const int part = 2 * blockIdx.x + (cw.ta == 0 ? 1 : 0);
-        for (int i = tid; i < ROWS * D / 4; i += kAtThreads) {
-            const int row = i / (D / 4), d4 = i % (D / 4), tt = d4 / (D / 16), x = d4 % (D / 16);
-            const int sw = D == 128 ? (row & 1) * 4 + tt : (row & 1) * 2 + (tt >> 1);
-            float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, stat_m[w * ROWS + row]);
-            float sum = 0.f;
-            float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int m = 0; m < RT; ++m) {
+            if (m > 0) __syncthreads();  // the sums of the rows before are read
+            {
+                const int row = m * 8 + g;
+                float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kAtWarps; ++w) {
-                sum += stat_l[w * ROWS + row] * at_exp2(stat_m[w * ROWS + row] - at_ref(top));
-                const float4 v =
-                    reinterpret_cast<const float4 *>(merge + (w * ROWS + row) * D + tt * (D / 4))[x ^ sw];
-                acc4.x += v.x; acc4.y += v.y; acc4.z += v.z; acc4.w += v.w;
-            }
-            if (whole) {
-                const int r = row0 + row, ri = r / a.G;
-                if (ri < cw.s.n) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    uint16_t *op = a.out + (int64_t)(cw.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D;
-                    uint2 pk;
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.x) : "f"(acc4.y * inv), "f"(acc4.x * inv));
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.y) : "f"(acc4.w * inv), "f"(acc4.z * inv));
-                    reinterpret_cast<uint2 *>(op)[d4] = pk;
+                for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, stat_m[w * ROWS + row]);
+                const float f = at_exp2(mx[m] - at_ref(top));
+                float4 *dst = reinterpret_cast<float4 *>(merge + (warp * 8 + g) * D + t * (D / 4));
+                const int sw = D == 128 ? (g & 1) * 4 + t : (g & 1) * 2 + (t >> 1);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    // entries 4 i .. 4 i + 3 of the thread's D / 4 consecutive ones
+                    const int e = i / (D / 32), j = 4 * (i % (D / 32));
+                    dst[i ^ sw] = make_float4(o[m][j][e] * f, o[m][j + 1][e] * f, o[m][j + 2][e] * f, o[m][j + 3][e] * f);
                 }
-            } else {
-                reinterpret_cast<float4 *>(a.part_o + ((int64_t)part * ROWS + row) * D)[d4] = acc4;
-                if (d4 == 0)
-                    reinterpret_cast<float2 *>(a.part_ml)[(int64_t)part * ROWS + row] = make_float2(top, sum);
+            }
+            if (m == 0 && more) store_q(nw);  // every warp is done with this segment's
+            __syncthreads();
+            if (tid < 8 * D / 4) {
+                const int r8 = tid / (D / 4), row = m * 8 + r8, d4 = tid % (D / 4), tt = d4 / (D / 16), x = d4 % (D / 16);
+                const int sw = D == 128 ? (r8 & 1) * 4 + tt : (r8 & 1) * 2 + (tt >> 1);
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, stat_m[w * ROWS + row]);
+                float sum = 0.f;
+                float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kAtWarps; ++w) {
+                    sum += stat_l[w * ROWS + row] * at_exp2(stat_m[w * ROWS + row] - at_ref(top));
+                    const float4 v = reinterpret_cast<const float4 *>(merge + (w * 8 + r8) * D + tt * (D / 4))[x ^ sw];
+                    acc4.x += v.x; acc4.y += v.y; acc4.z += v.z; acc4.w += v.w;
+                }
+                if (whole) {
+                    const int r = row0 + row, ri = r / a.G;
+                    if (ri < cw.s.n) {
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        uint16_t *op = a.out + (int64_t)(cw.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D;
+                        uint2 pk;
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.x) : "f"(acc4.y * inv), "f"(acc4.x * inv));
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.y) : "f"(acc4.w * inv), "f"(acc4.z * inv));
+                        reinterpret_cast<uint2 *>(op)[d4] = pk;
+                    }
+                } else {
+                    reinterpret_cast<float4 *>(a.part_o + ((int64_t)part * ROWS + row) * D)[d4] = acc4;
+                    if (d4 == 0)
+                        reinterpret_cast<float2 *>(a.part_ml)[(int64_t)part * ROWS + row] = make_float2(top, sum);
+                }
             }
         }
         if (!whole) {
@@ -582,9 +650,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
                 }
             }
         }
-        __syncthreads();  // the statistics and sums are free again
         wpos += cw.tb - cw.ta;
-        if (!at_next<RT>(cw, a)) break;
+        if (!more) break;
+        cw = nw;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -615,6 +683,7 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     a.k = c.k; a.vv = c.v; a.ks = c.k_scales; a.vs = c.v_scales;
     a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
     a.G = q_heads / c.n_heads;
+    a.page_log2 = c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
     a.scale_log2 = scale * 1.4426950408889634f;
     const int ctas = attn_ctas();
     uint8_t *ws = static_cast<uint8_t *>(workspace);
