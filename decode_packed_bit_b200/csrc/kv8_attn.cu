@@ -19,13 +19,15 @@
 //
 // Layout of the work.  A unit is (sequence, cache head, RT * 8 query rows); its
 // tokens come in tiles of 32.  All tiles of all units, in order, are cut into
-// equal ranges, one per CTA (one CTA per SM); lengths are read on the device,
-// so a captured graph follows them.  The warps of a CTA take a range's tiles in
-// turn, each with its own cp.async ring of key and value halves of tiles, which
-// runs on across the ends of units, and join their partial sums through shared
-// memory at the end of a unit; a unit cut between CTAs is joined in
-// CTA order by the last of them to arrive (a counter in the workspace, left
-// zeroed), so the result does not depend on timing.
+// equal ranges, one per CTA (one CTA per SM), and a CTA's range into equal ranges
+// for its warps; lengths are read on the device, so a captured graph follows
+// them.  A warp goes through its range alone, with a cp.async ring of key and
+// value halves of tiles that runs on across the ends of units, and writes the
+// units that lie wholly within.  What it has of a unit cut at its range's start
+// or end stays in shared memory; one barrier later the CTA joins those parts in
+// order.  A unit cut between CTAs is joined, in CTA order, by the last of them to
+// arrive (a counter in the workspace, left zeroed), so the result does not
+// depend on timing.
 #include <algorithm>
 #include <cfloat>
 
@@ -43,8 +45,6 @@ int kv8_attn_fault_flag()
     return (int)v;
 }
 
-constexpr int kAtWarps = 12;  // 168 registers a thread; with 8 warps the chains of a tile's steps showed
-constexpr int kAtThreads = kAtWarps * 32;
 constexpr int kAtTile = 32;  // tokens
 constexpr int kAtMaxRT = 2;
 
@@ -65,19 +65,21 @@ struct Kv8Attn {
 
 template <int D, int RT>
 struct AttnShape {
-    static constexpr int kHalf = kAtTile * D;        // bytes of a tile's keys, or of its values
+    static constexpr int kWarps = RT == 1 ? 12 : 8;  // 168 or 255 registers a thread
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = RT * 8;
-    static constexpr int kMergeBytes = kAtWarps * 8 * D * 4;  // eight rows at a time
-    static constexpr int kFixed = kMergeBytes + 2 * 2 * kAtWarps * kRows * 4 + RT * D * 16 + 2 * kRows * 4;
-    static constexpr int kHalves = std::min(6, (int)((226 * 1024 - kFixed) / (kAtWarps * (kHalf + 4))));
-    static constexpr int kRing = kAtWarps * kHalves * kHalf;
-    static constexpr int kQ = kRing;                                       // q fragments, [RT][D / 32][32] x 16 bytes
-    static constexpr int kMerge = kQ + RT * D * 16;
-    static constexpr int kStats = kMerge + kMergeBytes;                    // [2][m, l][warp][rows] fp32
-    static constexpr int kRowInfo = kStats + 2 * 2 * kAtWarps * kRows * 4; // [rows] factor, [rows] limit
-    static constexpr int kScales = kRowInfo + 2 * kRows * 4;               // [warp][half] fp32
-    static constexpr int kBytes = kScales + kAtWarps * kHalves * 4;
-    static_assert(kHalves >= 3 && kBytes <= 226 * 1024 + 512, "attention ring does not fit");
+    static constexpr int kHalf = kAtTile * D;                              // bytes of a tile's keys, or of its values
+    static constexpr int kPart = kRows * D * 4;                            // a part's sums
+    static constexpr int kQBytes = RT * D * 16;                            // q fragments of a warp, [RT][D / 32][32] x 16 bytes
+    static constexpr int kFixed = kWarps * (kPart + kQBytes + 2 * 2 * kRows * 4);
+    static constexpr int kHalves = std::min(6, (int)((224 * 1024 - kFixed) / (kWarps * (kHalf + 4))));
+    static constexpr int kRing = kWarps * kHalves * kHalf;
+    static constexpr int kQ = kRing;
+    static constexpr int kHead = kQ + kWarps * kQBytes;                    // sums of a unit cut at the warp's start
+    static constexpr int kStats = kHead + kWarps * kPart;                  // [m, l][2 warps][rows] fp32
+    static constexpr int kScales = kStats + 2 * 2 * kWarps * kRows * 4;    // [warp][half] fp32
+    static constexpr int kBytes = kScales + kWarps * kHalves * 4;
+    static_assert(kHalves >= 3 && kHalves * kHalf >= kPart && kBytes <= 225 * 1024, "attention ring does not fit");
 };
 
 __device__ __forceinline__ void at_cp16(unsigned dst, const void *src)
@@ -153,6 +155,22 @@ __device__ __forceinline__ void at_segment(AttnWalk &w, const Kv8Attn &a)
     w.seen = (vis + kAtTile - 1) / kAtTile;
 }
 
+// The first segment of the range of `left` tiles that starts `off` tiles after
+// sequence b's first.
+template <int RT>
+__device__ __forceinline__ void at_start(AttnWalk &w, const Kv8Attn &a, int b, int64_t off, int64_t left)
+{
+    at_sequence<RT>(w, a, b);
+    while (off >= (int64_t)w.units * w.tiles) {
+        off -= (int64_t)w.units * w.tiles;
+        at_sequence<RT>(w, a, w.b + 1);
+    }
+    w.left = left;
+    w.u = (int)(off / w.tiles);
+    w.ta = (int)(off % w.tiles);
+    at_segment<RT>(w, a);
+}
+
 // On to the next segment; false at the end of the range.
 template <int RT>
 __device__ __forceinline__ bool at_next(AttnWalk &w, const Kv8Attn &a)
@@ -175,21 +193,42 @@ __device__ __forceinline__ bool at_next(AttnWalk &w, const Kv8Attn &a)
     return true;
 }
 
+__device__ __forceinline__ void at_store4(uint16_t *p, float x, float y, float z, float w)
+{
+    uint2 v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(y), "f"(x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(w), "f"(z));
+    *reinterpret_cast<uint2 *>(p) = v;
+}
+
+// Where the 16-byte piece i of lane group t's quarter of a part's row lies: permuted
+// so that a quarter-warp's stores meet eight different ones.
+template <int D>
+__device__ __forceinline__ int at_piece(int row, int t, int i)
+{
+    return t * (D / 16) + (i ^ (D == 128 ? (row & 1) * 4 + t : (row & 1) * 2 + (t >> 1)));
+}
+
 template <int D, int RT>
-__global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
+__global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(const Kv8Attn a)
 {
     using S = AttnShape<D, RT>;
-    constexpr int ROWS = RT * 8, NJ = D / 8, NH = S::kHalves, KS = D / 32;
+    constexpr int W = S::kWarps, ROWS = S::kRows, NJ = D / 8, NH = S::kHalves, KS = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t sh_sum[kAtWarps], sh_units[kAtWarps];
+    __shared__ int64_t sh_sum[W], sh_units[W];
     __shared__ int64_t sh_off;
     __shared__ int sh_b, sh_last;
+    // a warp's cut units: sequence, unit, place of the unit's start in the whole
+    // work; of its parts the head is 2 warp, the tail 2 warp + 1
+    __shared__ int part_b[2 * W], part_u[2 * W];
+    __shared__ int64_t part_start[2 * W];
+    __shared__ int group_first[2 * W], group_n[2 * W], groups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     pdl_wait_primary();
 
     // ---- this CTA's range of the batch's tiles ----
-    const int per = (a.v.n_seqs + kAtThreads - 1) / kAtThreads;
+    const int per = (a.v.n_seqs + S::kThreads - 1) / S::kThreads;
     const int s0 = min(tid * per, a.v.n_seqs), s1 = min(s0 + per, a.v.n_seqs);
     auto seq_work = [&](int b, int64_t &units) -> int64_t {
         AttnWalk w;
@@ -210,19 +249,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
         sh_sum[warp] = incl;
         sh_units[warp] = units;
     }
+    if (tid < 2 * W) part_b[tid] = -1;
     __syncthreads();
     int64_t total = 0, before = 0;
     units = 0;
 #pragma unroll
-    for (int w = 0; w < kAtWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
         if (w < warp) before += sh_sum[w];
         total += sh_sum[w];
         units += sh_units[w];
     }
     if (total == 0) return;
     // CTAs: one per unit where units are short (no joining between CTAs), else
-    // enough that a range has three tiles for each warp
-    const int64_t C = min(min((int64_t)gridDim.x, total), max(units, (total + 3 * kAtWarps - 1) / (3 * kAtWarps)));
+    // enough that a warp has three tiles
+    const int64_t C = min(min((int64_t)gridDim.x, total), max(units, (total + 3 * W - 1) / (3 * W)));
     if (blockIdx.x >= C) return;
     const int64_t w0 = blockIdx.x * total / C, w1 = (blockIdx.x + 1) * total / C;
     {
@@ -236,16 +276,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
         }
     }
     __syncthreads();
+    // ---- this warp's range (none is empty before another that is not) ----
+    const int64_t active = min((int64_t)W, w1 - w0);
+    const int64_t v0 = min((int64_t)warp, active) * (w1 - w0) / active, v1 = min((int64_t)warp + 1, active) * (w1 - w0) / active;
+    const unsigned smem0 = (unsigned)__cvta_generic_to_shared(smem);
+    float *stat_m = reinterpret_cast<float *>(smem + S::kStats), *stat_l = stat_m + 2 * W * ROWS;
+    if (v1 > v0) {
     AttnWalk cw;
-    cw.left = w1 - w0;
-    at_sequence<RT>(cw, a, sh_b);
-    cw.u = (int)(sh_off / cw.tiles);
-    cw.ta = (int)(sh_off % cw.tiles);
-    at_segment<RT>(cw, a);
-    int64_t wpos = w0;  // of cw's segment
+    at_start<RT>(cw, a, sh_b, sh_off + v0, v1 - v0);
+    int64_t wpos = w0 + v0;  // of cw's segment
 
     // ---- this warp's ring ----
-    const unsigned smem0 = (unsigned)__cvta_generic_to_shared(smem);
     const unsigned ring = smem0 + warp * NH * S::kHalf, scal = smem0 + S::kScales + warp * NH * 4;
     // 16-byte slots of 128-byte lines, permuted so that the fragment loads below
     // meet eight different ones; lane l copies pieces l, l + 32, ...
@@ -254,7 +295,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
     const unsigned kdst = D == 128 ? prow * 128 + ((pch ^ (4 * (prow & 1))) << 4) : (prow >> 1) * 128 + (((prow & 1) * 4 + pch) << 4);
     const unsigned vdst = D == 128 ? prow * 128 + (pch << 4) : (prow >> 1) * 128 + (((prow & 1) * 4 + pch) << 4);
     AttnWalk ld = cw;
-    int ld_tile = ld.ta + warp, ld_slot = 0;
+    int ld_tile = ld.ta, ld_slot = 0;
     bool ld_more = true, ld_value = false;
     int64_t ld_at = 0;   // byte offset of the tile, this lane's first piece
     int64_t ld_ph = -1;  // its page and head, -1 for an absent page
@@ -264,7 +305,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
         if (!ld_value) {
             while (ld_more && ld_tile >= min(ld.tb, ld.seen)) {
                 ld_more = at_next<RT>(ld, a);
-                ld_tile = ld.ta + warp;
+                ld_tile = ld.ta;
             }
             ld_ph = -1;
             if (ld_more) {
@@ -274,7 +315,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
                     ld_ph = (int64_t)page * a.v.H + ld.h;
                     ld_at = ((ld_ph << a.page_log2) + (tok & (a.v.P - 1))) * D + lane * 16;
                 }
-                ld_tile += kAtWarps;
+                ++ld_tile;
             }
             present = ld_ph >= 0 ? present | (1u << ld_slot) : present & ~(1u << ld_slot);
         }
@@ -300,80 +341,66 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
 #pragma unroll 1
     for (int i = 0; i < NH - 1; ++i) issue();
     int slot = 0;
-
-    // ---- q of a unit's rows as two int8 limbs, in fragment order ----
-    // Thread x < ROWS D / 8 takes 8 entries of row x / (D / 8); a segment's q is
-    // loaded while the segment before it is worked on.
-    constexpr int QT = D / 8;  // threads per row
-    const int qrow = tid / QT, qpart = tid % QT;
-    uint4 qraw = make_uint4(0, 0, 0, 0);
-    auto load_q = [&](const AttnWalk &w) {
-        qraw = make_uint4(0, 0, 0, 0);
-        const int r = w.u % w.rts * ROWS + qrow, i = r / a.G;
-        if (qrow < ROWS && i < w.s.n)
-            qraw = __ldg(reinterpret_cast<const uint4 *>(a.q + (int64_t)(w.s.r0 + i) * a.q_stride +
-                                                         (int64_t)(w.h * a.G + r % a.G) * D + qpart * 8));
-    };
-    float *row_f = reinterpret_cast<float *>(smem + S::kRowInfo);
-    int *row_lim = reinterpret_cast<int *>(row_f + ROWS);
-    auto store_q = [&](const AttnWalk &w) {
-        if (tid >= ROWS * QT) return;
-        const int r = w.u % w.rts * ROWS + qrow, i = r / a.G;
-        // rows past the sequence's see what is there, as zeros
-        const int lim = i < w.s.n ? min(max(w.s.len - w.s.n + i + 1, 0), w.s.len) : w.s.len;
-        const uint32_t raw[4] = {qraw.x, qraw.y, qraw.z, qraw.w};
-        float f[8];
-        float top = 0.f;
-        bool bad = false;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-            f[y] = __uint_as_float(y & 1 ? raw[y / 2] & 0xFFFF0000u : raw[y / 2] << 16);
-            top = fmaxf(top, fabsf(f[y]));
-            bad |= !(fabsf(f[y]) <= FLT_MAX);
-        }
-        const unsigned group = QT == 16 ? 0xFFFFu << (lane & 16) : 0xFFu << (lane & 24);
-#pragma unroll
-        for (int o = 1; o < QT; o <<= 1) top = fmaxf(top, __shfl_xor_sync(group, top, o));
-        bad = (__ballot_sync(group, bad) & group) != 0;
-        const float inv = top >= 0x1p-100f && !bad ? 32512.f / top : 0.f;
-        uint32_t limb[4] = {0, 0, 0, 0};  // hi and lo of entries 0-3, of 4-7
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-            const int v = __float2int_rn(f[y] * inv), vh = (v + 128) >> 8;
-            limb[y / 4 * 2] |= (uint32_t)(vh & 0xFF) << (8 * (y & 3));
-            limb[y / 4 * 2 + 1] |= (uint32_t)((v - vh * 256) & 0xFF) << (8 * (y & 3));
-        }
-        // entries 8 qpart ..: 16-byte chunk qpart / 2 of a key, which lane t =
-        // chunk % 4 of fragments 2 (chunk / 4) and the next one holds
-        const int ch = qpart >> 1, frag = 2 * (ch >> 2) + (qpart & 1);
-        reinterpret_cast<uint4 *>(smem + S::kQ)[((qrow >> 3) * KS + frag) * 32 + (qrow & 7) * 4 + (ch & 3)] =
-            make_uint4(limb[0], limb[1], limb[2], limb[3]);
-        if (qpart == 0) {
-            row_f[qrow] = bad && lim > 0 ? NAN : top * (1.f / 32512.f) * a.scale_log2;
-            row_lim[qrow] = lim;
-        }
-    };
-    load_q(cw);
-    store_q(cw);
-    __syncthreads();
-
-    float *merge = reinterpret_cast<float *>(smem + S::kMerge);
-    int parity = 0;
+    const unsigned qsm = smem0 + S::kQ + warp * S::kQBytes;
 
     while (true) {
-        AttnWalk nw = cw;
-        const bool more = at_next<RT>(nw, a);
-        if (more) load_q(nw);
-        const int h = cw.h, row0 = cw.u % cw.rts * ROWS;
+        const int h = cw.h, row0 = (cw.u - h * cw.rts) * ROWS;
+        // ---- q of the unit's rows as two int8 limbs, in fragment order ----
         float rowf[RT];
         int lim[RT], lim_min = INT_MAX;
+        __syncwarp();
 #pragma unroll
         for (int m = 0; m < RT; ++m) {
-            rowf[m] = row_f[m * 8 + g];
-            lim[m] = row_lim[m * 8 + g];
+            const int r = row0 + m * 8 + g, i = r / a.G;
+            const bool valid = i < cw.s.n;
+            // rows past the sequence's see what is there, as zeros
+            lim[m] = valid ? min(max(cw.s.len - cw.s.n + i + 1, 0), cw.s.len) : cw.s.len;
             lim_min = min(lim_min, lim[m]);
+            const uint16_t *qp = a.q + (int64_t)(cw.s.r0 + i) * a.q_stride + (int64_t)(h * a.G + r % a.G) * D + t * 16;
+            uint4 u[D / 64][2];
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    u[c][x] = valid ? __ldg(reinterpret_cast<const uint4 *>(qp + c * 64 + x * 8)) : make_uint4(0, 0, 0, 0);
+            float top = 0.f;
+            bool bad = false;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t w = reinterpret_cast<const uint32_t *>(u[c])[x];
+                    const float f0 = fabsf(__uint_as_float(w << 16)), f1 = fabsf(__uint_as_float(w & 0xFFFF0000u));
+                    top = fmaxf(top, fmaxf(f0, f1));
+                    bad |= !(f0 <= FLT_MAX) || !(f1 <= FLT_MAX);
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 1) != 0;
+            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 2) != 0;
+            const float inv = top >= 0x1p-100f && !bad ? 32512.f / top : 0.f;
+            rowf[m] = bad && lim[m] > 0 ? NAN : top * (1.f / 32512.f) * a.scale_log2;
+            // 16-byte chunk t + 4 c of a key meets entries 64 c + 16 t ..: two
+            // fragments of 8 entries each
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t raw[4] = {u[c][x].x, u[c][x].y, u[c][x].z, u[c][x].w};
+                    uint32_t limb[4] = {0, 0, 0, 0};  // hi and lo of entries 0-3, of 4-7
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const float f = __uint_as_float(y & 1 ? raw[y / 2] & 0xFFFF0000u : raw[y / 2] << 16);
+                        const int v = __float2int_rn(f * inv), vh = (v + 128) >> 8;
+                        limb[y / 4 * 2] |= (uint32_t)(vh & 0xFF) << (8 * (y & 3));
+                        limb[y / 4 * 2 + 1] |= (uint32_t)((v - vh * 256) & 0xFF) << (8 * (y & 3));
+                    }
+                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(qsm + ((m * KS + 2 * c + x) * 32 + lane) * 16),
+                                 "r"(limb[0]), "r"(limb[1]), "r"(limb[2]), "r"(limb[3])
+                                 : "memory");
+                }
         }
-        lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+        lim_min = __reduce_min_sync(0xffffffffu, lim_min);  // (a lane reads back what it wrote itself)
 
         float o[RT][NJ][2], mx[RT], l[RT];
 #pragma unroll
@@ -384,7 +411,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
             for (int j = 0; j < NJ; ++j) o[m][j][0] = o[m][j][1] = 0.f;
         }
 
-        for (int tile = cw.ta + warp; tile < min(cw.tb, cw.seen); tile += kAtWarps) {
+        for (int tile = cw.ta; tile < min(cw.tb, cw.seen); ++tile) {
             asm volatile("cp.async.wait_group %0;" ::"n"(NH - 2) : "memory");
             __syncwarp();
             const bool there = (present >> slot) & 1;
@@ -413,7 +440,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
                     for (int m = 0; m < RT; ++m)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const uint4 u = at_lds16(smem0 + S::kQ + ((m * KS + 2 * c + y) * 32 + lane) * 16);
+                            const uint4 u = at_lds16(qsm + ((m * KS + 2 * c + y) * 32 + lane) * 16);
                             qf[m][y][0] = u.x; qf[m][y][1] = u.y; qf[m][y][2] = u.z; qf[m][y][3] = u.w;
                         }
 #pragma unroll
@@ -537,124 +564,160 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_kv8_attn(const Kv8Attn a)
             slot = slot + 1 == NH ? 0 : slot + 1;
         }
 
-        // ---- join the warps' sums ----
-        // (statistics alternate between two places: the next segment's may be
-        // written while this one's are still read)
-        float *stat_m = reinterpret_cast<float *>(smem + S::kStats) + parity * 2 * kAtWarps * ROWS;
-        float *stat_l = stat_m + kAtWarps * ROWS;
-        parity ^= 1;
+        // ---- the segment's end: out, or a part of a cut unit ----
+        const bool from = cw.ta == 0, to = cw.tb == cw.tiles;
+        AttnWalk nw = cw;
+        const bool more = at_next<RT>(nw, a);
+        const int part = 2 * warp + (from ? 1 : 0);
+        if (!more) asm volatile("cp.async.wait_group 0;" ::: "memory");  // the ring may take the tail
+        __syncwarp();
 #pragma unroll
         for (int m = 0; m < RT; ++m) {
             l[m] += __shfl_xor_sync(0xffffffffu, l[m], 1);
             l[m] += __shfl_xor_sync(0xffffffffu, l[m], 2);
-            if (t == 0) {
-                stat_m[warp * ROWS + m * 8 + g] = mx[m];
-                stat_l[warp * ROWS + m * 8 + g] = l[m];
-            }
-        }
-        __syncthreads();
-        const bool whole = cw.ta == 0 && cw.tb == cw.tiles;
-        const int part = 2 * blockIdx.x + (cw.ta == 0 ? 1 : 0);
+            if (from && to) {
+                const int r = row0 + m * 8 + g, ri = r / a.G;
+                if (ri < cw.s.n) {
+                    const float inv = l[m] == 0.f ? 0.f : 1.f / l[m];
+                    uint16_t *op = a.out + (int64_t)(cw.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D + t * (D / 4);
 #pragma unroll
-        for (int m = 0; m < RT; ++m) {
-            if (m > 0) __syncthreads();  // the sums of the rows before are read
-            {
-                const int row = m * 8 + g;
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, stat_m[w * ROWS + row]);
-                const float f = at_exp2(mx[m] - at_ref(top));
-                float4 *dst = reinterpret_cast<float4 *>(merge + (warp * 8 + g) * D + t * (D / 4));
-                const int sw = D == 128 ? (g & 1) * 4 + t : (g & 1) * 2 + (t >> 1);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int e = i / (D / 32), j = 4 * (i % (D / 32));
+                        at_store4(op + 4 * i, o[m][j][e] * inv, o[m][j + 1][e] * inv, o[m][j + 2][e] * inv, o[m][j + 3][e] * inv);
+                    }
+                }
+            } else {
+                float4 *dst = reinterpret_cast<float4 *>(from ? smem + warp * NH * S::kHalf : smem + S::kHead + warp * S::kPart) +
+                              (m * 8 + g) * (D / 4);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
                     // entries 4 i .. 4 i + 3 of the thread's D / 4 consecutive ones
                     const int e = i / (D / 32), j = 4 * (i % (D / 32));
-                    dst[i ^ sw] = make_float4(o[m][j][e] * f, o[m][j + 1][e] * f, o[m][j + 2][e] * f, o[m][j + 3][e] * f);
+                    dst[at_piece<D>(g, t, i)] = make_float4(o[m][j][e], o[m][j + 1][e], o[m][j + 2][e], o[m][j + 3][e]);
                 }
-            }
-            if (m == 0 && more) store_q(nw);  // every warp is done with this segment's
-            __syncthreads();
-            if (tid < 8 * D / 4) {
-                const int r8 = tid / (D / 4), row = m * 8 + r8, d4 = tid % (D / 4), tt = d4 / (D / 16), x = d4 % (D / 16);
-                const int sw = D == 128 ? (r8 & 1) * 4 + tt : (r8 & 1) * 2 + (tt >> 1);
-                float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, stat_m[w * ROWS + row]);
-                float sum = 0.f;
-                float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kAtWarps; ++w) {
-                    sum += stat_l[w * ROWS + row] * at_exp2(stat_m[w * ROWS + row] - at_ref(top));
-                    const float4 v = reinterpret_cast<const float4 *>(merge + (w * 8 + r8) * D + tt * (D / 4))[x ^ sw];
-                    acc4.x += v.x; acc4.y += v.y; acc4.z += v.z; acc4.w += v.w;
-                }
-                if (whole) {
-                    const int r = row0 + row, ri = r / a.G;
-                    if (ri < cw.s.n) {
-                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                        uint16_t *op = a.out + (int64_t)(cw.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D;
-                        uint2 pk;
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.x) : "f"(acc4.y * inv), "f"(acc4.x * inv));
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.y) : "f"(acc4.w * inv), "f"(acc4.z * inv));
-                        reinterpret_cast<uint2 *>(op)[d4] = pk;
-                    }
-                } else {
-                    reinterpret_cast<float4 *>(a.part_o + ((int64_t)part * ROWS + row) * D)[d4] = acc4;
-                    if (d4 == 0)
-                        reinterpret_cast<float2 *>(a.part_ml)[(int64_t)part * ROWS + row] = make_float2(top, sum);
+                if (t == 0) {
+                    stat_m[part * ROWS + m * 8 + g] = mx[m];
+                    stat_l[part * ROWS + m * 8 + g] = l[m];
                 }
             }
         }
-        if (!whole) {
-            // the CTAs that share the unit: its first tile's to its last's
-            const int64_t u0 = wpos - cw.ta, u1 = u0 + cw.tiles - 1;
-            const int c0 = (int)(((u0 + 1) * C - 1) / total), c1 = (int)(((u1 + 1) * C - 1) / total);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const bool last = atomicAdd(a.counters + c0, 1u) == (unsigned)(c1 - c0);
-                if (last) a.counters[c0] = 0;
-                __threadfence();
-                sh_last = last;
-            }
-            __syncthreads();
-            if (sh_last) {
-                const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-                for (int i = tid; i < ROWS * D / 4; i += kAtThreads) {
-                    const int row = i / (D / 4), d4 = i % (D / 4);
-                    const int r = row0 + row, ri = r / a.G;
-                    if (ri >= cw.s.n) continue;
-                    // parts in CTA order: the first CTA's holds the unit's start
-                    float top = -INFINITY;
-                    for (int c = c0; c <= c1; ++c)
-                        top = fmaxf(top, __ldcg(&ml[(int64_t)(2 * c + (c == c0)) * ROWS + row]).x);
-                    const float ref = at_ref(top);
-                    float sum = 0.f;
-                    float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const int64_t pr = (int64_t)(2 * c + (c == c0)) * ROWS + row;
-                        const float2 x = __ldcg(&ml[pr]);
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + pr * D) + d4);
-                        const float f = at_exp2(x.x - ref);
-                        sum += x.y * f;
-                        acc4.x += v.x * f; acc4.y += v.y * f; acc4.z += v.z * f; acc4.w += v.w * f;
-                    }
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    uint16_t *op = a.out + (int64_t)(cw.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D;
-                    uint2 pk;
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.x) : "f"(acc4.y * inv), "f"(acc4.x * inv));
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk.y) : "f"(acc4.w * inv), "f"(acc4.z * inv));
-                    reinterpret_cast<uint2 *>(op)[d4] = pk;
-                }
-            }
+        if (!(from && to) && lane == 0) {
+            part_b[part] = cw.b;
+            part_u[part] = cw.u;
+            part_start[part] = wpos - cw.ta;
         }
-        wpos += cw.tb - cw.ta;
         if (!more) break;
+        wpos += cw.tb - cw.ta;
         cw = nw;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+
+    // ---- join the parts of units cut between warps ----
+    if (tid == 0) {
+        int n = 0;
+        int64_t last = -1;
+        for (int p = 0; p < 2 * W; ++p) {
+            if (part_b[p] < 0) continue;
+            if (n == 0 || part_start[p] != last) {
+                group_first[n] = p;
+                group_n[n++] = 0;
+                last = part_start[p];
+            }
+            ++group_n[n - 1];
+        }
+        groups = n;
+    }
+    __syncthreads();
+    // parts of a unit lie in order: the tail of the warp it starts in, then heads
+    auto part_sums = [&](int p) -> const float4 * {
+        return reinterpret_cast<const float4 *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart);
+    };
+    for (int x = tid; x < groups * ROWS * (D / 4); x += S::kThreads) {
+        const int gi = x / (ROWS * (D / 4)), row = x / (D / 4) % ROWS, d4 = x % (D / 4);
+        const int p0 = group_first[gi], n = group_n[gi];
+        AttnWalk w;
+        at_sequence<RT>(w, a, part_b[p0]);
+        const int u = part_u[p0], at = at_piece<D>(row, d4 / (D / 16), d4 % (D / 16));
+        float top = -INFINITY;
+        for (int q = 0, p = p0; q < n; ++q, p += p & 1 ? 1 : 2) top = fmaxf(top, stat_m[p * ROWS + row]);
+        const float ref = at_ref(top);
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0, p = p0; q < n; ++q, p += p & 1 ? 1 : 2) {
+            const float f = at_exp2(stat_m[p * ROWS + row] - ref);
+            const float4 v = part_sums(p)[row * (D / 4) + at];
+            sum += stat_l[p * ROWS + row] * f;
+            o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+        }
+        const int64_t us = part_start[p0];
+        if (us >= w0 && us + w.tiles <= w1) {
+            const int h = u / w.rts, r = (u - h * w.rts) * ROWS + row, ri = r / a.G;
+            if (ri < w.s.n) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                at_store4(a.out + (int64_t)(w.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D + d4 * 4, o.x * inv,
+                          o.y * inv, o.z * inv, o.w * inv);
+            }
+        } else {
+            // the CTA's part: 0 of a unit that started before its range, else 1
+            const int64_t pr = (2 * (int64_t)blockIdx.x + (us >= w0 ? 1 : 0)) * ROWS + row;
+            reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
+            if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(top, sum);
+        }
+    }
+    // ---- join the parts of units cut between CTAs: the first and the last group ----
+    for (int k = 0; k < 2; ++k) {
+        const int gi = k == 0 ? 0 : groups - 1;
+        if (groups == 0 || (k == 1 && groups == 1)) break;
+        const int p0 = group_first[gi];
+        const int64_t us = part_start[p0];
+        AttnWalk w;
+        at_sequence<RT>(w, a, part_b[p0]);
+        if (us >= w0 && us + w.tiles <= w1) continue;
+        // the CTAs that share the unit: its first tile's to its last's
+        const int c0 = (int)(((us + 1) * C - 1) / total), c1 = (int)(((us + w.tiles) * C - 1) / total);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            const bool last = atomicAdd(a.counters + c0, 1u) == (unsigned)(c1 - c0);
+            if (last) a.counters[c0] = 0;
+            __threadfence();
+            sh_last = last;
+        }
+        __syncthreads();
+        if (!sh_last) continue;
+        // parts in CTA order; the first CTA's holds the unit's start.  Their
+        // statistics first (over the q fragments, no longer needed)
+        const int n = c1 - c0 + 1, u = part_u[p0], h = u / w.rts;
+        constexpr int kRoom = W * S::kQBytes / (ROWS * 8);
+        float2 *ml = reinterpret_cast<float2 *>(smem + S::kQ);
+        const float2 *src = reinterpret_cast<const float2 *>(a.part_ml);
+        auto place = [&](int c) { return 2 * (int64_t)(c0 + c) + (c == 0 ? 1 : 0); };
+        for (int x = tid; x < min(n, kRoom) * ROWS; x += S::kThreads)
+            ml[x] = __ldcg(src + place(x / ROWS) * ROWS + x % ROWS);
+        __syncthreads();
+        auto stat = [&](int c, int row) { return c < kRoom ? ml[c * ROWS + row] : __ldcg(src + place(c) * ROWS + row); };
+        for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
+            const int row = x / (D / 4), d4 = x % (D / 4), r = (u - h * w.rts) * ROWS + row, ri = r / a.G;
+            if (ri >= w.s.n) continue;
+            float top = -INFINITY;
+            for (int c = 0; c < n; ++c) top = fmaxf(top, stat(c, row).x);
+            const float ref = at_ref(top);
+            float sum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int c = 0; c < n; ++c) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (place(c) * ROWS + row) * D) + d4);
+                const float2 s = stat(c, row);
+                const float f = at_exp2(s.x - ref);
+                sum += s.y * f;
+                o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            at_store4(a.out + (int64_t)(w.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D + d4 * 4, o.x * inv, o.y * inv,
+                      o.z * inv, o.w * inv);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -697,17 +760,19 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     // (each tile of keys and values is then read for twice the rows)
     const bool one = (int64_t)b.n_rows * a.G <= 8 * (int64_t)b.n_seqs;
     void (*kern)(const Kv8Attn);
-    int smem;
+    int smem, threads;
     if (c.head_dim == 128) {
         kern = one ? k_kv8_attn<128, 1> : k_kv8_attn<128, 2>;
         smem = one ? AttnShape<128, 1>::kBytes : AttnShape<128, 2>::kBytes;
+        threads = one ? AttnShape<128, 1>::kThreads : AttnShape<128, 2>::kThreads;
     } else {
         kern = one ? k_kv8_attn<64, 1> : k_kv8_attn<64, 2>;
         smem = one ? AttnShape<64, 1>::kBytes : AttnShape<64, 2>::kBytes;
+        threads = one ? AttnShape<64, 1>::kThreads : AttnShape<64, 2>::kThreads;
     }
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return LOWBIT_ERR_CUDA;
-    const cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kAtThreads), smem, st, a);
+    const cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(threads), smem, st, a);
     return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 
