@@ -14,8 +14,8 @@
 //     fixed point the same way (two uint8 limbs, at most 2^-17 of the tile's
 //     largest off), and meet v's codes; the exact int32 sum of a tile is
 //     scaled by v's page scale and the running maximum in fp32.
-// Nothing is converted per cached value but the byte transposition of v (4
-// tokens x 4 entries, 8 PRMT per 16 bytes).
+// Nothing is converted per cached value: a key's bytes are a fragment as they
+// lie, and ldmatrix transposes v's (tokens have to run along a fragment's words).
 //
 // Layout of the work.  A unit is (sequence, cache head, RT * 8 query rows); its
 // tokens come in tiles of 32.  All tiles of all units, in order, are cut into
@@ -57,7 +57,8 @@ struct Kv8Attn {
     int64_t q_stride, out_stride;
     int G;            // query heads per cache head
     int page_log2;
-    float scale_log2; // scale * log2(e)
+    float scale_log2; // |scale| * log2(e)
+    float limbs;      // 32512 with the sign of scale
     unsigned *counters;   // [CTAs], zero between calls
     float *part_ml;       // [2 CTAs][rows][2]
     float *part_o;        // [2 CTAs][rows][D]
@@ -69,7 +70,8 @@ struct AttnShape {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRows = RT * 8;
     static constexpr int kHalf = kAtTile * D;                              // bytes of a tile's keys, or of its values
-    static constexpr int kPart = kRows * D * 4;                            // a part's sums
+    static constexpr int kPitch = D + 8;                                  // floats per row of a part: no bank conflicts
+    static constexpr int kPart = kRows * kPitch * 4;                       // a part's sums
     static constexpr int kQBytes = RT * D * 16;                            // q fragments of a warp, [RT][D / 32][32] x 16 bytes
     static constexpr int kFixed = kWarps * (kPart + kQBytes + 2 * 2 * kRows * 4);
     static constexpr int kHalves = std::min(6, (int)((224 * 1024 - kFixed) / (kWarps * (kHalf + 4))));
@@ -90,28 +92,37 @@ __device__ __forceinline__ void at_cp4(unsigned dst, const void *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+// FIRST: the sums start at zero.
+template <bool FIRST>
 __device__ __forceinline__ void at_mma_ss(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (FIRST)
+        asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                     : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
+    else
+        asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void at_mma_us(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
+}
+// Bytes of 32 rows x 16 columns, one row address per lane, transposed: {b[0], b[2]}
+// and {b[1], b[3]} are the B fragments (k = row) of columns 0-7 and 8-15.
+__device__ __forceinline__ void at_ldsm_t(uint32_t (&b)[4], unsigned addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+                 : "r"(addr));
 }
 __device__ __forceinline__ uint4 at_lds16(unsigned a)
 {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 at_lds8(unsigned a)
-{
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
     return v;
 }
 __device__ __forceinline__ float at_exp2(float x)
@@ -120,6 +131,8 @@ __device__ __forceinline__ float at_exp2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+constexpr float kAtLog2P = 15.994353436858858f;  // log2(65280): 255 * 256, so that both limbs fit a byte
+
 // x, but 0 for -inf: a reference that -inf may be subtracted from
 __device__ __forceinline__ float at_ref(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -130,6 +143,13 @@ struct AttnWalk {
     int b, u, units, tiles, ta, tb, seen, h;
     Kv8Seq s;
     int rts;  // row tiles of the sequence
+};
+
+// A part of a unit that a warp has less than all tiles of.
+struct AttnPart {
+    int64_t start;  // the unit's first tile, in the whole work
+    int tiles, r0, row0, h, n;
+    bool there;
 };
 
 __device__ __forceinline__ int at_tiles(int len) { return max(1, (len + kAtTile - 1) / kAtTile); }
@@ -193,20 +213,15 @@ __device__ __forceinline__ bool at_next(AttnWalk &w, const Kv8Attn &a)
     return true;
 }
 
-__device__ __forceinline__ void at_store4(uint16_t *p, float x, float y, float z, float w)
+__device__ __forceinline__ uint32_t at_bf16x2(float lo, float hi)
 {
-    uint2 v;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(y), "f"(x));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(w), "f"(z));
-    *reinterpret_cast<uint2 *>(p) = v;
+    uint32_t v;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
 }
-
-// Where the 16-byte piece i of lane group t's quarter of a part's row lies: permuted
-// so that a quarter-warp's stores meet eight different ones.
-template <int D>
-__device__ __forceinline__ int at_piece(int row, int t, int i)
+__device__ __forceinline__ void at_store4(uint16_t *p, const float4 &v, float f)
 {
-    return t * (D / 16) + (i ^ (D == 128 ? (row & 1) * 4 + t : (row & 1) * 2 + (t >> 1)));
+    *reinterpret_cast<uint2 *>(p) = make_uint2(at_bf16x2(v.x * f, v.y * f), at_bf16x2(v.z * f, v.w * f));
 }
 
 template <int D, int RT>
@@ -218,11 +233,9 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     __shared__ int64_t sh_sum[W], sh_units[W];
     __shared__ int64_t sh_off;
     __shared__ int sh_b, sh_last;
-    // a warp's cut units: sequence, unit, place of the unit's start in the whole
-    // work; of its parts the head is 2 warp, the tail 2 warp + 1
-    __shared__ int part_b[2 * W], part_u[2 * W];
-    __shared__ int64_t part_start[2 * W];
-    __shared__ int group_first[2 * W], group_n[2 * W], groups;
+    // a warp's parts of cut units: the head is 2 warp, the tail 2 warp + 1
+    __shared__ AttnPart parts[2 * W];
+    __shared__ int group_first[W + 1], group_n[W + 1], groups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         sh_sum[warp] = incl;
         sh_units[warp] = units;
     }
-    if (tid < 2 * W) part_b[tid] = -1;
+    if (tid < 2 * W) parts[tid].there = false;
     __syncthreads();
     int64_t total = 0, before = 0;
     units = 0;
@@ -293,7 +306,10 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     constexpr int CH = D / 16;
     const int prow = lane / CH, pch = lane % CH;
     const unsigned kdst = D == 128 ? prow * 128 + ((pch ^ (4 * (prow & 1))) << 4) : (prow >> 1) * 128 + (((prow & 1) * 4 + pch) << 4);
-    const unsigned vdst = D == 128 ? prow * 128 + (pch << 4) : (prow >> 1) * 128 + (((prow & 1) * 4 + pch) << 4);
+    const unsigned vdst = D == 128 ? prow * 128 + ((pch ^ prow) << 4)
+                                   : (prow >> 1) * 128 + (((prow & 1) * 4 + (pch ^ (prow >> 1))) << 4);
+    // this lane's row of a tile's values, for the transposing loads
+    const unsigned vrow = D == 128 ? lane * 128 + ((lane & 7) << 4) : (lane >> 1) * 128 + (lane & 1) * 64 + (((lane >> 1) & 3) << 4);
     AttnWalk ld = cw;
     int ld_tile = ld.ta, ld_slot = 0;
     bool ld_more = true, ld_value = false;
@@ -324,13 +340,9 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
             const unsigned st = ring + ld_slot * S::kHalf;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                // rows advance by 32 / CH: 4 (D = 128) or 8 (two lines by two)
-                if (ld_value) {
-                    const unsigned x = D == 128 ? (unsigned)(2 * (i & 3)) << 4 : (unsigned)(2 * ((2 * i + (prow >> 2)) & 3)) << 4;
-                    at_cp16(st + i * 512 + (vdst ^ x), src + i * 512);
-                } else {
-                    at_cp16(st + i * 512 + kdst, src + i * 512);
-                }
+                // rows advance by 4 (D = 128) or 8
+                const unsigned dst = ld_value ? (D == 128 ? vdst ^ ((i & 1) << 6) : vdst) : kdst;
+                at_cp16(st + i * 512 + dst, src + i * 512);
             }
             if (lane == 0) at_cp4(scal + ld_slot * 4, (ld_value ? a.vs : a.ks) + ld_ph);
         }
@@ -378,7 +390,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 1) != 0;
             bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 2) != 0;
-            const float inv = top >= 0x1p-100f && !bad ? 32512.f / top : 0.f;
+            const float inv = top >= 0x1p-100f && !bad ? a.limbs / top : 0.f;
             rowf[m] = bad && lim[m] > 0 ? NAN : top * (1.f / 32512.f) * a.scale_log2;
             // 16-byte chunk t + 4 c of a key meets entries 64 c + 16 t ..: two
             // fragments of 8 entries each
@@ -428,12 +440,6 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
                 // tokens its probability fragment holds
                 int acc[RT][4][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int m = 0; m < RT; ++m)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) acc[m][j][x] = 0;
-#pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     uint32_t qf[RT][2][4];
 #pragma unroll
@@ -450,37 +456,37 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
                         const uint4 x = at_lds16(st + (D == 128 ? tr : tr >> 1) * 128 + (sl << 4));
 #pragma unroll
                         for (int m = 0; m < RT; ++m) {
-                            at_mma_ss(acc[m][j], qf[m][0], x.x, x.y);
-                            at_mma_ss(acc[m][j], qf[m][1], x.z, x.w);
+                            if (c == 0)
+                                at_mma_ss<true>(acc[m][j], qf[m][0], x.x, x.y);
+                            else
+                                at_mma_ss<false>(acc[m][j], qf[m][0], x.x, x.y);
+                            at_mma_ss<false>(acc[m][j], qf[m][1], x.z, x.w);
                         }
                     }
                 }
                 const bool masked = (tile + 1) * kAtTile > lim_min;
 #pragma unroll
                 for (int m = 0; m < RT; ++m) {
-                    const float f = rowf[m] * ks;
-                    float s[8];
+                    const float f = rowf[m] * ks;  // >= 0: the largest score is the largest integer's
+                    int s[8], top = INT_MIN;
+                    const int tok = tile * kAtTile + 4 * t;
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {  // token 16 (x / 4) + 4 t + x % 4
                         const int j = 2 * (x >> 2) + ((x >> 1) & 1), e = x & 1;
-                        s[x] = (float)(acc[m][j][e] * 256 + acc[m][j][2 + e]) * f;
+                        s[x] = acc[m][j][e] * 256 + acc[m][j][2 + e];
+                        if (!masked || tok + 16 * (x >> 2) + (x & 3) < lim[m]) top = max(top, s[x]);
                     }
-                    if (masked) {
-                        const int tok = tile * kAtTile + 4 * t;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            if (tok + 16 * (x >> 2) + (x & 3) >= lim[m]) s[x] = -INFINITY;
-                    }
-                    float tm = s[0];
-#pragma unroll
-                    for (int x = 1; x < 8; ++x) tm = fmaxf(tm, s[x]);
-                    tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 1));
-                    tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 2));
-                    const float ref = at_ref(tm);
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // the sums of limbs stay above INT_MIN
+                    const float tm = top == INT_MIN ? -INFINITY : (float)top * f;
+                    // probabilities in parts of 1 / 65280 of the tile's largest
+                    const float ref = kAtLog2P - at_ref(tm);
                     uint32_t v[8], sum = 0;
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        v[x] = __float2uint_rn(at_exp2(s[x] - ref) * 65280.f);
+                        v[x] = __float2uint_rn(at_exp2(fmaf((float)s[x], f, ref)));
+                        if (masked && tok + 16 * (x >> 2) + (x & 3) >= lim[m]) v[x] = 0;
                         sum += v[x];
                     }
 #pragma unroll
@@ -519,45 +525,18 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs) : "r"(scal + slot * 4));
 #pragma unroll
                 for (int m = 0; m < RT; ++m) fac[m] *= vs;
-                // products with v: column n of block j is entry (D / 8) n + j
-                constexpr int VW = D / 32;  // words of a token's entries per thread
-                uint32_t x[2][4][VW];
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh)
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t b[4];
+                    at_ldsm_t(b, (vb + vrow) ^ (c << 4));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = 16 * hh + 4 * t + i;
-                        if constexpr (D == 128) {
-                            const uint4 u = at_lds16(vb + row * 128 + ((g ^ (2 * t)) << 4));
-                            x[hh][i][0] = u.x; x[hh][i][1] = u.y; x[hh][i][2] = u.z; x[hh][i][3] = u.w;
-                        } else {
-                            const int sl = (row & 1) * 4 + (g >> 1);
-                            const uint2 u = at_lds8(vb + (row >> 1) * 128 + ((sl ^ (2 * t)) << 4) + (g & 1) * 8);
-                            x[hh][i][0] = u.x; x[hh][i][1] = u.y;
-                        }
-                    }
-#pragma unroll
-                for (int w = 0; w < VW; ++w) {
-                    uint32_t b[2][4];
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const uint32_t t0 = __byte_perm(x[hh][0][w], x[hh][1][w], 0x5140),
-                                       t1 = __byte_perm(x[hh][2][w], x[hh][3][w], 0x5140),
-                                       t2 = __byte_perm(x[hh][0][w], x[hh][1][w], 0x7362),
-                                       t3 = __byte_perm(x[hh][2][w], x[hh][3][w], 0x7362);
-                        b[hh][0] = __byte_perm(t0, t1, 0x5410);
-                        b[hh][1] = __byte_perm(t0, t1, 0x7632);
-                        b[hh][2] = __byte_perm(t2, t3, 0x5410);
-                        b[hh][3] = __byte_perm(t2, t3, 0x7632);
-                    }
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
+                    for (int y = 0; y < 2; ++y)
 #pragma unroll
                         for (int m = 0; m < RT; ++m) {
-                            int c[4] = {0, 0, 0, 0};
-                            at_mma_us(c, pf[m], b[0][y], b[1][y]);
-                            o[m][4 * w + y][0] = fmaf((float)(c[0] * 256 + c[2]), fac[m], o[m][4 * w + y][0]);
-                            o[m][4 * w + y][1] = fmaf((float)(c[1] * 256 + c[3]), fac[m], o[m][4 * w + y][1]);
+                            int p[4];
+                            at_mma_us(p, pf[m], b[y], b[2 + y]);
+                            o[m][2 * c + y][0] = fmaf((float)(p[0] * 256 + p[2]), fac[m], o[m][2 * c + y][0]);
+                            o[m][2 * c + y][1] = fmaf((float)(p[1] * 256 + p[3]), fac[m], o[m][2 * c + y][1]);
                         }
                 }
             }
@@ -579,33 +558,23 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
                 const int r = row0 + m * 8 + g, ri = r / a.G;
                 if (ri < cw.s.n) {
                     const float inv = l[m] == 0.f ? 0.f : 1.f / l[m];
-                    uint16_t *op = a.out + (int64_t)(cw.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D + t * (D / 4);
+                    uint16_t *op = a.out + (int64_t)(cw.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D + 2 * t;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const int e = i / (D / 32), j = 4 * (i % (D / 32));
-                        at_store4(op + 4 * i, o[m][j][e] * inv, o[m][j + 1][e] * inv, o[m][j + 2][e] * inv, o[m][j + 3][e] * inv);
-                    }
+                    for (int j = 0; j < NJ; ++j)
+                        *reinterpret_cast<uint32_t *>(op + 8 * j) = at_bf16x2(o[m][j][0] * inv, o[m][j][1] * inv);
                 }
             } else {
-                float4 *dst = reinterpret_cast<float4 *>(from ? smem + warp * NH * S::kHalf : smem + S::kHead + warp * S::kPart) +
-                              (m * 8 + g) * (D / 4);
+                float *dst = reinterpret_cast<float *>(from ? smem + warp * NH * S::kHalf : smem + S::kHead + warp * S::kPart) +
+                             (m * 8 + g) * S::kPitch + 2 * t;
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    // entries 4 i .. 4 i + 3 of the thread's D / 4 consecutive ones
-                    const int e = i / (D / 32), j = 4 * (i % (D / 32));
-                    dst[at_piece<D>(g, t, i)] = make_float4(o[m][j][e], o[m][j + 1][e], o[m][j + 2][e], o[m][j + 3][e]);
-                }
+                for (int j = 0; j < NJ; ++j) *reinterpret_cast<float2 *>(dst + 8 * j) = make_float2(o[m][j][0], o[m][j][1]);
                 if (t == 0) {
                     stat_m[part * ROWS + m * 8 + g] = mx[m];
                     stat_l[part * ROWS + m * 8 + g] = l[m];
                 }
             }
         }
-        if (!(from && to) && lane == 0) {
-            part_b[part] = cw.b;
-            part_u[part] = cw.u;
-            part_start[part] = wpos - cw.ta;
-        }
+        if (!(from && to) && lane == 0) parts[part] = AttnPart{wpos - cw.ta, cw.tiles, cw.s.r0, row0, h, cw.s.n, true};
         if (!more) break;
         wpos += cw.tb - cw.ta;
         cw = nw;
@@ -614,31 +583,38 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     __syncthreads();
 
     // ---- join the parts of units cut between warps ----
-    if (tid == 0) {
-        int n = 0;
-        int64_t last = -1;
-        for (int p = 0; p < 2 * W; ++p) {
-            if (part_b[p] < 0) continue;
-            if (n == 0 || part_start[p] != last) {
-                group_first[n] = p;
-                group_n[n++] = 0;
-                last = part_start[p];
-            }
-            ++group_n[n - 1];
+    // Parts of a unit lie in order: the tail of the warp it starts in (or the head
+    // of the CTA's first), then the heads of the following ones.
+    if (warp == 0) {
+        const unsigned heads = __ballot_sync(0xffffffffu, lane < W && parts[min(lane, W - 1) * 2].there);
+        const unsigned tails = __ballot_sync(0xffffffffu, lane < W && parts[min(lane, W - 1) * 2 + 1].there);
+        const int before = (int)(heads & 1);
+        const bool from_head = lane == 31 && before;  // an idle lane takes the first head's group
+        if (from_head || (tails >> lane & 1)) {
+            int w = from_head ? 0 : lane, n = 1;
+            if (!(from_head && (tails & 1)))
+                while (heads >> (w + 1) & 1) {
+                    ++n;
+                    if (tails >> ++w & 1) break;
+                }
+            const int gi = from_head ? 0 : before + __popc(tails & ((1u << lane) - 1));
+            group_first[gi] = from_head ? 0 : 2 * lane + 1;
+            group_n[gi] = n;
         }
-        groups = n;
+        if (lane == 0) groups = before + __popc(tails);
     }
     __syncthreads();
-    // parts of a unit lie in order: the tail of the warp it starts in, then heads
-    auto part_sums = [&](int p) -> const float4 * {
-        return reinterpret_cast<const float4 *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart);
+    auto part_sums = [&](int p) {
+        return reinterpret_cast<const float *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart);
+    };
+    auto out_at = [&](const AttnPart &u, int row, int d4) -> uint16_t * {  // null past the sequence's rows
+        const int r = u.row0 + row, ri = r / a.G;
+        return ri < u.n ? a.out + (int64_t)(u.r0 + ri) * a.out_stride + (int64_t)(u.h * a.G + r % a.G) * D + d4 * 4 : nullptr;
     };
     for (int x = tid; x < groups * ROWS * (D / 4); x += S::kThreads) {
         const int gi = x / (ROWS * (D / 4)), row = x / (D / 4) % ROWS, d4 = x % (D / 4);
         const int p0 = group_first[gi], n = group_n[gi];
-        AttnWalk w;
-        at_sequence<RT>(w, a, part_b[p0]);
-        const int u = part_u[p0], at = at_piece<D>(row, d4 / (D / 16), d4 % (D / 16));
+        const AttnPart u = parts[p0];
         float top = -INFINITY;
         for (int q = 0, p = p0; q < n; ++q, p += p & 1 ? 1 : 2) top = fmaxf(top, stat_m[p * ROWS + row]);
         const float ref = at_ref(top);
@@ -646,21 +622,15 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int q = 0, p = p0; q < n; ++q, p += p & 1 ? 1 : 2) {
             const float f = at_exp2(stat_m[p * ROWS + row] - ref);
-            const float4 v = part_sums(p)[row * (D / 4) + at];
+            const float4 v = *reinterpret_cast<const float4 *>(part_sums(p) + row * S::kPitch + d4 * 4);
             sum += stat_l[p * ROWS + row] * f;
             o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
         }
-        const int64_t us = part_start[p0];
-        if (us >= w0 && us + w.tiles <= w1) {
-            const int h = u / w.rts, r = (u - h * w.rts) * ROWS + row, ri = r / a.G;
-            if (ri < w.s.n) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                at_store4(a.out + (int64_t)(w.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D + d4 * 4, o.x * inv,
-                          o.y * inv, o.z * inv, o.w * inv);
-            }
+        if (u.start >= w0 && u.start + u.tiles <= w1) {
+            if (uint16_t *op = out_at(u, row, d4)) at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
         } else {
             // the CTA's part: 0 of a unit that started before its range, else 1
-            const int64_t pr = (2 * (int64_t)blockIdx.x + (us >= w0 ? 1 : 0)) * ROWS + row;
+            const int64_t pr = (2 * (int64_t)blockIdx.x + (u.start >= w0 ? 1 : 0)) * ROWS + row;
             reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
             if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(top, sum);
         }
@@ -669,13 +639,10 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     for (int k = 0; k < 2; ++k) {
         const int gi = k == 0 ? 0 : groups - 1;
         if (groups == 0 || (k == 1 && groups == 1)) break;
-        const int p0 = group_first[gi];
-        const int64_t us = part_start[p0];
-        AttnWalk w;
-        at_sequence<RT>(w, a, part_b[p0]);
-        if (us >= w0 && us + w.tiles <= w1) continue;
+        const AttnPart u = parts[group_first[gi]];
+        if (u.start >= w0 && u.start + u.tiles <= w1) continue;
         // the CTAs that share the unit: its first tile's to its last's
-        const int c0 = (int)(((us + 1) * C - 1) / total), c1 = (int)(((us + w.tiles) * C - 1) / total);
+        const int c0 = (int)(((u.start + 1) * C - 1) / total), c1 = (int)(((u.start + u.tiles) * C - 1) / total);
         __threadfence();
         __syncthreads();
         if (tid == 0) {
@@ -688,7 +655,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         if (!sh_last) continue;
         // parts in CTA order; the first CTA's holds the unit's start.  Their
         // statistics first (over the q fragments, no longer needed)
-        const int n = c1 - c0 + 1, u = part_u[p0], h = u / w.rts;
+        const int n = c1 - c0 + 1;
         constexpr int kRoom = W * S::kQBytes / (ROWS * 8);
         float2 *ml = reinterpret_cast<float2 *>(smem + S::kQ);
         const float2 *src = reinterpret_cast<const float2 *>(a.part_ml);
@@ -698,8 +665,9 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         __syncthreads();
         auto stat = [&](int c, int row) { return c < kRoom ? ml[c * ROWS + row] : __ldcg(src + place(c) * ROWS + row); };
         for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
-            const int row = x / (D / 4), d4 = x % (D / 4), r = (u - h * w.rts) * ROWS + row, ri = r / a.G;
-            if (ri >= w.s.n) continue;
+            const int row = x / (D / 4), d4 = x % (D / 4);
+            uint16_t *op = out_at(u, row, d4);
+            if (!op) continue;
             float top = -INFINITY;
             for (int c = 0; c < n; ++c) top = fmaxf(top, stat(c, row).x);
             const float ref = at_ref(top);
@@ -713,9 +681,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
                 sum += s.y * f;
                 o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            at_store4(a.out + (int64_t)(w.s.r0 + ri) * a.out_stride + (int64_t)(h * a.G + r % a.G) * D + d4 * 4, o.x * inv, o.y * inv,
-                      o.z * inv, o.w * inv);
+            at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
         }
     }
 }
@@ -747,7 +713,8 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
     a.G = q_heads / c.n_heads;
     a.page_log2 = c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    a.limbs = scale < 0.f ? -32512.f : 32512.f;
     const int ctas = attn_ctas();
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.counters = reinterpret_cast<unsigned *>(ws);

@@ -521,7 +521,7 @@ lowbit_status lowbit_rope(const void *q, int64_t q_stride, void *q_out, int64_t 
 /* KV8 cache: keys and values as int8 codes in pages of page_tokens tokens,
  * with one fp32 scale for each page and head; a value is code * scale.
  *   k, v               [n_pages][n_heads][page_tokens][head_dim] int8
- *   k_scales, v_scales [n_pages][n_heads] fp32
+ *   k_scales, v_scales [n_pages][n_heads] fp32, >= 0
  * page_tokens is 32, 64 or 128; head_dim is 64 or 128; n_heads <= 1024;
  * n_pages * n_heads < 2^31.  The buffers may exceed 4 GB. */
 typedef struct {

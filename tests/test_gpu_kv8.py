@@ -200,6 +200,17 @@ def test_attention_several_rows(lb, H, G, D, P, lens, rows):
     check_attention(cache, table, lens, q, 0.1, rs, out)
 
 
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+def test_attention_scale_of_any_sign(lb, n, scale):
+    lens = [100, 70]
+    n_pages, table = make_batch(15, lens, 32)
+    cache = make_cache(lb, 15, n_pages, 2, 32, 64)
+    q = torch.randn((2 * n, 8, 64), device="cuda").bfloat16()
+    out = attend(lb, cache, table, lens, q, scale, starts([n, n]))
+    check_attention(cache, table, lens, q, scale, starts([n, n]), out)
+
+
 @pytest.mark.parametrize("rows", [[1, 1, 1], [300, 200, 90]])
 def test_attention_rows_without_a_place(lb, rows):
     """More rows than tokens: those before the first token see nothing and give zeros."""
