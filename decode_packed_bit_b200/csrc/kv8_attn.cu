@@ -74,7 +74,8 @@ struct AttnShape {
     static constexpr int kPart = kRows * kPitch * 4;                       // a part's sums
     static constexpr int kQBytes = RT * D * 16;                            // q fragments of a warp, [RT][D / 32][32] x 16 bytes
     static constexpr int kFixed = kWarps * (kPart + kQBytes + 2 * 2 * kRows * 4);
-    static constexpr int kHalves = std::min(6, (int)((224 * 1024 - kFixed) / (kWarps * (kHalf + 4))));
+    static constexpr int kFit = (224 * 1024 - kFixed) / (kWarps * (kHalf + 4));
+    static constexpr int kHalves = kFit >= 5 ? 5 : 3;  // odd: what a place in the loop copies is keys, or values, always
     static constexpr int kRing = kWarps * kHalves * kHalf;
     static constexpr int kQ = kRing;
     static constexpr int kHead = kQ + kWarps * kQBytes;                    // sums of a unit cut at the warp's start
@@ -312,46 +313,53 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     const unsigned vrow = D == 128 ? lane * 128 + ((lane & 7) << 4) : (lane >> 1) * 128 + (lane & 1) * 64 + (((lane >> 1) & 3) << 4);
     AttnWalk ld = cw;
     int ld_tile = ld.ta, ld_slot = 0;
-    bool ld_more = true, ld_value = false;
-    int64_t ld_at = 0;   // byte offset of the tile, this lane's first piece
-    int64_t ld_ph = -1;  // its page and head, -1 for an absent page
+    bool ld_more = true;
+    int64_t ld_ph = -1;  // the tile's page and head, -1 for an absent page
+    const int8_t *ld_v = nullptr;  // its values, this lane's first piece
     unsigned present = 0;  // one bit per slot: keys that are there
-    // Copies the next half of a tile (nothing at the end of the range).
-    auto issue = [&]() {
-        if (!ld_value) {
-            while (ld_more && ld_tile >= min(ld.tb, ld.seen)) {
-                ld_more = at_next<RT>(ld, a);
-                ld_tile = ld.ta;
-            }
-            ld_ph = -1;
-            if (ld_more) {
-                const int tok = ld_tile * kAtTile;
-                const int page = kv8_page(a.v, ld.b, tok >> a.page_log2, &g_at_fault);
-                if (page >= 0) {
-                    ld_ph = (int64_t)page * a.v.H + ld.h;
-                    ld_at = ((ld_ph << a.page_log2) + (tok & (a.v.P - 1))) * D + lane * 16;
-                }
-                ++ld_tile;
-            }
-            present = ld_ph >= 0 ? present | (1u << ld_slot) : present & ~(1u << ld_slot);
+    // Copies the next tile's keys (nothing at the end of the range), then its values.
+    auto issue_k = [&]() {
+        while (ld_more && ld_tile >= min(ld.tb, ld.seen)) {
+            ld_more = at_next<RT>(ld, a);
+            ld_tile = ld.ta;
         }
-        if (ld_ph >= 0) {
-            const int8_t *src = (ld_value ? a.vv : a.k) + ld_at;
-            const unsigned st = ring + ld_slot * S::kHalf;
+        ld_ph = -1;
+        present &= ~(1u << ld_slot);
+        if (ld_more) {
+            const int tok = ld_tile * kAtTile;
+            const int page = kv8_page(a.v, ld.b, tok >> a.page_log2, &g_at_fault);
+            ++ld_tile;
+            if (page >= 0) {
+                present |= 1u << ld_slot;
+                ld_ph = (int64_t)page * a.v.H + ld.h;
+                const int64_t at = ((ld_ph << a.page_log2) + (tok & (a.v.P - 1))) * D + lane * 16;
+                const int8_t *src = a.k + at;
+                ld_v = a.vv + at;
+                const unsigned st = ring + ld_slot * S::kHalf + kdst;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                // rows advance by 4 (D = 128) or 8
-                const unsigned dst = ld_value ? (D == 128 ? vdst ^ ((i & 1) << 6) : vdst) : kdst;
-                at_cp16(st + i * 512 + dst, src + i * 512);
+                for (int i = 0; i < D / 16; ++i) at_cp16(st + i * 512, src + i * 512);
+                if (lane == 0) at_cp4(scal + ld_slot * 4, a.ks + ld_ph);
             }
-            if (lane == 0) at_cp4(scal + ld_slot * 4, (ld_value ? a.vs : a.ks) + ld_ph);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        ld_value = !ld_value;
+        ld_slot = ld_slot + 1 == NH ? 0 : ld_slot + 1;
+    };
+    auto issue_v = [&]() {
+        if (ld_ph >= 0) {
+            const unsigned st = ring + ld_slot * S::kHalf + vdst;
+            // rows advance by 4 (D = 128, two permutations in turn) or 8
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) at_cp16((D == 128 && (i & 1) ? st ^ 64 : st) + i * 512, ld_v + i * 512);
+            if (lane == 0) at_cp4(scal + ld_slot * 4, a.vs + ld_ph);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
         ld_slot = ld_slot + 1 == NH ? 0 : ld_slot + 1;
     };
 #pragma unroll 1
-    for (int i = 0; i < NH - 1; ++i) issue();
+    for (int i = 0; i < NH / 2; ++i) {
+        issue_k();
+        issue_v();
+    }
     int slot = 0;
     const unsigned qsm = smem0 + S::kQ + warp * S::kQBytes;
 
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
             asm volatile("cp.async.wait_group %0;" ::"n"(NH - 2) : "memory");
             __syncwarp();
             const bool there = (present >> slot) & 1;
-            issue();  // into the slot read last, while this one is worked on
+            issue_k();  // into the slot read last, while this one is worked on
             uint32_t pf[RT][4];
             float fac[RT], al[RT];
             bool same = true;
@@ -474,8 +482,15 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
                     for (int x = 0; x < 8; ++x) {  // token 16 (x / 4) + 4 t + x % 4
                         const int j = 2 * (x >> 2) + ((x >> 1) & 1), e = x & 1;
                         s[x] = acc[m][j][e] * 256 + acc[m][j][2 + e];
-                        if (!masked || tok + 16 * (x >> 2) + (x & 3) < lim[m]) top = max(top, s[x]);
                     }
+                    if (masked) {
+                        asm volatile("" ::: "memory");  // a branch, not eight selections in every tile
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (tok + 16 * (x >> 2) + (x & 3) >= lim[m]) s[x] = INT_MIN;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) top = max(top, s[x]);
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // the sums of limbs stay above INT_MIN
@@ -486,9 +501,15 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         v[x] = __float2uint_rn(at_exp2(fmaf((float)s[x], f, ref)));
-                        if (masked && tok + 16 * (x >> 2) + (x & 3) >= lim[m]) v[x] = 0;
-                        sum += v[x];
                     }
+                    if (masked) {
+                        asm volatile("" ::: "memory");
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            if (s[x] == INT_MIN) v[x] = 0;  // a small f alone would not make it so
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) sum += v[x];
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         const uint32_t a01 = __byte_perm(v[4 * hh], v[4 * hh + 1], 0x5410),
@@ -518,7 +539,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
             slot = slot + 1 == NH ? 0 : slot + 1;
             asm volatile("cp.async.wait_group %0;" ::"n"(NH - 2) : "memory");
             __syncwarp();
-            issue();
+            issue_v();
             if (there) {
                 const unsigned vb = ring + slot * S::kHalf;
                 float vs;
@@ -643,43 +664,51 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         if (u.start >= w0 && u.start + u.tiles <= w1) continue;
         // the CTAs that share the unit: its first tile's to its last's
         const int c0 = (int)(((u.start + 1) * C - 1) / total), c1 = (int)(((u.start + u.tiles) * C - 1) / total);
-        __threadfence();
-        __syncthreads();
+        __syncthreads();  // the CTA's part is written; the counter's release carries it
         if (tid == 0) {
-            const bool last = atomicAdd(a.counters + c0, 1u) == (unsigned)(c1 - c0);
-            if (last) a.counters[c0] = 0;
-            __threadfence();
-            sh_last = last;
+            unsigned seen;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.counters + c0) : "memory");
+            sh_last = seen == (unsigned)(c1 - c0);
+            if (sh_last) a.counters[c0] = 0;
         }
         __syncthreads();
         if (!sh_last) continue;
-        // parts in CTA order; the first CTA's holds the unit's start.  Their
-        // statistics first (over the q fragments, no longer needed)
+        // parts in CTA order; the first CTA's holds the unit's start.  A batch's
+        // loads are all under way before the first is used.
         const int n = c1 - c0 + 1;
-        constexpr int kRoom = W * S::kQBytes / (ROWS * 8);
-        float2 *ml = reinterpret_cast<float2 *>(smem + S::kQ);
-        const float2 *src = reinterpret_cast<const float2 *>(a.part_ml);
-        auto place = [&](int c) { return 2 * (int64_t)(c0 + c) + (c == 0 ? 1 : 0); };
-        for (int x = tid; x < min(n, kRoom) * ROWS; x += S::kThreads)
-            ml[x] = __ldcg(src + place(x / ROWS) * ROWS + x % ROWS);
-        __syncthreads();
-        auto stat = [&](int c, int row) { return c < kRoom ? ml[c * ROWS + row] : __ldcg(src + place(c) * ROWS + row); };
+        constexpr int kBatch = 16;
+        const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
         for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
             const int row = x / (D / 4), d4 = x % (D / 4);
             uint16_t *op = out_at(u, row, d4);
             if (!op) continue;
-            float top = -INFINITY;
-            for (int c = 0; c < n; ++c) top = fmaxf(top, stat(c, row).x);
-            const float ref = at_ref(top);
-            float sum = 0.f;
+            float top = -INFINITY, sum = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int c = 0; c < n; ++c) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + (place(c) * ROWS + row) * D) + d4);
-                const float2 s = stat(c, row);
-                const float f = at_exp2(s.x - ref);
-                sum += s.y * f;
-                o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+            for (int c = 0; c < n; c += kBatch) {
+                float2 s[kBatch];
+                float4 v[kBatch];
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    if (c + q < n) {
+                        const int64_t pr = (2 * (int64_t)(c0 + c + q) + (c + q == 0 ? 1 : 0)) * ROWS + row;
+                        s[q] = __ldcg(ml + pr);
+                        v[q] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + pr * D) + d4);
+                    }
+                float now = top;
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    if (c + q < n) now = fmaxf(now, s[q].x);
+                const float ref = at_ref(now), f0 = at_exp2(top - ref);
+                sum *= f0;
+                o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+                top = now;
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q)
+                    if (c + q < n) {
+                        const float f = at_exp2(s[q].x - ref);
+                        sum += s[q].y * f;
+                        o.x += v[q].x * f; o.y += v[q].y * f; o.z += v[q].z * f; o.w += v[q].w * f;
+                    }
             }
             at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
         }
