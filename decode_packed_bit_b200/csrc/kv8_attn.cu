@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     __shared__ int sh_b, sh_last;
     // a warp's parts of cut units: the head is 2 warp, the tail 2 warp + 1
     __shared__ AttnPart parts[2 * W];
-    __shared__ int group_first[W + 1], group_n[W + 1], groups;
+    __shared__ int order[2 * W], listed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -604,63 +604,63 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     __syncthreads();
 
     // ---- join the parts of units cut between warps ----
-    // Parts of a unit lie in order: the tail of the warp it starts in (or the head
-    // of the CTA's first), then the heads of the following ones.
+    // The parts there are, in order; a unit's begin with the tail of the warp it
+    // starts in (or with the head of the CTA's first).
     if (warp == 0) {
-        const unsigned heads = __ballot_sync(0xffffffffu, lane < W && parts[min(lane, W - 1) * 2].there);
-        const unsigned tails = __ballot_sync(0xffffffffu, lane < W && parts[min(lane, W - 1) * 2 + 1].there);
-        const int before = (int)(heads & 1);
-        const bool from_head = lane == 31 && before;  // an idle lane takes the first head's group
-        if (from_head || (tails >> lane & 1)) {
-            int w = from_head ? 0 : lane, n = 1;
-            if (!(from_head && (tails & 1)))
-                while (heads >> (w + 1) & 1) {
-                    ++n;
-                    if (tails >> ++w & 1) break;
-                }
-            const int gi = from_head ? 0 : before + __popc(tails & ((1u << lane) - 1));
-            group_first[gi] = from_head ? 0 : 2 * lane + 1;
-            group_n[gi] = n;
+        const bool there = lane < 2 * W && parts[min(lane, 2 * W - 1)].there;
+        const unsigned all = __ballot_sync(0xffffffffu, there);
+        const unsigned begins = __ballot_sync(0xffffffffu, there && ((lane & 1) || lane == 0));
+        if (there) {
+            const unsigned later = all & ~((2u << lane) - 1);
+            const bool ends = !later || (begins >> (__ffs(later) - 1) & 1);
+            order[__popc(all & ((1u << lane) - 1))] = lane | (begins >> lane & 1 ? 64 : 0) | (ends ? 128 : 0);
         }
-        if (lane == 0) groups = before + __popc(tails);
+        if (lane == 0) listed = __popc(all);
     }
     __syncthreads();
-    auto part_sums = [&](int p) {
-        return reinterpret_cast<const float *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart);
-    };
     auto out_at = [&](const AttnPart &u, int row, int d4) -> uint16_t * {  // null past the sequence's rows
         const int r = u.row0 + row, ri = r / a.G;
         return ri < u.n ? a.out + (int64_t)(u.r0 + ri) * a.out_stride + (int64_t)(u.h * a.G + r % a.G) * D + d4 * 4 : nullptr;
     };
-    for (int x = tid; x < groups * ROWS * (D / 4); x += S::kThreads) {
-        const int gi = x / (ROWS * (D / 4)), row = x / (D / 4) % ROWS, d4 = x % (D / 4);
-        const int p0 = group_first[gi], n = group_n[gi];
-        const AttnPart u = parts[p0];
-        float top = -INFINITY;
-        for (int q = 0, p = p0; q < n; ++q, p += p & 1 ? 1 : 2) top = fmaxf(top, stat_m[p * ROWS + row]);
-        const float ref = at_ref(top);
-        float sum = 0.f;
+    const int parts_n = listed;
+    for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
+        const int row = x / (D / 4), d4 = x % (D / 4);
+        float top = -INFINITY, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q = 0, p = p0; q < n; ++q, p += p & 1 ? 1 : 2) {
-            const float f = at_exp2(stat_m[p * ROWS + row] - ref);
-            const float4 v = *reinterpret_cast<const float4 *>(part_sums(p) + row * S::kPitch + d4 * 4);
-            sum += stat_l[p * ROWS + row] * f;
-            o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
-        }
-        if (u.start >= w0 && u.start + u.tiles <= w1) {
-            if (uint16_t *op = out_at(u, row, d4)) at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
-        } else {
-            // the CTA's part: 0 of a unit that started before its range, else 1
-            const int64_t pr = (2 * (int64_t)blockIdx.x + (u.start >= w0 ? 1 : 0)) * ROWS + row;
-            reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
-            if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(top, sum);
+#pragma unroll 4
+        for (int k = 0; k < parts_n; ++k) {
+            const int p = order[k] & 63;
+            const float m = stat_m[p * ROWS + row], l = stat_l[p * ROWS + row];
+            const float4 v = *reinterpret_cast<const float4 *>(
+                reinterpret_cast<const float *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart) +
+                row * S::kPitch + d4 * 4);
+            if (order[k] & 64) {
+                top = m;
+                sum = l;
+                o = v;
+            } else {
+                const float now = fmaxf(top, m), ref = at_ref(now), f0 = at_exp2(top - ref), f1 = at_exp2(m - ref);
+                top = now;
+                sum = sum * f0 + l * f1;
+                o.x = o.x * f0 + v.x * f1; o.y = o.y * f0 + v.y * f1; o.z = o.z * f0 + v.z * f1; o.w = o.w * f0 + v.w * f1;
+            }
+            if (order[k] & 128) {
+                const AttnPart &u = parts[p];
+                if (u.start >= w0 && u.start + u.tiles <= w1) {
+                    if (uint16_t *op = out_at(u, row, d4)) at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
+                } else {
+                    // the CTA's part: 0 of a unit that started before its range, else 1
+                    const int64_t pr = (2 * (int64_t)blockIdx.x + (u.start >= w0 ? 1 : 0)) * ROWS + row;
+                    reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
+                    if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(top, sum);
+                }
+            }
         }
     }
-    // ---- join the parts of units cut between CTAs: the first and the last group ----
-    for (int k = 0; k < 2; ++k) {
-        const int gi = k == 0 ? 0 : groups - 1;
-        if (groups == 0 || (k == 1 && groups == 1)) break;
-        const AttnPart u = parts[group_first[gi]];
+    // ---- join the parts of units cut between CTAs: the first and the last unit ----
+    for (int k = 0; k < 2 && parts_n > 0; ++k) {
+        const AttnPart u = parts[order[k == 0 ? 0 : parts_n - 1] & 63];
+        if (k == 1 && u.start == parts[order[0] & 63].start) break;
         if (u.start >= w0 && u.start + u.tiles <= w1) continue;
         // the CTAs that share the unit: its first tile's to its last's
         const int c0 = (int)(((u.start + 1) * C - 1) / total), c1 = (int)(((u.start + u.tiles) * C - 1) / total);
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         // parts in CTA order; the first CTA's holds the unit's start.  A batch's
         // loads are all under way before the first is used.
         const int n = c1 - c0 + 1;
-        constexpr int kBatch = 16;
+        constexpr int kBatch = 20;
         const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
         for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
             const int row = x / (D / 4), d4 = x % (D / 4);
