@@ -1,0 +1,580 @@
+// kv8_attn_tc.cu -- attention of many rows per sequence (prompts) over the KV8
+// cache, on the 5th-generation tensor cores (tcgen05.mma kind::f16).
+//
+// out[r] = sum_t softmax_t(scale q[r] . k[t]) v[t], t up to the row's position,
+// in one pass with a running maximum and sum per row.  Both products take the
+// cache's codes as f16, which holds them exactly:
+//   - a row of q is scaled by a power of two to its own largest value and becomes
+//     f16: its bf16 mantissa fits, and entries below 2^-14 of the largest are off
+//     by 2^-25 of it at most.  S = Q K^T is then exact but for fp32 sums; the
+//     row's power, the softmax scale and k's page scale multiply S.
+//   - v's page scale goes into the exponent: with x = s + log2(vs) a probability
+//     is exp2(x - m), m a running maximum of x, so P fits f16 (at most 2^8, off by
+//     2^-12 of itself) for any scales, O sums P times codes, and the row sum takes
+//     P / vs in fp32.
+// m follows the true maximum only when that is more than 8 ahead, which after
+// the first tiles is rare: only then O is rescaled in tensor memory.
+//
+// A CTA takes two tiles of up to 128 rows (query tokens x the query heads that
+// share a cache head) of one sequence and cache head, which share K and V:
+//   warps 0-3, 4-7  softmax of tile 0, 1: a thread has a row, so its maximum and
+//                   sum need no exchange; S is read from tensor memory twice, 32
+//                   columns at a time, and P goes over S's place there;
+//   warps 8-11      turn codes into f16 in shared memory (K-major keys, MN-major
+//                   values, 128-byte swizzle), the next tile's codes under way in
+//                   registers;
+//   warp 12         allocates tensor memory and issues the MMAs, one tile's
+//                   products while the other tile is in its softmax.
+// Bound by the exponentials (16 a clock and SM) and the tensor cores alike: 128
+// x 128 scores take about 1024 clocks of either at D = 128.
+// Every mbarrier wait is bounded in time; one that runs out records a fault and
+// the CTA leaves its loops, releases tensor memory and exits.
+#include <algorithm>
+#include <cfloat>
+
+#include "kv8_common.cuh"
+#include "tc_common.cuh"
+
+namespace lowbit {
+
+__device__ unsigned g_att_range;  // a length, page or row was out of range
+__device__ unsigned g_att_fault;  // a bounded wait ran out
+
+constexpr int kAttRows = 128;    // rows of a tile
+constexpr int kAttTokens = 128;  // tokens of a step
+constexpr int kAttConvWarp = 8, kAttMmaWarp = 12;
+constexpr int kAttThreads = 13 * 32;
+constexpr int kAttInfo = 4;  // steps of scales kept
+
+struct Kv8AttnTc {
+    Kv8View v;
+    const int8_t *k, *vv;
+    const float *ks, *vs;
+    const uint16_t *q;
+    uint16_t *out;
+    int64_t q_stride, out_stride;
+    int G, tokens;     // query heads per cache head; tokens of a tile: 128 / G
+    int page_log2, items;
+    float scale_log2;  // |scale| * log2(e)
+    float sign;        // of scale
+};
+
+template <int D>
+struct AttnTc {
+    static constexpr int kHalves = D / 64;                 // 64 entries are a 128-byte row
+    static constexpr int kTile = kHalves * 128 * 128;      // bytes of 128 rows of f16
+    static constexpr int kQ = 0;                           // [2]
+    static constexpr int kK = 2 * kTile;                   // [2 stages]
+    static constexpr int kV = 4 * kTile;                   // [2 stages]
+    static constexpr int kInfoAt = 6 * kTile;              // [kAttInfo][4 chunks] {ks or -1, log2 vs, 1 / vs, vs != 0}
+    static constexpr int kBars = kInfoAt + kAttInfo * 4 * 16;
+    static constexpr int kBytes = kBars + 16 * 8 + 16 + 1024;
+    static constexpr unsigned kTmem = 512;                 // S 0, S 1, O 0, O 1
+};
+
+// Shared-memory descriptors, 128-byte swizzle.  K-major: rows 128 bytes apart,
+// 8-row groups 1024.
+__device__ __forceinline__ uint64_t att_desc_k(unsigned addr)
+{
+    return ((uint64_t)(addr >> 4) & 0x3FFFull) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// MN-major: 64 entries of MN a row of 128 bytes, rows (k) 128 bytes apart, 8-row
+// groups 1024, the next 64 entries 16384 on.
+__device__ __forceinline__ uint64_t att_desc_mn(unsigned addr)
+{
+    return ((uint64_t)(addr >> 4) & 0x3FFFull) | (1024ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <bool ACC>
+__device__ __forceinline__ void att_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
+}
+__device__ __forceinline__ void att_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+__device__ __forceinline__ void att_ld32(uint32_t addr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void att_st32(uint32_t addr, const uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void att_st16(uint32_t addr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void att_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void att_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float att_exp2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t att_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four int8 codes -> two words of exact f16: 0x6400 + u is 1024 + u for a byte u,
+// and u = code + 128.
+__device__ __forceinline__ uint2 att_codes(uint32_t w)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(b) : "r"(0x64806480u));
+    return make_uint2(a, b);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc a)
+{
+    using S = AttnTc<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const unsigned smem0 = smem_u32(smem);
+    float4 *info = reinterpret_cast<float4 *>(smem + S::kInfoAt);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
+    uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6;
+    uint64_t *sfull = bars + 8, *pready = bars + 10, *pvdone = bars + 12, *done = bars + 14;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    // ---- the unit: later rows (more tokens to see) first ----
+    const int H = a.v.H, item = (int)((a.items - 1) - blockIdx.x / H), h = blockIdx.x % H;
+    const int pair = 2 * a.tokens;
+    int b = item, nth = 0;
+    if (a.v.row_start) {
+        b = kv8_find_seq(a.v, item, pair, 1);
+        if (b < 0) return;
+        nth = item - (max(__ldg(a.v.row_start + b), 0) / pair + b);
+    }
+    const Kv8Seq s = kv8_seq(a.v, b, &g_att_range);
+    const int64_t i64 = (int64_t)nth * pair;
+    if (i64 >= s.n) return;
+    const int i0 = (int)i64;                                     // first row of the unit
+    const int rows = min(pair, s.n - i0);
+    const bool two = rows > a.tokens;
+    const int seen = min(max(s.len - s.n + i0 + rows, 0), s.len);  // by its last row
+    const int steps = (seen + kAttTokens - 1) / kAttTokens;
+
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(kfull + x, 4);
+            mbar_init(kempty + x, 1);
+            mbar_init(vfull + x, 4);
+            mbar_init(vempty + x, 1);
+            mbar_init(sfull + x, 2);  // the MMAs, and the thread that knows the scales are there
+            mbar_init(pready + x, 4);
+            mbar_init(pvdone + x, 1);
+        }
+        mbar_init(done, 1);
+        mbar_fence_init();
+    }
+    if (warp == kAttMmaWarp) tmem_alloc(tmem_slot, S::kTmem);
+
+    // ---- q of a thread's row into shared memory ----
+    const int tile = warp >> 2;  // softmax warps
+    int lim = seen;  // a place without a row sees everything, as zeros: no masks for its sake
+    float row_f = 0.f;
+    int64_t out_at = -1;
+    if (warp < kAttConvWarp) {
+        const int r = threadIdx.x & 127, i = r / a.G, ti = i0 + tile * a.tokens + i;
+        const bool valid = i < a.tokens && ti < i0 + rows;
+        const uint16_t *qp = a.q;
+        if (valid) {
+            lim = min(max(s.len - s.n + ti + 1, 0), s.len);
+            const int64_t row = s.r0 + ti, col = (int64_t)(h * a.G + r % a.G) * D;
+            qp = a.q + row * a.q_stride + col;
+            out_at = row * a.out_stride + col;
+        }
+        float top = 0.f;
+        bool bad = false;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float f0 = fabsf(__uint_as_float(w[y] << 16)), f1 = fabsf(__uint_as_float(w[y] & 0xFFFF0000u));
+                top = fmaxf(top, fmaxf(f0, f1));
+                bad |= !(f0 <= FLT_MAX) || !(f1 <= FLT_MAX);
+            }
+        }
+        // the power of two at or below the largest value (2^126 for 2^127, too)
+        const bool some = top >= 0x1p-100f && !bad;
+        const uint32_t e = min(__float_as_uint(top) >> 23, 253u);
+        const float down = some ? __uint_as_float((254u - e) << 23) * a.sign : 0.f;
+        row_f = bad && lim > 0 ? NAN : some ? __uint_as_float(e << 23) * a.scale_log2 : 0.f;
+        uint8_t *qs = smem + S::kQ + tile * S::kTile + r * 128;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                o[y] = some ? att_f16x2(__uint_as_float(w[y] << 16) * down, __uint_as_float(w[y] & 0xFFFF0000u) * down) : 0u;
+            *reinterpret_cast<uint4 *>(qs + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+
+    if (warp < kAttConvWarp) {
+        if (tile == 0 || two) {
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t ts = tmem + lanes + (uint32_t)(tile * 128), to = tmem + lanes + (uint32_t)(256 + tile * 128);
+            float m = -INFINITY, l = 0.f;
+            const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+            for (int i = 0; i < steps; ++i) {
+                if (!mbar_wait_warp(sfull + tile, i & 1, &g_att_fault)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float4 *inf = info + (i % kAttInfo) * 4;
+                const bool masked = (i + 1) * kAttTokens > lim_min;
+                const int left = lim - i * kAttTokens;  // columns this row sees
+                // the largest x = s + log2(vs) of the row
+                float x = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 in = inf[c];
+                    if (in.x < 0.f) continue;  // no page
+                    uint32_t v[32];
+                    att_ld32(ts + 32 * c, v);
+                    att_wait_ld();
+                    float top = -INFINITY;
+                    if (masked) {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            if (32 * c + y < left) top = fmaxf(top, __uint_as_float(v[y]));
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) top = fmaxf(top, __uint_as_float(v[y]));
+                    }
+                    if (top > -INFINITY) x = fmaxf(x, fmaf(top, row_f * in.x, in.y));
+                }
+                const bool grow = x > m + 8.f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float now = grow ? x : m, f = grow ? att_exp2(m - now) : 1.f;
+                    m = now;
+                    l *= f;
+                    if (i > 0) {
+                        if (!mbar_wait_warp(pvdone + tile, (i - 1) & 1, &g_att_fault)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            att_ld32(to + 32 * c, v);
+                            att_wait_ld();
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) v[y] = __float_as_uint(__uint_as_float(v[y]) * f);
+                            att_st32(to + 32 * c, v);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 in = inf[c];
+                    uint32_t p[16];
+                    if (in.x < 0.f) {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) p[y] = 0;
+                    } else {
+                        uint32_t v[32];
+                        att_ld32(ts + 32 * c, v);
+                        att_wait_ld();
+                        const float f = row_f * in.x, g = in.y - ref;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) {
+                            float p0 = att_exp2(fmaf(__uint_as_float(v[2 * y]), f, g));
+                            float p1 = att_exp2(fmaf(__uint_as_float(v[2 * y + 1]), f, g));
+                            if (masked) {
+                                if (32 * c + 2 * y >= left) p0 = 0.f;
+                                if (32 * c + 2 * y + 1 >= left) p1 = 0.f;
+                            }
+                            sum += p0 + p1;
+                            p[y] = att_f16x2(p0, p1);
+                        }
+                        if (in.w == 0.f)
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) p[y] = 0;
+                        l = fmaf(sum, in.z, l);
+                    }
+                    att_st16(ts + 16 * c, p);
+                }
+                att_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pready + tile);
+            }
+            if (ok && steps > 0) ok = mbar_wait_warp(pvdone + tile, (steps - 1) & 1, &g_att_fault);
+            tc_fence_after();
+            if (ok) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    if (steps > 0) {
+                        att_ld32(to + 32 * c, v);
+                        att_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) v[y] = 0;
+                    }
+                    if (out_at >= 0) {
+                        uint4 *op = reinterpret_cast<uint4 *>(a.out + out_at + 32 * c);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                                    : "=r"(o[z])
+                                    : "f"(__uint_as_float(v[8 * y + 2 * z + 1]) * inv), "f"(__uint_as_float(v[8 * y + 2 * z]) * inv));
+                            op[y] = make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp < kAttMmaWarp) {
+        // ---- codes to f16: this thread's 16-byte pieces of a step are rows
+        // 8 (4 (x / halves) + w) + lane % 8, pieces 4 (x % halves) + lane / 8 ----
+        constexpr int NP = 4 * S::kHalves;
+        const int w = warp - kAttConvWarp, r7 = lane & 7, c4 = lane >> 3;
+        uint4 rk[NP], rv[NP];
+        float4 next_info = make_float4(-1.f, 0.f, 1.f, 0.f);
+        auto page_of = [&](int tok) {  // of the 32 tokens from tok on; -1: none
+            return tok < seen ? kv8_page(a.v, b, tok >> a.page_log2, &g_att_range) : -1;
+        };
+        auto load = [&](const int8_t *codes, int i, uint4 (&raw)[NP]) {
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+                const int row = 8 * (4 * (x / S::kHalves) + w) + r7, piece = 4 * (x % S::kHalves) + c4;
+                const int tok = i * kAttTokens + row, page = page_of(tok & ~31);
+                raw[x] = make_uint4(0, 0, 0, 0);
+                if (page >= 0)
+                    raw[x] = __ldg(reinterpret_cast<const uint4 *>(
+                        codes + ((((int64_t)page * H + h) << a.page_log2) + (tok & (a.v.P - 1))) * D + piece * 16));
+            }
+        };
+        auto load_info = [&](int i) {  // scales of the 32 tokens from 32 lane on
+            next_info = make_float4(-1.f, 0.f, 1.f, 0.f);
+            if (w == 0 && lane < 4) {
+                const int page = page_of(i * kAttTokens + lane * 32);
+                if (page >= 0) {
+                    const int64_t ph = (int64_t)page * H + h;
+                    // a page of zeros (its probabilities still count in the row's
+                    // sum) stands with a scale that never leads the maximum
+                    const float vs = __ldg(a.vs + ph), e = vs < 0x1p-100f ? 0x1p-60f : vs;
+                    next_info = make_float4(fabsf(__ldg(a.ks + ph)), log2f(e), 1.f / e, vs < 0x1p-100f ? 0.f : 1.f);
+                }
+            }
+        };
+        auto store = [&](unsigned at, const uint4 (&raw)[NP]) {
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+                const int row = 8 * (4 * (x / S::kHalves) + w) + r7;
+                const uint2 p0 = att_codes(raw[x].x), p1 = att_codes(raw[x].y), p2 = att_codes(raw[x].z), p3 = att_codes(raw[x].w);
+                const unsigned base = at + (x % S::kHalves) * 16384 + row * 128;
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(base + (((2 * c4) ^ r7) << 4)), "r"(p0.x), "r"(p0.y),
+                             "r"(p1.x), "r"(p1.y)
+                             : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(base + (((2 * c4 + 1) ^ r7) << 4)), "r"(p2.x), "r"(p2.y),
+                             "r"(p3.x), "r"(p3.y)
+                             : "memory");
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
+        if (steps > 0) {
+            load(a.k, 0, rk);
+            load_info(0);
+            load(a.vv, 0, rv);
+        }
+        for (int i = 0; i < steps; ++i) {
+            const int st = i & 1, j = i >> 1;
+            if (j > 0 && !mbar_wait_warp(kempty + st, (j - 1) & 1, &g_att_fault)) break;
+            if (w == 0 && lane < 4) info[(i % kAttInfo) * 4 + lane] = next_info;
+            store(smem0 + S::kK + st * S::kTile, rk);
+            if (lane == 0) mbar_arrive(kfull + st);
+            if (i + 1 < steps) {
+                load(a.k, i + 1, rk);
+                load_info(i + 1);
+            }
+            if (j > 0 && !mbar_wait_warp(vempty + st, (j - 1) & 1, &g_att_fault)) break;
+            store(smem0 + S::kV + st * S::kTile, rv);
+            if (lane == 0) mbar_arrive(vfull + st);
+            if (i + 1 < steps) load(a.vv, i + 1, rv);
+        }
+    } else {
+        // ---- MMAs: f16 operands, fp32 sums, M = 128 ----
+        const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kAttTokens >> 3) << 17) | ((uint32_t)(kAttRows >> 4) << 24);
+        const uint32_t idesc_o = (1u << 4) | (1u << 16) /*B is MN-major*/ | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kAttRows >> 4) << 24);
+        auto scores = [&](int q, int i) {
+            const unsigned qa = smem0 + S::kQ + q * S::kTile, ka = smem0 + S::kK + (i & 1) * S::kTile;
+            const uint32_t d = tmem + (uint32_t)(q * 128);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const unsigned at = (k >> 2) * 16384 + (k & 3) * 32;
+                    if (k == 0)
+                        att_mma_ss<false>(d, att_desc_k(qa + at), att_desc_k(ka + at), idesc_s);
+                    else
+                        att_mma_ss<true>(d, att_desc_k(qa + at), att_desc_k(ka + at), idesc_s);
+                }
+                umma_commit(sfull + q);
+                mbar_arrive(sfull + q);
+                if (q == (two ? 1 : 0)) umma_commit(kempty + (i & 1));
+            }
+            __syncwarp();
+        };
+        auto values = [&](int q, int i) {
+            const unsigned va = smem0 + S::kV + (i & 1) * S::kTile;
+            const uint32_t d = tmem + (uint32_t)(256 + q * 128), p = tmem + (uint32_t)(q * 128);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kAttTokens / 16; ++k)
+                    att_mma_ts(d, p + 8 * k, att_desc_mn(va + k * 2048), idesc_o, i > 0 || k > 0);
+                umma_commit(pvdone + q);
+                if (q == (two ? 1 : 0)) umma_commit(vempty + (i & 1));
+            }
+            __syncwarp();
+        };
+        const int tiles = two ? 2 : 1;
+        for (int i = -1; i < steps && ok; ++i) {
+            for (int q = 0; q < tiles && ok; ++q) {
+                if (i >= 0) {
+                    if (!mbar_wait_warp(pready + q, i & 1, &g_att_fault) ||
+                        (q == 0 && !mbar_wait_warp(vfull + (i & 1), (i >> 1) & 1, &g_att_fault))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    values(q, i);
+                }
+                if (i + 1 < steps) {
+                    if (q == 0 && !mbar_wait_warp(kfull + ((i + 1) & 1), ((i + 1) >> 1) & 1, &g_att_fault)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    scores(q, i + 1);
+                }
+            }
+        }
+        // also after a failed wait: `done` tells that every MMA issued has
+        // completed, before tensor memory is released
+        if (elect_one()) umma_commit(done);
+        __syncwarp();
+        mbar_wait_warp(done, 0, &g_att_fault);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kAttMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kTmem);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// Units of the call, at most: pairs of tiles, see kv8_find_seq.
+static int64_t attn_tc_units(const lowbit_kv8_cache &c, const lowbit_kv8_batch &b, int q_heads)
+{
+    const int64_t pair = 2 * (kAttRows / (q_heads / c.n_heads));
+    return (b.row_start ? b.n_rows / pair + b.n_seqs : b.n_seqs) * c.n_heads;
+}
+
+bool kv8_attn_tc_takes(const lowbit_kv8_cache &c, const lowbit_kv8_batch &b, int q_heads)
+{
+    const int64_t rows = (int64_t)b.n_rows * (q_heads / c.n_heads);
+    return rows >= 64 * (int64_t)b.n_seqs && rows * c.n_heads >= 32 * 256 && attn_tc_units(c, b, q_heads) < (int64_t(1) << 31);
+}
+
+lowbit_status kv8_attn_tc_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch &b, const uint16_t *q,
+                                 int64_t q_stride, int q_heads, float scale, uint16_t *out, int64_t out_stride,
+                                 cudaStream_t st)
+{
+    Kv8AttnTc a;
+    a.v = kv8_view(c, b);
+    a.k = c.k; a.vv = c.v; a.ks = c.k_scales; a.vs = c.v_scales;
+    a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
+    a.G = q_heads / c.n_heads;
+    a.tokens = kAttRows / a.G;
+    a.page_log2 = c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
+    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    a.sign = scale < 0.f ? -1.f : 1.f;
+    const int64_t units = attn_tc_units(c, b, q_heads);
+    a.items = (int)(units / c.n_heads);
+    void (*kern)(const Kv8AttnTc) = c.head_dim == 128 ? k_kv8_attn_tc<128> : k_kv8_attn_tc<64>;
+    const int smem = c.head_dim == 128 ? AttnTc<128>::kBytes : AttnTc<64>::kBytes;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return LOWBIT_ERR_CUDA;
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)units), dim3(kAttThreads), smem, st, a);
+    return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
+}
+
+// Bit 0: a length, page or row out of range; bit 1: a bounded wait ran out; < 0:
+// not to be read.
+int kv8_attn_tc_fault_flags()
+{
+    unsigned r = 0, f = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&r, g_att_range, sizeof(r)) != cudaSuccess) return -1;
+    if (cudaMemcpyFromSymbol(&f, g_att_fault, sizeof(f)) != cudaSuccess) return -1;
+    cudaMemcpyToSymbol(g_att_range, &zero, sizeof(zero));
+    cudaMemcpyToSymbol(g_att_fault, &zero, sizeof(zero));
+    return (r ? 1 : 0) | (f ? 2 : 0);
+}
+
+}  // namespace lowbit

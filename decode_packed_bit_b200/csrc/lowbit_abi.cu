@@ -78,6 +78,10 @@ int kv8_attn_fault_flag();
 size_t kv8_attn_workspace_bytes(const lowbit_kv8_cache &);
 lowbit_status kv8_attn_launch(const lowbit_kv8_cache &, const lowbit_kv8_batch &, const uint16_t *, int64_t, int, float,
                               uint16_t *, int64_t, void *, cudaStream_t);
+bool kv8_attn_tc_takes(const lowbit_kv8_cache &, const lowbit_kv8_batch &, int);
+int kv8_attn_tc_fault_flags();
+lowbit_status kv8_attn_tc_launch(const lowbit_kv8_cache &, const lowbit_kv8_batch &, const uint16_t *, int64_t, int,
+                                 float, uint16_t *, int64_t, cudaStream_t);
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 constexpr int kQ1MaxM = 16;
@@ -127,9 +131,9 @@ int lowbit_version(void) { return 100; }
 int lowbit_fault_flags(void)
 {
     const int f4 = i4tc_fault_flag(), fs = q1stack_fault_flag(), fg = smg_fault_flag();
-    const int fk = kv8_fault_flag(), fa = kv8_attn_fault_flag();
-    if (f4 < 0 || fs < 0 || fg < 0 || fk < 0 || fa < 0) return -1;
-    return (f4 ? 1 : 0) | (fs ? 4 : 0) | (fg ? 8 : 0) | (fk || fa ? 16 : 0);
+    const int fk = kv8_fault_flag(), fa = kv8_attn_fault_flag(), ft = kv8_attn_tc_fault_flags();
+    if (f4 < 0 || fs < 0 || fg < 0 || fk < 0 || fa < 0 || ft < 0) return -1;
+    return (f4 ? 1 : 0) | (fs ? 4 : 0) | (fg ? 8 : 0) | (fk || fa || (ft & 1) ? 16 : 0) | (ft & 2 ? 32 : 0);
 }
 
 lowbit_status lowbit_pack(lowbit_format fmt, const int8_t *codes, int64_t rows, int64_t cols,
@@ -684,6 +688,8 @@ lowbit_status lowbit_kv8_attention(const lowbit_kv8_cache *cache, const lowbit_k
     LB_CHECK(q && out && workspace, LOWBIT_ERR_INVALID_ARG);
     LB_CHECK(aligned16(q) && aligned16(out) && aligned16(workspace), LOWBIT_ERR_MISALIGNED);
     LB_CHECK(workspace_bytes >= kv8_attn_workspace_bytes(*cache), LOWBIT_ERR_INVALID_ARG);
+    if (kv8_attn_tc_takes(*cache, *batch, q_heads))
+        return kv8_attn_tc_launch(*cache, *batch, q, q_stride, q_heads, scale, out, out_stride, as_stream(stream));
     return kv8_attn_launch(*cache, *batch, q, q_stride, q_heads, scale, out, out_stride, workspace, as_stream(stream));
 }
 

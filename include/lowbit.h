@@ -100,7 +100,8 @@ int lowbit_version(void);
  * bit 3 = a wait on the shared activation ring of a small-batch kernel
  * (Q1_0_g128 at 2 <= M <= 16, INT4_G64 at 2 <= M <= 32; the results of such
  * a call are then not valid), bit 4 = a length, page or row of a KV8 batch out
- * of range (see lowbit_kv8_batch); -1 = the flags could not
+ * of range (see lowbit_kv8_batch), bit 5 = a bounded wait inside
+ * lowbit_kv8_attention's tcgen05 kernel; -1 = the flags could not
  * be read.  This is a diagnostic call, not part of any product: it reads the
  * flags from device memory and therefore synchronises with the device (every
  * other entry point is asynchronous). */
@@ -589,7 +590,12 @@ lowbit_status lowbit_kv8_read(const lowbit_kv8_cache *cache, const lowbit_kv8_ba
  *   out  n_rows rows of q_heads * head_dim bf16, out_stride elements apart
  *        (strides multiples of 8)
  * q_heads a multiple of n_heads, at most 64 query heads per head of the cache.
- * A non-finite q makes its row and head NaN.
+ * A non-finite q makes its row and head NaN; a row of q whose largest value is
+ * below 2^-100 counts as zeros, and so does a page whose v_scales is.
+ * Few rows per sequence (a decode step, tokens to be checked) run on the integer
+ * tensor cores, split over the tokens; many rows (prompts: at least 64 rows x
+ * query heads per cache head for each sequence, and 8192 of them in all) on
+ * tcgen05.  Both keep sums and probabilities' statistics in fp32.
  * workspace: lowbit_kv8_attention_workspace_bytes(cache, batch, q_heads) bytes,
  * zero-filled before its first use (calls leave what they need zeroed).  Calls
  * that share one must be ordered on one stream; that holds for replays of

@@ -200,6 +200,62 @@ def test_attention_several_rows(lb, H, G, D, P, lens, rows):
     check_attention(cache, table, lens, q, 0.1, rs, out)
 
 
+# Calls that take the tcgen05 kernel: many rows.  Its steps fit the same bound: q as f16 is nearer than q's fixed
+# point there, and a probability's f16 rounding, 2^-12 of itself, adds 2^-12 of the largest value, half of what the
+# bound allows the fixed-point ones.
+PROMPTS = [(2, 4, 128, 64, [700, 650], [600, 640]), (4, 5, 64, 32, [333, 128, 900], [200, 128, 130]),
+           (8, 1, 128, 128, [1500], [1100]), (1, 64, 64, 128, [300], [150]), (3, 12, 128, 32, [400, 0, 100], [300, 5, 20]),
+           (2, 3, 64, 64, [129, 1000, 128], [129, 1000, 250]), (8, 8, 128, 64, [257], [129])]
+
+
+@pytest.mark.parametrize("H,G,D,P,lens,rows", PROMPTS)
+def test_attention_prompts(lb, H, G, D, P, lens, rows):
+    assert sum(rows) * G * H >= 8192 and sum(rows) * G >= 64 * len(rows)
+    n_pages, table = make_batch(sum(rows) + D, lens, P)
+    cache = make_cache(lb, D + G, n_pages, H, P, D)
+    rs = starts(rows)
+    q = torch.randn((sum(rows) + 3, H * G, D), device="cuda").bfloat16() * 1.5
+    out = attend(lb, cache, table, lens, q, 0.1, rs)
+    check_attention(cache, table, lens, q, 0.1, rs, out)
+    assert lb.lowbit_fault_flags() == 0
+    for _ in range(3):
+        assert torch.equal(out, attend(lb, cache, table, lens, q, 0.1, rs))
+
+
+def test_attention_prompts_extremes(lb):
+    """Growing and falling scores, scales far apart between pages (zero among them), huge, tiny and non-finite rows of
+    q, an absent page, stale codes behind the end."""
+    H, G, D, P, lens, rows = 4, 4, 128, 32, [900, 300], [700, 300]
+    n_pages, table = make_batch(16, lens, P)
+    cache = make_cache(lb, 16, n_pages, H, P, D)
+    order = table[0, :29]
+    grow = torch.linspace(-3, 3, 29, device="cuda")
+    cache.k_scales[order.tolist()] *= torch.exp(grow)[:, None]
+    cache.v_scales[order.tolist()] *= torch.exp(-2 * grow)[:, None]
+    cache.v_scales[int(order[3])] = 0
+    cache.k_scales[int(order[5])] = 0
+    table[1, 2] = -1
+    cache.v[int(table[1, 9]), :, 12:] = 127
+    rs = starts(rows)
+    q = torch.randn((sum(rows), H * G, D), device="cuda").bfloat16()
+    q[10, 0] *= 50
+    q[11, 1] = 0
+    q[12, 2] = 1e-37
+    q[13, 3, 5] = 1e5
+    for scale in (0.05, -0.05):
+        out = attend(lb, cache, table, lens, q, scale, rs)
+        check_attention(cache, table, lens, q, scale, rs, out)
+    assert lb.lowbit_fault_flags() == 16
+    z = q.clone()
+    z[500, 7, 100], z[800, 3, 0] = float("nan"), float("-inf")
+    got = attend(lb, cache, table, lens, z, -0.05, rs)
+    assert torch.isnan(got[500, 7]).all() and torch.isnan(got[800, 3]).all()
+    keep = torch.ones(got.shape[:2], dtype=torch.bool, device="cuda")
+    keep[500, 7] = keep[800, 3] = False
+    assert torch.equal(got[keep], out[keep])
+    assert lb.lowbit_fault_flags() == 16
+
+
 @pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("scale", [-0.1, 0.0])
 def test_attention_scale_of_any_sign(lb, n, scale):
