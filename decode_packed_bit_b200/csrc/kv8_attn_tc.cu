@@ -31,6 +31,7 @@
 // the CTA leaves its loops, releases tensor memory and exits.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "kv8_common.cuh"
 #include "tc_common.cuh"
@@ -94,13 +95,14 @@ __device__ __forceinline__ void att_mma_ss(uint32_t d, uint64_t a, uint64_t b, u
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
 }
-__device__ __forceinline__ void att_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+template <bool ACC>
+__device__ __forceinline__ void att_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+        "r"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0));
 }
 
 __device__ __forceinline__ void att_ld32(uint32_t addr, uint32_t (&v)[32])
@@ -125,15 +127,28 @@ __device__ __forceinline__ void att_st32(uint32_t addr, const uint32_t (&v)[32])
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
-__device__ __forceinline__ void att_st16(uint32_t addr, const uint32_t (&v)[16])
+__device__ __forceinline__ void att_ld16(uint32_t addr, uint32_t (&v)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void att_st8(uint32_t addr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void att_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The same, and the values loaded may be used only after it.
+__device__ __forceinline__ void att_wait_ld(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+}
 __device__ __forceinline__ void att_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float att_exp2(float x)
@@ -158,6 +173,75 @@ __device__ __forceinline__ uint2 att_codes(uint32_t w)
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(0x64806480u));
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(b) : "r"(0x64806480u));
     return make_uint2(a, b);
+}
+
+// The largest x = s + log2(vs) of a thread's row of S (columns < left where MASK).
+// Sixteen columns are loaded while those before them are worked on (two times 32
+// would not fit the 128 registers of 13 warps).
+template <bool MASK>
+__device__ __forceinline__ float att_top(uint32_t ts, const float4 *inf, int left, float row_f)
+{
+    float x = -INFINITY;
+    uint32_t v[2][16];
+    att_ld16(ts, v[0]);
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            att_wait_ld(v[h]);
+            if (c + h < 7) att_ld16(ts + 16 * (c + h + 1), v[h ^ 1]);
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+                top[y & 3] = fmaxf(top[y & 3], !MASK || 16 * (c + h) + y < left ? __uint_as_float(v[h][y]) : -INFINITY);
+            __syncwarp();  // the tensor-memory loads want the warp together, whatever became of the choices above
+        }
+        const float4 in = inf[c >> 1];
+        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // (32 tokens without a page have in.x < 0)
+        if (in.x >= 0.f && (!MASK || most > -INFINITY)) x = fmaxf(x, fmaf(most, row_f * in.x, in.y));
+    }
+    return x;
+}
+
+// The row's probabilities over S's place; returns their sum over vs.
+template <bool MASK>
+__device__ __forceinline__ float att_probs(uint32_t ts, const float4 *inf, int left, float row_f, float ref)
+{
+    float l = 0.f;
+    uint32_t v[2][16];
+    att_ld16(ts, v[0]);
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {
+        const float4 in = inf[c >> 1];
+        const float f = row_f * in.x, g = in.y - ref;
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            att_wait_ld(v[h]);
+            if (c + h < 7) att_ld16(ts + 16 * (c + h + 1), v[h ^ 1]);
+            uint32_t p[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                float p0 = att_exp2(fmaf(__uint_as_float(v[h][2 * y]), f, g));
+                float p1 = att_exp2(fmaf(__uint_as_float(v[h][2 * y + 1]), f, g));
+                if (MASK) {
+                    if (16 * (c + h) + 2 * y >= left) p0 = 0.f;
+                    if (16 * (c + h) + 2 * y + 1 >= left) p1 = 0.f;
+                }
+                sum[0] += p0;
+                sum[1] += p1;
+                p[y] = att_f16x2(p0, p1);
+            }
+            if (in.w == 0.f)  // values of zero, or no page
+#pragma unroll
+                for (int y = 0; y < 8; ++y) p[y] = 0;
+            __syncwarp();
+            att_st8(ts + 8 * (c + h), p);
+        }
+        if (in.x >= 0.f) l = fmaf(sum[0] + sum[1], in.z, l);
+    }
+    return l;
 }
 
 template <int D>
@@ -276,26 +360,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                 const float4 *inf = info + (i % kAttInfo) * 4;
                 const bool masked = (i + 1) * kAttTokens > lim_min;
                 const int left = lim - i * kAttTokens;  // columns this row sees
-                // the largest x = s + log2(vs) of the row
-                float x = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 in = inf[c];
-                    if (in.x < 0.f) continue;  // no page
-                    uint32_t v[32];
-                    att_ld32(ts + 32 * c, v);
-                    att_wait_ld();
-                    float top = -INFINITY;
-                    if (masked) {
-#pragma unroll
-                        for (int y = 0; y < 32; ++y)
-                            if (32 * c + y < left) top = fmaxf(top, __uint_as_float(v[y]));
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) top = fmaxf(top, __uint_as_float(v[y]));
-                    }
-                    if (top > -INFINITY) x = fmaxf(x, fmaf(top, row_f * in.x, in.y));
-                }
+                float x = masked ? att_top<true>(ts, inf, left, row_f) : att_top<false>(ts, inf, left, row_f);
+                __syncwarp();
                 const bool grow = x > m + 8.f;
                 if (__any_sync(0xffffffffu, grow)) {
                     const float now = grow ? x : m, f = grow ? att_exp2(m - now) : 1.f;
@@ -319,37 +385,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                     }
                 }
                 const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 in = inf[c];
-                    uint32_t p[16];
-                    if (in.x < 0.f) {
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) p[y] = 0;
-                    } else {
-                        uint32_t v[32];
-                        att_ld32(ts + 32 * c, v);
-                        att_wait_ld();
-                        const float f = row_f * in.x, g = in.y - ref;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int y = 0; y < 16; ++y) {
-                            float p0 = att_exp2(fmaf(__uint_as_float(v[2 * y]), f, g));
-                            float p1 = att_exp2(fmaf(__uint_as_float(v[2 * y + 1]), f, g));
-                            if (masked) {
-                                if (32 * c + 2 * y >= left) p0 = 0.f;
-                                if (32 * c + 2 * y + 1 >= left) p1 = 0.f;
-                            }
-                            sum += p0 + p1;
-                            p[y] = att_f16x2(p0, p1);
-                        }
-                        if (in.w == 0.f)
-#pragma unroll
-                            for (int y = 0; y < 16; ++y) p[y] = 0;
-                        l = fmaf(sum, in.z, l);
-                    }
-                    att_st16(ts + 16 * c, p);
-                }
+                l += masked ? att_probs<true>(ts, inf, left, row_f, ref) : att_probs<false>(ts, inf, left, row_f, ref);
                 att_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -391,32 +427,33 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         constexpr int NP = 4 * S::kHalves;
         const int w = warp - kAttConvWarp, r7 = lane & 7, c4 = lane >> 3;
         uint4 rk[NP], rv[NP];
+        // Lane c < 4 knows the page of the step's 32 tokens from 32 c on (-1: none),
+        // looked up one step ahead of the codes, and the first warp's its scales.
         float4 next_info = make_float4(-1.f, 0.f, 1.f, 0.f);
-        auto page_of = [&](int tok) {  // of the 32 tokens from tok on; -1: none
+        auto pages_of = [&](int i) {
+            const int tok = i * kAttTokens + (lane & 3) * 32;
             return tok < seen ? kv8_page(a.v, b, tok >> a.page_log2, &g_att_range) : -1;
         };
-        auto load = [&](const int8_t *codes, int i, uint4 (&raw)[NP]) {
+        auto load = [&](const int8_t *codes, int i, int pages, uint4 (&raw)[NP]) {
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
                 const int row = 8 * (4 * (x / S::kHalves) + w) + r7, piece = 4 * (x % S::kHalves) + c4;
-                const int tok = i * kAttTokens + row, page = page_of(tok & ~31);
-                raw[x] = make_uint4(0, 0, 0, 0);
-                if (page >= 0)
-                    raw[x] = __ldg(reinterpret_cast<const uint4 *>(
-                        codes + ((((int64_t)page * H + h) << a.page_log2) + (tok & (a.v.P - 1))) * D + piece * 16));
+                // rows 8 (4 y + w) .. + 7 lie in the 32 tokens from 32 y on
+                const int page = __shfl_sync(0xffffffffu, pages, x / S::kHalves);
+                raw[x] = page < 0 ? make_uint4(0, 0, 0, 0)
+                                  : __ldg(reinterpret_cast<const uint4 *>(
+                                        codes + ((((int64_t)page * H + h) << a.page_log2) + ((i * kAttTokens + row) & (a.v.P - 1))) * D +
+                                        piece * 16));
             }
         };
-        auto load_info = [&](int i) {  // scales of the 32 tokens from 32 lane on
+        auto load_info = [&](int page) {
             next_info = make_float4(-1.f, 0.f, 1.f, 0.f);
-            if (w == 0 && lane < 4) {
-                const int page = page_of(i * kAttTokens + lane * 32);
-                if (page >= 0) {
-                    const int64_t ph = (int64_t)page * H + h;
-                    // a page of zeros (its probabilities still count in the row's
-                    // sum) stands with a scale that never leads the maximum
-                    const float vs = __ldg(a.vs + ph), e = vs < 0x1p-100f ? 0x1p-60f : vs;
-                    next_info = make_float4(fabsf(__ldg(a.ks + ph)), log2f(e), 1.f / e, vs < 0x1p-100f ? 0.f : 1.f);
-                }
+            if (w == 0 && lane < 4 && page >= 0) {
+                const int64_t ph = (int64_t)page * H + h;
+                // a page of zeros (its probabilities still count in the row's
+                // sum) stands with a scale that never leads the maximum
+                const float vs = __ldg(a.vs + ph), e = vs < 0x1p-100f ? 0x1p-60f : vs;
+                next_info = make_float4(fabsf(__ldg(a.ks + ph)), log2f(e), 1.f / e, vs < 0x1p-100f ? 0.f : 1.f);
             }
         };
         auto store = [&](unsigned at, const uint4 (&raw)[NP]) {
@@ -435,81 +472,82 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
         };
-        if (steps > 0) {
-            load(a.k, 0, rk);
-            load_info(0);
-            load(a.vv, 0, rv);
-        }
+        int pages = pages_of(0), next_pages = pages_of(1);
+        load(a.k, 0, pages, rk);
+        load_info(pages);
+        load(a.vv, 0, pages, rv);
         for (int i = 0; i < steps; ++i) {
             const int st = i & 1, j = i >> 1;
+            pages = next_pages;  // of step i + 1: none past the last
+            next_pages = pages_of(i + 2);
             if (j > 0 && !mbar_wait_warp(kempty + st, (j - 1) & 1, &g_att_fault)) break;
             if (w == 0 && lane < 4) info[(i % kAttInfo) * 4 + lane] = next_info;
             store(smem0 + S::kK + st * S::kTile, rk);
             if (lane == 0) mbar_arrive(kfull + st);
-            if (i + 1 < steps) {
-                load(a.k, i + 1, rk);
-                load_info(i + 1);
-            }
+            load(a.k, i + 1, pages, rk);
+            load_info(pages);
             if (j > 0 && !mbar_wait_warp(vempty + st, (j - 1) & 1, &g_att_fault)) break;
             store(smem0 + S::kV + st * S::kTile, rv);
             if (lane == 0) mbar_arrive(vfull + st);
-            if (i + 1 < steps) load(a.vv, i + 1, rv);
+            load(a.vv, i + 1, pages, rv);
         }
     } else {
         // ---- MMAs: f16 operands, fp32 sums, M = 128 ----
         const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kAttTokens >> 3) << 17) | ((uint32_t)(kAttRows >> 4) << 24);
         const uint32_t idesc_o = (1u << 4) | (1u << 16) /*B is MN-major*/ | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kAttRows >> 4) << 24);
-        auto scores = [&](int q, int i) {
-            const unsigned qa = smem0 + S::kQ + q * S::kTile, ka = smem0 + S::kK + (i & 1) * S::kTile;
-            const uint32_t d = tmem + (uint32_t)(q * 128);
+        // what the compiler can see is the same for the whole warp may live in
+        // uniform registers, as MMA operands have to
+        const uint32_t base = __reduce_max_sync(0xffffffffu, tmem), sm = __reduce_max_sync(0xffffffffu, smem0);
+        const int last = __reduce_max_sync(0xffffffffu, steps);
+        const bool both = __any_sync(0xffffffffu, two);
+        auto scores = [&](auto tile_c, int i) {
+            constexpr int q = decltype(tile_c)::value;
+            const uint64_t qd = att_desc_k(sm + S::kQ + q * S::kTile), kd = att_desc_k(sm + S::kK + (i & 1) * S::kTile);
             if (elect_one()) {
+                att_mma_ss<false>(base + q * 128, qd, kd, idesc_s);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const unsigned at = (k >> 2) * 16384 + (k & 3) * 32;
-                    if (k == 0)
-                        att_mma_ss<false>(d, att_desc_k(qa + at), att_desc_k(ka + at), idesc_s);
-                    else
-                        att_mma_ss<true>(d, att_desc_k(qa + at), att_desc_k(ka + at), idesc_s);
-                }
+                for (int k = 1; k < D / 16; ++k)
+                    att_mma_ss<true>(base + q * 128, qd + (k >> 2) * 1024 + (k & 3) * 2, kd + (k >> 2) * 1024 + (k & 3) * 2, idesc_s);
                 umma_commit(sfull + q);
                 mbar_arrive(sfull + q);
-                if (q == (two ? 1 : 0)) umma_commit(kempty + (i & 1));
+                if (q == 1 || !both) umma_commit(kempty + (i & 1));
             }
             __syncwarp();
         };
-        auto values = [&](int q, int i) {
-            const unsigned va = smem0 + S::kV + (i & 1) * S::kTile;
-            const uint32_t d = tmem + (uint32_t)(256 + q * 128), p = tmem + (uint32_t)(q * 128);
+        auto values = [&](auto tile_c, int i) {
+            constexpr int q = decltype(tile_c)::value;
+            const uint64_t vd = att_desc_mn(sm + S::kV + (i & 1) * S::kTile);
+            const uint32_t d = base + 256 + q * 128, p = base + q * 128;
             if (elect_one()) {
+                if (i == 0)
+                    att_mma_ts<false>(d, p, vd, idesc_o);
+                else
+                    att_mma_ts<true>(d, p, vd, idesc_o);
 #pragma unroll
-                for (int k = 0; k < kAttTokens / 16; ++k)
-                    att_mma_ts(d, p + 8 * k, att_desc_mn(va + k * 2048), idesc_o, i > 0 || k > 0);
+                for (int k = 1; k < kAttTokens / 16; ++k) att_mma_ts<true>(d, p + 8 * k, vd + k * 128, idesc_o);
                 umma_commit(pvdone + q);
-                if (q == (two ? 1 : 0)) umma_commit(vempty + (i & 1));
+                if (q == 1 || !both) umma_commit(vempty + (i & 1));
             }
             __syncwarp();
         };
-        const int tiles = two ? 2 : 1;
-        for (int i = -1; i < steps && ok; ++i) {
-            for (int q = 0; q < tiles && ok; ++q) {
-                if (i >= 0) {
-                    if (!mbar_wait_warp(pready + q, i & 1, &g_att_fault) ||
-                        (q == 0 && !mbar_wait_warp(vfull + (i & 1), (i >> 1) & 1, &g_att_fault))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    values(q, i);
-                }
-                if (i + 1 < steps) {
-                    if (q == 0 && !mbar_wait_warp(kfull + ((i + 1) & 1), ((i + 1) >> 1) & 1, &g_att_fault)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    scores(q, i + 1);
-                }
+        auto step = [&](auto tile_c, int i) {  // tile's P V of step i, then its scores of step i + 1
+            constexpr int q = decltype(tile_c)::value;
+            if (i >= 0) {
+                if (!mbar_wait_warp(pready + q, i & 1, &g_att_fault)) return false;
+                if (q == 0 && !mbar_wait_warp(vfull + (i & 1), (i >> 1) & 1, &g_att_fault)) return false;
+                tc_fence_after();
+                values(tile_c, i);
             }
+            if (i + 1 < last) {
+                if (q == 0 && !mbar_wait_warp(kfull + ((i + 1) & 1), ((i + 1) >> 1) & 1, &g_att_fault)) return false;
+                tc_fence_after();
+                scores(tile_c, i + 1);
+            }
+            return true;
+        };
+        for (int i = -1; i < last; ++i) {
+            if (!step(std::integral_constant<int, 0>{}, i)) break;
+            if (both && !step(std::integral_constant<int, 1>{}, i)) break;
         }
         // also after a failed wait: `done` tells that every MMA issued has
         // completed, before tensor memory is released
