@@ -495,59 +495,69 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         // ---- MMAs: f16 operands, fp32 sums, M = 128 ----
         const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kAttTokens >> 3) << 17) | ((uint32_t)(kAttRows >> 4) << 24);
         const uint32_t idesc_o = (1u << 4) | (1u << 16) /*B is MN-major*/ | ((uint32_t)(D >> 3) << 17) | ((uint32_t)(kAttRows >> 4) << 24);
-        // what the compiler can see is the same for the whole warp may live in
-        // uniform registers, as MMA operands have to
-        const uint32_t base = __reduce_max_sync(0xffffffffu, tmem), sm = __reduce_max_sync(0xffffffffu, smem0);
+        // MMA operands have to be in uniform registers: what comes from a warp
+        // reduction is the same for the whole warp in the compiler's eyes too, and
+        // tile and stage are constants of the unrolled code, so that a
+        // descriptor is a sum of such a value and an immediate.
+        const uint32_t base = __reduce_max_sync(0xffffffffu, tmem);
+        const uint32_t sm = __reduce_max_sync(0xffffffffu, smem0);
         const int last = __reduce_max_sync(0xffffffffu, steps);
         const bool both = __any_sync(0xffffffffu, two);
-        auto scores = [&](auto tile_c, int i) {
-            constexpr int q = decltype(tile_c)::value;
-            const uint64_t qd = att_desc_k(sm + S::kQ + q * S::kTile), kd = att_desc_k(sm + S::kK + (i & 1) * S::kTile);
+        const uint64_t desc_k0 = att_desc_k(sm), desc_v0 = att_desc_mn(sm + S::kV);
+        auto scores = [&](auto tile_c, auto stage_c) {
+            constexpr int q = decltype(tile_c)::value, st = decltype(stage_c)::value;
+            constexpr int qo = (S::kQ + q * S::kTile) >> 4, ko = (S::kK + st * S::kTile) >> 4;
             if (elect_one()) {
-                att_mma_ss<false>(base + q * 128, qd, kd, idesc_s);
+                att_mma_ss<false>(base + q * 128, desc_k0 + qo, desc_k0 + ko, idesc_s);
 #pragma unroll
-                for (int k = 1; k < D / 16; ++k)
-                    att_mma_ss<true>(base + q * 128, qd + (k >> 2) * 1024 + (k & 3) * 2, kd + (k >> 2) * 1024 + (k & 3) * 2, idesc_s);
+                for (int k = 1; k < D / 16; ++k) {
+                    const int at = (k >> 2) * 1024 + (k & 3) * 2;
+                    att_mma_ss<true>(base + q * 128, desc_k0 + (qo + at), desc_k0 + (ko + at), idesc_s);
+                }
                 umma_commit(sfull + q);
                 mbar_arrive(sfull + q);
-                if (q == 1 || !both) umma_commit(kempty + (i & 1));
+                if (q == 1 || !both) umma_commit(kempty + st);
             }
             __syncwarp();
         };
-        auto values = [&](auto tile_c, int i) {
-            constexpr int q = decltype(tile_c)::value;
-            const uint64_t vd = att_desc_mn(sm + S::kV + (i & 1) * S::kTile);
-            const uint32_t d = base + 256 + q * 128, p = base + q * 128;
+        auto values = [&](auto tile_c, auto stage_c, bool first) {
+            constexpr int q = decltype(tile_c)::value, st = decltype(stage_c)::value;
+            constexpr int vo = (st * S::kTile) >> 4;
+            const uint32_t d = base + (256 + q * 128), p = base + q * 128;
             if (elect_one()) {
-                if (i == 0)
-                    att_mma_ts<false>(d, p, vd, idesc_o);
+                if (first)
+                    att_mma_ts<false>(d, p, desc_v0 + vo, idesc_o);
                 else
-                    att_mma_ts<true>(d, p, vd, idesc_o);
+                    att_mma_ts<true>(d, p, desc_v0 + vo, idesc_o);
 #pragma unroll
-                for (int k = 1; k < kAttTokens / 16; ++k) att_mma_ts<true>(d, p + 8 * k, vd + k * 128, idesc_o);
+                for (int k = 1; k < kAttTokens / 16; ++k) att_mma_ts<true>(d, p + 8 * k, desc_v0 + (vo + k * 128), idesc_o);
                 umma_commit(pvdone + q);
-                if (q == 1 || !both) umma_commit(vempty + (i & 1));
+                if (q == 1 || !both) umma_commit(vempty + st);
             }
             __syncwarp();
         };
-        auto step = [&](auto tile_c, int i) {  // tile's P V of step i, then its scores of step i + 1
-            constexpr int q = decltype(tile_c)::value;
+        // a tile's P V of step i, then its scores of step i + 1
+        auto step = [&](auto tile_c, auto stage_c, int i) {
+            constexpr int q = decltype(tile_c)::value, st = decltype(stage_c)::value;
             if (i >= 0) {
                 if (!mbar_wait_warp(pready + q, i & 1, &g_att_fault)) return false;
-                if (q == 0 && !mbar_wait_warp(vfull + (i & 1), (i >> 1) & 1, &g_att_fault)) return false;
+                if (q == 0 && !mbar_wait_warp(vfull + st, (i >> 1) & 1, &g_att_fault)) return false;
                 tc_fence_after();
-                values(tile_c, i);
+                values(tile_c, stage_c, i == 0);
             }
             if (i + 1 < last) {
-                if (q == 0 && !mbar_wait_warp(kfull + ((i + 1) & 1), ((i + 1) >> 1) & 1, &g_att_fault)) return false;
+                if (q == 0 && !mbar_wait_warp(kfull + (st ^ 1), ((i + 1) >> 1) & 1, &g_att_fault)) return false;
                 tc_fence_after();
-                scores(tile_c, i + 1);
+                scores(tile_c, std::integral_constant<int, st ^ 1>{});
             }
             return true;
         };
-        for (int i = -1; i < last; ++i) {
-            if (!step(std::integral_constant<int, 0>{}, i)) break;
-            if (both && !step(std::integral_constant<int, 1>{}, i)) break;
+        using C0 = std::integral_constant<int, 0>;
+        using C1 = std::integral_constant<int, 1>;
+        for (int i = -1; i < last; i += 2) {  // odd steps lie in stage 1
+            if (!step(C0{}, C1{}, i) || (both && !step(C1{}, C1{}, i))) break;
+            if (i + 1 >= last) break;
+            if (!step(C0{}, C0{}, i + 1) || (both && !step(C1{}, C0{}, i + 1))) break;
         }
         // also after a failed wait: `done` tells that every MMA issued has
         // completed, before tensor memory is released
