@@ -116,17 +116,6 @@ __device__ __forceinline__ void att_ld32(uint32_t addr, uint32_t (&v)[32])
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void att_st32(uint32_t addr, const uint32_t (&v)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
 __device__ __forceinline__ void att_ld16(uint32_t addr, uint32_t (&v)[16])
 {
     asm volatile(
@@ -135,11 +124,13 @@ __device__ __forceinline__ void att_ld16(uint32_t addr, uint32_t (&v)[16])
           "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
 }
-__device__ __forceinline__ void att_st8(uint32_t addr, const uint32_t (&v)[8])
+__device__ __forceinline__ void att_st16(uint32_t addr, const uint32_t (&v)[16])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 __device__ __forceinline__ void att_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // The same, and the values loaded may be used only after it.
@@ -148,6 +139,14 @@ __device__ __forceinline__ void att_wait_ld(uint32_t (&v)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
                    "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+}
+__device__ __forceinline__ void att_wait_ld(uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                   "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                   "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
 __device__ __forceinline__ void att_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -175,71 +174,65 @@ __device__ __forceinline__ uint2 att_codes(uint32_t w)
     return make_uint2(a, b);
 }
 
-// The largest x = s + log2(vs) of a thread's row of S (columns < left where MASK).
-// Sixteen columns are loaded while those before them are worked on (two times 32
-// would not fit the 128 registers of 13 warps).
-template <bool MASK>
-__device__ __forceinline__ float att_top(uint32_t ts, const float4 *inf, int left, float row_f)
+// Half a thread's row of S, columns 64 H .. 64 H + 63.
+__device__ __forceinline__ void att_load_half(uint32_t at, uint32_t (&v)[2][32])
+{
+    att_ld32(at, v[0]);
+    att_ld32(at + 32, v[1]);
+    att_wait_ld(v[0]);
+    att_wait_ld(v[1]);
+}
+
+// The largest x = s + log2(vs) of the half (columns < left where MASK).
+template <bool MASK, int H>
+__device__ __forceinline__ float att_top(const uint32_t (&v)[2][32], const float4 *inf, int left, float row_f)
 {
     float x = -INFINITY;
-    uint32_t v[2][16];
-    att_ld16(ts, v[0]);
 #pragma unroll
-    for (int c = 0; c < 8; c += 2) {
+    for (int c = 0; c < 2; ++c) {
+        const float4 in = inf[2 * H + c];
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            att_wait_ld(v[h]);
-            if (c + h < 7) att_ld16(ts + 16 * (c + h + 1), v[h ^ 1]);
-#pragma unroll
-            for (int y = 0; y < 16; ++y)
-                top[y & 3] = fmaxf(top[y & 3], !MASK || 16 * (c + h) + y < left ? __uint_as_float(v[h][y]) : -INFINITY);
-            __syncwarp();  // the tensor-memory loads want the warp together, whatever became of the choices above
-        }
-        const float4 in = inf[c >> 1];
+        for (int y = 0; y < 32; ++y)
+            top[y & 3] = fmaxf(top[y & 3], !MASK || 64 * H + 32 * c + y < left ? __uint_as_float(v[c][y]) : -INFINITY);
         const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // (32 tokens without a page have in.x < 0)
         if (in.x >= 0.f && (!MASK || most > -INFINITY)) x = fmaxf(x, fmaf(most, row_f * in.x, in.y));
     }
+    __syncwarp();  // the tensor-memory loads want the warp together, whatever became of the choices above
     return x;
 }
 
-// The row's probabilities over S's place; returns their sum over vs.
-template <bool MASK>
-__device__ __forceinline__ float att_probs(uint32_t ts, const float4 *inf, int left, float row_f, float ref)
+// The half's probabilities to tensor memory; returns their sum over vs.
+template <bool MASK, int H>
+__device__ __forceinline__ float att_probs(uint32_t to, const uint32_t (&v)[2][32], const float4 *inf, int left, float row_f,
+                                           float ref)
 {
     float l = 0.f;
-    uint32_t v[2][16];
-    att_ld16(ts, v[0]);
 #pragma unroll
-    for (int c = 0; c < 8; c += 2) {
-        const float4 in = inf[c >> 1];
+    for (int c = 0; c < 2; ++c) {
+        const float4 in = inf[2 * H + c];
         const float f = row_f * in.x, g = in.y - ref;
         float sum[2] = {0.f, 0.f};
+        uint32_t p[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            att_wait_ld(v[h]);
-            if (c + h < 7) att_ld16(ts + 16 * (c + h + 1), v[h ^ 1]);
-            uint32_t p[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                float p0 = att_exp2(fmaf(__uint_as_float(v[h][2 * y]), f, g));
-                float p1 = att_exp2(fmaf(__uint_as_float(v[h][2 * y + 1]), f, g));
-                if (MASK) {
-                    if (16 * (c + h) + 2 * y >= left) p0 = 0.f;
-                    if (16 * (c + h) + 2 * y + 1 >= left) p1 = 0.f;
-                }
-                sum[0] += p0;
-                sum[1] += p1;
-                p[y] = att_f16x2(p0, p1);
+        for (int y = 0; y < 16; ++y) {
+            float p0 = att_exp2(fmaf(__uint_as_float(v[c][2 * y]), f, g));
+            float p1 = att_exp2(fmaf(__uint_as_float(v[c][2 * y + 1]), f, g));
+            if (MASK) {
+                if (64 * H + 32 * c + 2 * y >= left) p0 = 0.f;
+                if (64 * H + 32 * c + 2 * y + 1 >= left) p1 = 0.f;
             }
-            if (in.w == 0.f)  // values of zero, or no page
-#pragma unroll
-                for (int y = 0; y < 8; ++y) p[y] = 0;
-            __syncwarp();
-            att_st8(ts + 8 * (c + h), p);
+            sum[0] += p0;
+            sum[1] += p1;
+            p[y] = att_f16x2(p0, p1);
         }
+        if (in.w == 0.f)  // values of zero, or no page
+#pragma unroll
+            for (int y = 0; y < 16; ++y) p[y] = 0;
         if (in.x >= 0.f) l = fmaf(sum[0] + sum[1], in.z, l);
+        __syncwarp();
+        att_st16(to + 32 * H + 16 * c, p);
     }
     return l;
 }
@@ -351,6 +344,21 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             const uint32_t ts = tmem + lanes + (uint32_t)(tile * 128), to = tmem + lanes + (uint32_t)(256 + tile * 128);
             float m = -INFINITY, l = 0.f;
             const int lim_min = __reduce_min_sync(0xffffffffu, lim);
+            // O *= f, once the products into it so far are done
+            auto rescale = [&](int i, float f) {
+                if (!mbar_wait_warp(pvdone + tile, (i - 1) & 1, &g_att_fault)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t o[16];
+                    att_ld16(to + 16 * c, o);
+                    att_wait_ld(o);
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                    att_st16(to + 16 * c, o);
+                }
+                return true;
+            };
             for (int i = 0; i < steps; ++i) {
                 if (!mbar_wait_warp(sfull + tile, i & 1, &g_att_fault)) {
                     ok = false;
@@ -360,32 +368,35 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                 const float4 *inf = info + (i % kAttInfo) * 4;
                 const bool masked = (i + 1) * kAttTokens > lim_min;
                 const int left = lim - i * kAttTokens;  // columns this row sees
-                float x = masked ? att_top<true>(ts, inf, left, row_f) : att_top<false>(ts, inf, left, row_f);
-                __syncwarp();
-                const bool grow = x > m + 8.f;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float now = grow ? x : m, f = grow ? att_exp2(m - now) : 1.f;
-                    m = now;
-                    l *= f;
-                    if (i > 0) {
-                        if (!mbar_wait_warp(pvdone + tile, (i - 1) & 1, &g_att_fault)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            att_ld32(to + 32 * c, v);
-                            att_wait_ld();
-#pragma unroll
-                            for (int y = 0; y < 32; ++y) v[y] = __float_as_uint(__uint_as_float(v[y]) * f);
-                            att_st32(to + 32 * c, v);
-                        }
+                // The row's second half is looked at first, so that the first is at
+                // hand when the maximum is known: three loads of half a row (a
+                // whole row would not fit the 128 registers of 13 warps).  P's
+                // columns lie below those of S still to be read.
+                auto work = [&](auto mask_c) {
+                    constexpr bool MASK = decltype(mask_c)::value;
+                    uint32_t v[2][32];
+                    att_load_half(ts + 64, v);
+                    float x = att_top<MASK, 1>(v, inf, left, row_f);
+                    att_load_half(ts, v);
+                    x = fmaxf(x, att_top<MASK, 0>(v, inf, left, row_f));
+                    const bool grow = x > m + 8.f;
+                    bool go = true;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float now = grow ? x : m, f = grow ? att_exp2(m - now) : 1.f;
+                        m = now;
+                        l *= f;
+                        if (i > 0) go = rescale(i, f);
                     }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    l += att_probs<MASK, 0>(ts, v, inf, left, row_f, ref);
+                    att_load_half(ts + 64, v);
+                    l += att_probs<MASK, 1>(ts, v, inf, left, row_f, ref);
+                    return go;
+                };
+                if (!(masked ? work(std::true_type{}) : work(std::false_type{}))) {
+                    ok = false;
+                    break;
                 }
-                const float ref = m == -INFINITY ? 0.f : m;
-                l += masked ? att_probs<true>(ts, inf, left, row_f, ref) : att_probs<false>(ts, inf, left, row_f, ref);
                 att_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -429,31 +440,39 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         uint4 rk[NP], rv[NP];
         // Lane c < 4 knows the page of the step's 32 tokens from 32 c on (-1: none),
         // looked up one step ahead of the codes, and the first warp's its scales.
-        float4 next_info = make_float4(-1.f, 0.f, 1.f, 0.f);
+        float2 raw_info = make_float2(-1.f, 0.f);  // ks (-1: no page), vs
         auto pages_of = [&](int i) {
             const int tok = i * kAttTokens + (lane & 3) * 32;
             return tok < seen ? kv8_page(a.v, b, tok >> a.page_log2, &g_att_range) : -1;
         };
+        const unsigned own = (unsigned)(8 * w + r7) * D + c4 * 16;  // of 32 tokens, this thread's first piece
         auto load = [&](const int8_t *codes, int i, int pages, uint4 (&raw)[NP]) {
+            const int8_t *src[4];  // the 32 tokens from 32 y on, null without a page
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int page = __shfl_sync(0xffffffffu, pages, y), slot = (i * kAttTokens + 32 * y) & (a.v.P - 1);
+                src[y] = page < 0 ? nullptr : codes + ((((int64_t)page * H + h) << a.page_log2) + slot) * D + own;
+            }
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
-                const int row = 8 * (4 * (x / S::kHalves) + w) + r7, piece = 4 * (x % S::kHalves) + c4;
-                // rows 8 (4 y + w) .. + 7 lie in the 32 tokens from 32 y on
-                const int page = __shfl_sync(0xffffffffu, pages, x / S::kHalves);
-                raw[x] = page < 0 ? make_uint4(0, 0, 0, 0)
-                                  : __ldg(reinterpret_cast<const uint4 *>(
-                                        codes + ((((int64_t)page * H + h) << a.page_log2) + ((i * kAttTokens + row) & (a.v.P - 1))) * D +
-                                        piece * 16));
+                const int8_t *p = src[x / S::kHalves];
+                raw[x] = make_uint4(0, 0, 0, 0);
+                if (p) raw[x] = __ldg(reinterpret_cast<const uint4 *>(p + (x % S::kHalves) * 64));
             }
         };
         auto load_info = [&](int page) {
-            next_info = make_float4(-1.f, 0.f, 1.f, 0.f);
+            raw_info = make_float2(-1.f, 0.f);
             if (w == 0 && lane < 4 && page >= 0) {
                 const int64_t ph = (int64_t)page * H + h;
+                raw_info = make_float2(__ldg(a.ks + ph), __ldg(a.vs + ph));
+            }
+        };
+        auto store_info = [&](int i) {
+            if (w == 0 && lane < 4) {
                 // a page of zeros (its probabilities still count in the row's
                 // sum) stands with a scale that never leads the maximum
-                const float vs = __ldg(a.vs + ph), e = vs < 0x1p-100f ? 0x1p-60f : vs;
-                next_info = make_float4(fabsf(__ldg(a.ks + ph)), log2f(e), 1.f / e, vs < 0x1p-100f ? 0.f : 1.f);
+                const float vs = raw_info.y, e = vs < 0x1p-100f ? 0x1p-60f : vs;
+                info[(i % kAttInfo) * 4 + lane] = make_float4(raw_info.x, log2f(e), 1.f / e, vs < 0x1p-100f ? 0.f : 1.f);
             }
         };
         auto store = [&](unsigned at, const uint4 (&raw)[NP]) {
@@ -481,7 +500,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             pages = next_pages;  // of step i + 1: none past the last
             next_pages = pages_of(i + 2);
             if (j > 0 && !mbar_wait_warp(kempty + st, (j - 1) & 1, &g_att_fault)) break;
-            if (w == 0 && lane < 4) info[(i % kAttInfo) * 4 + lane] = next_info;
+            store_info(i);
             store(smem0 + S::kK + st * S::kTile, rk);
             if (lane == 0) mbar_arrive(kfull + st);
             load(a.k, i + 1, pages, rk);
