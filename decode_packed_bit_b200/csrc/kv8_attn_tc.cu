@@ -174,67 +174,68 @@ __device__ __forceinline__ uint2 att_codes(uint32_t w)
     return make_uint2(a, b);
 }
 
-// Half a thread's row of S, columns 64 H .. 64 H + 63.
-__device__ __forceinline__ void att_load_half(uint32_t at, uint32_t (&v)[2][32])
+// The largest x = s + log2(vs) of 32 columns of a row (columns < left where MASK).
+template <bool MASK>
+__device__ __forceinline__ float att_top(const uint32_t (&v)[32], const float4 &in, int left, float row_f)
 {
-    att_ld32(at, v[0]);
-    att_ld32(at + 32, v[1]);
-    att_wait_ld(v[0]);
-    att_wait_ld(v[1]);
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int y = 0; y < 32; ++y) top[y & 3] = fmaxf(top[y & 3], !MASK || y < left ? __uint_as_float(v[y]) : -INFINITY);
+    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    // (32 tokens without a page have in.x < 0)
+    return in.x >= 0.f && (!MASK || most > -INFINITY) ? fmaf(most, row_f * in.x, in.y) : -INFINITY;
 }
 
-// The largest x = s + log2(vs) of the half (columns < left where MASK).
-template <bool MASK, int H>
-__device__ __forceinline__ float att_top(const uint32_t (&v)[2][32], const float4 *inf, int left, float row_f)
-{
-    float x = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const float4 in = inf[2 * H + c];
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int y = 0; y < 32; ++y)
-            top[y & 3] = fmaxf(top[y & 3], !MASK || 64 * H + 32 * c + y < left ? __uint_as_float(v[c][y]) : -INFINITY);
-        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        // (32 tokens without a page have in.x < 0)
-        if (in.x >= 0.f && (!MASK || most > -INFINITY)) x = fmaxf(x, fmaf(most, row_f * in.x, in.y));
-    }
-    __syncwarp();  // the tensor-memory loads want the warp together, whatever became of the choices above
-    return x;
-}
-
-// The half's probabilities to tensor memory; returns their sum over vs.
-template <bool MASK, int H>
-__device__ __forceinline__ float att_probs(uint32_t to, const uint32_t (&v)[2][32], const float4 *inf, int left, float row_f,
+// Their probabilities, two a word, and the sum over vs.
+template <bool MASK>
+__device__ __forceinline__ float att_probs(uint32_t (&p)[16], const uint32_t (&v)[32], const float4 &in, int left, float row_f,
                                            float ref)
 {
-    float l = 0.f;
+    const float f = row_f * in.x, g = in.y - ref;
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const float4 in = inf[2 * H + c];
-        const float f = row_f * in.x, g = in.y - ref;
-        float sum[2] = {0.f, 0.f};
-        uint32_t p[16];
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-            float p0 = att_exp2(fmaf(__uint_as_float(v[c][2 * y]), f, g));
-            float p1 = att_exp2(fmaf(__uint_as_float(v[c][2 * y + 1]), f, g));
-            if (MASK) {
-                if (64 * H + 32 * c + 2 * y >= left) p0 = 0.f;
-                if (64 * H + 32 * c + 2 * y + 1 >= left) p1 = 0.f;
-            }
-            sum[0] += p0;
-            sum[1] += p1;
-            p[y] = att_f16x2(p0, p1);
+    for (int y = 0; y < 16; ++y) {
+        float p0 = att_exp2(fmaf(__uint_as_float(v[2 * y]), f, g));
+        float p1 = att_exp2(fmaf(__uint_as_float(v[2 * y + 1]), f, g));
+        if (MASK) {
+            if (2 * y >= left) p0 = 0.f;
+            if (2 * y + 1 >= left) p1 = 0.f;
         }
-        if (in.w == 0.f)  // values of zero, or no page
-#pragma unroll
-            for (int y = 0; y < 16; ++y) p[y] = 0;
-        if (in.x >= 0.f) l = fmaf(sum[0] + sum[1], in.z, l);
-        __syncwarp();
-        att_st16(to + 32 * H + 16 * c, p);
+        sum[0] += p0;
+        sum[1] += p1;
+        p[y] = att_f16x2(p0, p1);
     }
-    return l;
+    if (in.w == 0.f)  // values of zero, or no page
+#pragma unroll
+        for (int y = 0; y < 16; ++y) p[y] = 0;
+    return in.x >= 0.f ? (sum[0] + sum[1]) * in.z : 0.f;
+}
+
+// Two tiles' rows of a sequence: rows [i0, i0 + rows) of sequence b, whose last sees
+// `seen` tokens, in `steps` steps.  rows = 0: an item past a sequence's rows.
+struct AttUnit {
+    int b, i0, rows, seen, steps;
+    Kv8Seq s;
+};
+__device__ __forceinline__ AttUnit att_unit(const Kv8AttnTc &a, int item)
+{
+    AttUnit u = {};
+    const int pair = 2 * a.tokens;
+    int nth = 0;
+    u.b = item;
+    if (a.v.row_start) {
+        u.b = kv8_find_seq(a.v, item, pair, 1);
+        if (u.b < 0) return u;
+        nth = item - (max(__ldg(a.v.row_start + u.b), 0) / pair + u.b);
+    }
+    u.s = kv8_seq(a.v, u.b, &g_att_range);
+    const int64_t i0 = (int64_t)nth * pair;
+    if (i0 >= u.s.n) return u;
+    u.i0 = (int)i0;
+    u.rows = min(pair, u.s.n - u.i0);
+    u.seen = min(max(u.s.len - u.s.n + u.i0 + u.rows, 0), u.s.len);
+    u.steps = (u.seen + kAttTokens - 1) / kAttTokens;
+    return u;
 }
 
 template <int D>
@@ -253,23 +254,36 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
     pdl_launch_dependents();
     pdl_wait_primary();
 
-    // ---- the unit: later rows (more tokens to see) first ----
-    const int H = a.v.H, item = (int)((a.items - 1) - blockIdx.x / H), h = blockIdx.x % H;
-    const int pair = 2 * a.tokens;
-    int b = item, nth = 0;
-    if (a.v.row_start) {
-        b = kv8_find_seq(a.v, item, pair, 1);
-        if (b < 0) return;
-        nth = item - (max(__ldg(a.v.row_start + b), 0) / pair + b);
+    // ---- the unit: those with more tokens to see first ----
+    const int H = a.v.H, h = blockIdx.x % H;
+    int item = (int)((a.items - 1) - blockIdx.x / H);  // within a sequence that is the order already
+    if (a.v.n_seqs > 1 && a.items <= kAttThreads) {
+        // between sequences it is not: every CTA ranks the items by their steps
+        // (in the order of the rows, the longest sequence's could come last, and
+        // the SMs wait for them: 757 against 620 us for the three prompts below)
+        int *cost = reinterpret_cast<int *>(smem);
+        if (threadIdx.x < kAttThreads) cost[threadIdx.x] = (int)threadIdx.x < a.items ? att_unit(a, threadIdx.x).steps : -1;
+        __syncthreads();
+        const int mine = cost[threadIdx.x];
+        int rank = 0;
+        for (int u = 0; u < a.items; u += 4) {
+            const int4 c = reinterpret_cast<const int4 *>(cost)[u / 4];
+            const int t = (int)threadIdx.x - u;  // equal ones in order
+            rank += c.x > mine || (c.x == mine && t > 0);
+            rank += c.y > mine || (c.y == mine && t > 1);
+            rank += c.z > mine || (c.z == mine && t > 2);
+            rank += c.w > mine || (c.w == mine && t > 3);
+        }
+        if ((int)threadIdx.x < a.items && rank == (int)(blockIdx.x / H)) cost[kAttThreads] = threadIdx.x;
+        __syncthreads();
+        item = cost[kAttThreads];
+        __syncthreads();  // its place is q's
     }
-    const Kv8Seq s = kv8_seq(a.v, b, &g_att_range);
-    const int64_t i64 = (int64_t)nth * pair;
-    if (i64 >= s.n) return;
-    const int i0 = (int)i64;                                     // first row of the unit
-    const int rows = min(pair, s.n - i0);
+    const AttUnit unit = att_unit(a, item);
+    if (unit.rows == 0) return;
+    const Kv8Seq &s = unit.s;
+    const int b = unit.b, i0 = unit.i0, rows = unit.rows, seen = unit.seen, steps = unit.steps;
     const bool two = rows > a.tokens;
-    const int seen = min(max(s.len - s.n + i0 + rows, 0), s.len);  // by its last row
-    const int steps = (seen + kAttTokens - 1) / kAttTokens;
 
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -368,34 +382,41 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                 const float4 *inf = info + (i % kAttInfo) * 4;
                 const bool masked = (i + 1) * kAttTokens > lim_min;
                 const int left = lim - i * kAttTokens;  // columns this row sees
-                // The row's second half is looked at first, so that the first is at
-                // hand when the maximum is known: three loads of half a row (a
-                // whole row would not fit the 128 registers of 13 warps).  P's
-                // columns lie below those of S still to be read.
-                auto work = [&](auto mask_c) {
-                    constexpr bool MASK = decltype(mask_c)::value;
-                    uint32_t v[2][32];
-                    att_load_half(ts + 64, v);
-                    float x = att_top<MASK, 1>(v, inf, left, row_f);
-                    att_load_half(ts, v);
-                    x = fmaxf(x, att_top<MASK, 0>(v, inf, left, row_f));
-                    const bool grow = x > m + 8.f;
-                    bool go = true;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float now = grow ? x : m, f = grow ? att_exp2(m - now) : 1.f;
-                        m = now;
-                        l *= f;
-                        if (i > 0) go = rescale(i, f);
+                // 32 columns at a time, in loops that are not unrolled: the roles'
+                // code together has to stay in the SM's instruction cache (with
+                // both passes unrolled, masked and not, it was fetched from the
+                // GPC's cache over and over, which bound the kernel)
+                float x = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    att_ld32(ts + 32 * c, v);
+                    const float4 in = inf[c];
+                    att_wait_ld(v);
+                    x = fmaxf(x, masked ? att_top<true>(v, in, left - 32 * c, row_f) : att_top<false>(v, in, left - 32 * c, row_f));
+                    __syncwarp();
+                }
+                const bool grow = x > m + 8.f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float now = grow ? x : m, f = grow ? att_exp2(m - now) : 1.f;
+                    m = now;
+                    l *= f;
+                    if (i > 0 && !rescale(i, f)) {
+                        ok = false;
+                        break;
                     }
-                    const float ref = m == -INFINITY ? 0.f : m;
-                    l += att_probs<MASK, 0>(ts, v, inf, left, row_f, ref);
-                    att_load_half(ts + 64, v);
-                    l += att_probs<MASK, 1>(ts, v, inf, left, row_f, ref);
-                    return go;
-                };
-                if (!(masked ? work(std::true_type{}) : work(std::false_type{}))) {
-                    ok = false;
-                    break;
+                }
+                const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {  // P's columns lie below those of S still to be read
+                    uint32_t v[32], p[16];
+                    att_ld32(ts + 32 * c, v);
+                    const float4 in = inf[c];
+                    att_wait_ld(v);
+                    l += masked ? att_probs<true>(p, v, in, left - 32 * c, row_f, ref)
+                                : att_probs<false>(p, v, in, left - 32 * c, row_f, ref);
+                    __syncwarp();
+                    att_st16(ts + 16 * c, p);
                 }
                 att_wait_st();
                 tc_fence_before();
@@ -491,24 +512,30 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
         };
-        int pages = pages_of(0), next_pages = pages_of(1);
-        load(a.k, 0, pages, rk);
-        load_info(pages);
-        load(a.vv, 0, pages, rv);
-        for (int i = 0; i < steps; ++i) {
-            const int st = i & 1, j = i >> 1;
-            pages = next_pages;  // of step i + 1: none past the last
-            next_pages = pages_of(i + 2);
-            if (j > 0 && !mbar_wait_warp(kempty + st, (j - 1) & 1, &g_att_fault)) break;
-            store_info(i);
-            store(smem0 + S::kK + st * S::kTile, rk);
-            if (lane == 0) mbar_arrive(kfull + st);
-            load(a.k, i + 1, pages, rk);
-            load_info(pages);
-            if (j > 0 && !mbar_wait_warp(vempty + st, (j - 1) & 1, &g_att_fault)) break;
-            store(smem0 + S::kV + st * S::kTile, rv);
-            if (lane == 0) mbar_arrive(vfull + st);
-            load(a.vv, i + 1, pages, rv);
+        // Keys run a step ahead of values: the scores of step i + 1 are issued with
+        // P V of step i.
+        int page_k = pages_of(0), page_v = page_k;  // of the keys, of the values loaded next
+        load(a.k, 0, page_k, rk);
+        load_info(page_k);
+        for (int i = 0; i <= steps; ++i) {
+            // keys of step i, values of step i - 1
+            const int next = pages_of(i + 1);
+            if (i < steps) {
+                if (i > 1 && !mbar_wait_warp(kempty + (i & 1), ((i >> 1) - 1) & 1, &g_att_fault)) break;
+                store_info(i);
+                store(smem0 + S::kK + (i & 1) * S::kTile, rk);
+                if (lane == 0) mbar_arrive(kfull + (i & 1));
+                load(a.k, i + 1, next, rk);
+                load_info(next);
+            }
+            if (i > 0) {
+                const int o = i - 1;
+                if (o > 1 && !mbar_wait_warp(vempty + (o & 1), ((o >> 1) - 1) & 1, &g_att_fault)) break;
+                store(smem0 + S::kV + (o & 1) * S::kTile, rv);
+                if (lane == 0) mbar_arrive(vfull + (o & 1));
+            }
+            load(a.vv, i, page_v, rv);
+            page_v = next;
         }
     } else {
         // ---- MMAs: f16 operands, fp32 sums, M = 128 ----
