@@ -73,6 +73,24 @@ struct AttnTc {
     static constexpr unsigned kTmem = 512;                 // S 0, S 1, O 0, O 1
 };
 
+// Wait for a phase with the whole warp polling: 110 clocks from the arrival to
+// going on, against 250 when lane 0 polls and the warp votes on its verdict; a
+// step has several such hand-offs in a row.  Bounded as mbar_wait is.
+__device__ __forceinline__ bool att_wait(uint64_t *bar, unsigned parity)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kTcWaitNs)) {
+            atomicExch(&g_att_fault, 1u);
+            return false;
+        }
+    }
+}
+
 // Shared-memory descriptors, 128-byte swizzle.  K-major: rows 128 bytes apart,
 // 8-row groups 1024.
 __device__ __forceinline__ uint64_t att_desc_k(unsigned addr)
@@ -360,7 +378,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             const int lim_min = __reduce_min_sync(0xffffffffu, lim);
             // O *= f, once the products into it so far are done
             auto rescale = [&](int i, float f) {
-                if (!mbar_wait_warp(pvdone + tile, (i - 1) & 1, &g_att_fault)) return false;
+                if (!att_wait(pvdone + tile, (i - 1) & 1)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
@@ -374,7 +392,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                 return true;
             };
             for (int i = 0; i < steps; ++i) {
-                if (!mbar_wait_warp(sfull + tile, i & 1, &g_att_fault)) {
+                if (!att_wait(sfull + tile, i & 1)) {
                     ok = false;
                     break;
                 }
@@ -423,7 +441,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(pready + tile);
             }
-            if (ok && steps > 0) ok = mbar_wait_warp(pvdone + tile, (steps - 1) & 1, &g_att_fault);
+            if (ok && steps > 0) ok = att_wait(pvdone + tile, (steps - 1) & 1);
             tc_fence_after();
             if (ok) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -521,7 +539,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             // keys of step i, values of step i - 1
             const int next = pages_of(i + 1);
             if (i < steps) {
-                if (i > 1 && !mbar_wait_warp(kempty + (i & 1), ((i >> 1) - 1) & 1, &g_att_fault)) break;
+                if (i > 1 && !att_wait(kempty + (i & 1), ((i >> 1) - 1) & 1)) break;
                 store_info(i);
                 store(smem0 + S::kK + (i & 1) * S::kTile, rk);
                 if (lane == 0) mbar_arrive(kfull + (i & 1));
@@ -530,7 +548,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             }
             if (i > 0) {
                 const int o = i - 1;
-                if (o > 1 && !mbar_wait_warp(vempty + (o & 1), ((o >> 1) - 1) & 1, &g_att_fault)) break;
+                if (o > 1 && !att_wait(vempty + (o & 1), ((o >> 1) - 1) & 1)) break;
                 store(smem0 + S::kV + (o & 1) * S::kTile, rv);
                 if (lane == 0) mbar_arrive(vfull + (o & 1));
             }
@@ -586,13 +604,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         auto step = [&](auto tile_c, auto stage_c, int i) {
             constexpr int q = decltype(tile_c)::value, st = decltype(stage_c)::value;
             if (i >= 0) {
-                if (!mbar_wait_warp(pready + q, i & 1, &g_att_fault)) return false;
-                if (q == 0 && !mbar_wait_warp(vfull + st, (i >> 1) & 1, &g_att_fault)) return false;
+                if (!att_wait(pready + q, i & 1)) return false;
+                if (q == 0 && !att_wait(vfull + st, (i >> 1) & 1)) return false;
                 tc_fence_after();
                 values(tile_c, stage_c, i == 0);
             }
             if (i + 1 < last) {
-                if (q == 0 && !mbar_wait_warp(kfull + (st ^ 1), ((i + 1) >> 1) & 1, &g_att_fault)) return false;
+                if (q == 0 && !att_wait(kfull + (st ^ 1), ((i + 1) >> 1) & 1)) return false;
                 tc_fence_after();
                 scores(tile_c, std::integral_constant<int, st ^ 1>{});
             }
@@ -609,7 +627,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         // completed, before tensor memory is released
         if (elect_one()) umma_commit(done);
         __syncwarp();
-        mbar_wait_warp(done, 0, &g_att_fault);
+        att_wait(done, 0);
     }
     tc_fence_before();
     __syncthreads();
