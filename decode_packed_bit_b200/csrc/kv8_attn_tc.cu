@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
     float4 *info = reinterpret_cast<float4 *>(smem + S::kInfoAt);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + S::kBars);
     uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6;
-    uint64_t *sfull = bars + 8, *pready = bars + 10, *pvdone = bars + 12, *done = bars + 14;
+    uint64_t *sfull = bars + 8, *pready = bars + 10, *pvdone = bars + 12, *done = bars + 14, *qfull = bars + 15;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_launch_dependents();
@@ -314,9 +314,15 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             mbar_init(pvdone + x, 1);
         }
         mbar_init(done, 1);
+        mbar_init(qfull, kAttConvWarp);
         mbar_fence_init();
     }
     if (warp == kAttMmaWarp) tmem_alloc(tmem_slot, S::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
 
     // ---- q of a thread's row into shared memory ----
     const int tile = warp >> 2;  // softmax warps
@@ -333,17 +339,24 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             qp = a.q + row * a.q_stride + col;
             out_at = row * a.out_stride + col;
         }
+        // the row twice, 128 bytes of it at a time (all of it in registers would
+        // spill): its largest value, then its entries
         float top = 0.f;
         bool bad = false;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+            uint4 u[8];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const float f0 = fabsf(__uint_as_float(w[y] << 16)), f1 = fabsf(__uint_as_float(w[y] & 0xFFFF0000u));
-                top = fmaxf(top, fmaxf(f0, f1));
-                bad |= !(f0 <= FLT_MAX) || !(f1 <= FLT_MAX);
+            for (int c = 0; c < 8; ++c) u[c] = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float f0 = fabsf(__uint_as_float(w[y] << 16)), f1 = fabsf(__uint_as_float(w[y] & 0xFFFF0000u));
+                    top = fmaxf(top, fmaxf(f0, f1));
+                    bad |= !(f0 <= FLT_MAX) || !(f1 <= FLT_MAX);
+                }
             }
         }
         // the power of two at or below the largest value (2^126 for 2^127, too)
@@ -352,25 +365,24 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         const float down = some ? __uint_as_float((254u - e) << 23) * a.sign : 0.f;
         row_f = bad && lim > 0 ? NAN : some ? __uint_as_float(e << 23) * a.scale_log2 : 0.f;
         uint8_t *qs = smem + S::kQ + tile * S::kTile + r * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c) : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            uint32_t o[4];
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+            uint4 u[8];
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-                o[y] = some ? att_f16x2(__uint_as_float(w[y] << 16) * down, __uint_as_float(w[y] & 0xFFFF0000u) * down) : 0u;
-            *reinterpret_cast<uint4 *>(qs + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int c = 0; c < 8; ++c) u[c] = valid ? __ldg(reinterpret_cast<const uint4 *>(qp) + c0 + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t w[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    o[y] = some ? att_f16x2(__uint_as_float(w[y] << 16) * down, __uint_as_float(w[y] & 0xFFFF0000u) * down) : 0u;
+                *reinterpret_cast<uint4 *>(qs + (c0 >> 3) * 16384 + ((c ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    bool ok = true;
-
-    if (warp < kAttConvWarp) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qfull);
         if (tile == 0 || two) {
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t ts = tmem + lanes + (uint32_t)(tile * 128), to = tmem + lanes + (uint32_t)(256 + tile * 128);
@@ -618,7 +630,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         };
         using C0 = std::integral_constant<int, 0>;
         using C1 = std::integral_constant<int, 1>;
-        for (int i = -1; i < last; i += 2) {  // odd steps lie in stage 1
+        bool go = att_wait(qfull, 0);
+        for (int i = -1; go && i < last; i += 2) {  // odd steps lie in stage 1
             if (!step(C0{}, C1{}, i) || (both && !step(C1{}, C1{}, i))) break;
             if (i + 1 >= last) break;
             if (!step(C0{}, C0{}, i + 1) || (both && !step(C1{}, C0{}, i + 1))) break;
