@@ -338,20 +338,27 @@ LOWBIT_F32 = 0
 LOWBIT_BF16 = 1
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 _types = {}  # torch dtypes of the operands that may be either -> lowbit_dtype
+_float32 = _bfloat16 = _int32 = _int64 = _int16 = _int8 = None  # torch's, set on the first call (torch is imported late)
 
 
-def _device() -> int:
-    """The current CUDA device; every operand has to be there."""
+def _first_call():
     import torch
-    if not _types:
-        _types.update({torch.float32: LOWBIT_F32, torch.bfloat16: LOWBIT_BF16})
-    return torch.cuda.current_device()
+    global _float32, _bfloat16, _int32, _int64, _int16, _int8, _device, _current_stream
+    torch.cuda.init()
+    _float32, _bfloat16 = torch.float32, torch.bfloat16
+    _int32, _int64, _int16, _int8 = torch.int32, torch.int64, torch.int16, torch.int8
+    _types.update({_float32: LOWBIT_F32, _bfloat16: LOWBIT_BF16})
+    _device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _device()
+
+
+_device = _first_call  # the current CUDA device; every operand has to be there
+_current_stream = None
 
 
 def _raw_stream(stream, dev):
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -368,16 +375,19 @@ def _dense(t, dtype, shape, what, dev):
 
 def _bits16(t, shape, what, dev):
     """The same for bf16 values, as such or as int16 bit patterns."""
-    import torch
-    return _dense(t, torch.int16 if t.dtype is torch.int16 else torch.bfloat16, shape, what, dev)
+    return _dense(t, _int16 if t.dtype is _int16 else _bfloat16, shape, what, dev)
 
 
 def _rows(t, dtype, shape, what, dev):
     """Address and row stride of a [rows][heads][dim] tensor whose rows are dense and may lie apart."""
-    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if t.dtype is not dtype or t.shape != shape or s2 != 1 or (s1 != shape[2] and shape[1] > 1) or t.get_device() != dev:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _refuse(t, what, f"a {dtype} tensor of shape {shape} with dense rows on cuda:{dev}")
-    return t.data_ptr(), s0 if shape[0] > 1 else shape[1] * shape[2]
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2]
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
+        _refuse(t, what, f"a {dtype} tensor of shape {shape} with dense rows on cuda:{dev}")
+    return t.data_ptr(), s0
 
 
 def _either(t, what):
@@ -400,8 +410,7 @@ def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, works
     x bf16 [M][K], ids int32 [M]; a, b, base, ys: equal-length lists of bf16 [L][rank][K], bf16 [L][N][rank],
     fp32 [M][N] and fp32 [M][N] (base_r may be y_r itself); ranks int32 [L] and scales fp32 [L], or None.
     workspace: lowbit_lora_workspace_bytes(R, M, N, K, rank) bytes."""
-    import torch
-    dev, f32 = _device(), torch.float32
+    dev = _device()
     R = len(a)
     if not 1 <= R == len(b) == len(base) == len(ys):
         raise ValueError("lowbit_lora_add_group: lists of different lengths")
@@ -410,11 +419,11 @@ def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, works
     N = b[0].shape[1]
     sa, sb, sy, sl = (L, rank, K), (L, N, rank), (M, N), (L,)
     _check(lib().lowbit_lora_add_group(
-        _bits16(x, (M, K), "x", dev), _dense(ids, torch.int32, (M,), "ids", dev),
+        _bits16(x, (M, K), "x", dev), _dense(ids, _int32, (M,), "ids", dev),
         _ptrs([_bits16(t, sa, "a", dev) for t in a]), _ptrs([_bits16(t, sb, "b", dev) for t in b]),
-        None if ranks is None else _dense(ranks, torch.int32, sl, "ranks", dev),
-        None if scales is None else _dense(scales, f32, sl, "scales", dev),
-        _ptrs([_dense(t, f32, sy, "base", dev) for t in base]), _ptrs([_dense(t, f32, sy, "y", dev) for t in ys]),
+        None if ranks is None else _dense(ranks, _int32, sl, "ranks", dev),
+        None if scales is None else _dense(scales, _float32, sl, "scales", dev),
+        _ptrs([_dense(t, _float32, sy, "base", dev) for t in base]), _ptrs([_dense(t, _float32, sy, "y", dev) for t in ys]),
         R, M, N, K, rank, L, None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
         _raw_stream(stream, dev)), "lowbit_lora_add_group")
 
@@ -439,7 +448,6 @@ def lowbit_rope_phases(rot: int, base: float = 10000.0, scaling="plain", factor:
 def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnitude=1.0, stream=None):
     """q [M][q_heads][D] -> q_out and k [M][kv_heads][D] -> k_out (either pair may be None), fp32 or bf16, rows dense
     and any stride (a multiple of 8) apart; positions int32 [M]; phases int64 [rot / 2].  In place where types match."""
-    import torch
     dev = _device()
     ref, ref_out = (q, q_out) if q is not None else (k, k_out)
     M, _, D = ref.shape
@@ -456,8 +464,8 @@ def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnit
         kp, ks = _rows(k, ref.dtype, (M, kh, D), "k", dev)
         ko, kos = _rows(k_out, ref_out.dtype, (M, kh, D), "k_out", dev)
     _check(lib().lowbit_rope(qp, qs, qo, qos, qh, kp, ks, ko, kos, kh, ti, to,
-                             _dense(positions, torch.int32, (M,), "positions", dev),
-                             _dense(phases, torch.int64, (half,), "phases", dev), M, D, 2 * half,
+                             _dense(positions, _int32, (M,), "positions", dev),
+                             _dense(phases, _int64, (half,), "phases", dev), M, D, 2 * half,
                              1 if interleaved else 0, magnitude, _raw_stream(stream, dev)), "lowbit_rope")
 
 
@@ -478,13 +486,12 @@ class KV8Cache:
     [n_pages][n_heads].  Holds them alive; a call reads or writes them in place."""
 
     def __init__(self, k, k_scales, v, v_scales):
-        import torch
         dev = _device()
         n_pages, heads, page, dim = k.shape
-        self._c = _KV8CacheC(_dense(k, torch.int8, (n_pages, heads, page, dim), "k", dev),
-                             _dense(k_scales, torch.float32, (n_pages, heads), "k_scales", dev),
-                             _dense(v, torch.int8, (n_pages, heads, page, dim), "v", dev),
-                             _dense(v_scales, torch.float32, (n_pages, heads), "v_scales", dev), n_pages, heads, page,
+        self._c = _KV8CacheC(_dense(k, _int8, (n_pages, heads, page, dim), "k", dev),
+                             _dense(k_scales, _float32, (n_pages, heads), "k_scales", dev),
+                             _dense(v, _int8, (n_pages, heads, page, dim), "v", dev),
+                             _dense(v_scales, _float32, (n_pages, heads), "v_scales", dev), n_pages, heads, page,
                              dim)
         self._ref = ctypes.byref(self._c)
         self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
@@ -504,8 +511,7 @@ class KV8Cache:
 
 
 def _kv8_batch(cache, page_table, kv_len, row_start, rows, dev):
-    import torch
-    i32 = torch.int32
+    i32 = _int32
     B, width = page_table.shape
     if cache.device != dev:
         raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
@@ -555,13 +561,12 @@ def lowbit_kv8_attention(cache: KV8Cache, page_table, kv_len, q, out, scale, row
     q, out bf16 [rows][q_heads][head_dim], rows dense and any stride (a multiple of 8) apart; page_table, kv_len and
     row_start as for lowbit_kv8_append.  workspace: lowbit_kv8_attention_workspace_bytes(...) bytes, zero-filled before
     their first use."""
-    import torch
     dev = _device()
     rows, heads, _ = q.shape
     shape = (rows, heads, cache.head_dim)
     batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
-    qp, qs = _rows(q, torch.bfloat16, shape, "q", dev)
-    op, os_ = _rows(out, torch.bfloat16, shape, "out", dev)
+    qp, qs = _rows(q, _bfloat16, shape, "q", dev)
+    op, os_ = _rows(out, _bfloat16, shape, "out", dev)
     _check(lib().lowbit_kv8_attention(cache._ref, ctypes.byref(batch), qp, qs, heads, scale, op, os_,
                                       None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
                                       _raw_stream(stream, dev)), "lowbit_kv8_attention")
