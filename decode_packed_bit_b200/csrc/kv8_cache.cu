@@ -10,10 +10,11 @@
 // bits on every run, whatever the launch shape.
 //
 // Bound by HBM for prompts (each new value read, a byte written) and by latency
-// for a decode step.  One group of threads takes one (page, head, k or v): a
-// warp where a call brings about a token per sequence, a CTA where it brings
-// whole pages.  The values are read twice (the second time from the L1 or L2
-// cache): the scale has to be known before the first code.
+// for a decode step.  One CTA takes one (page, head, k or v).  For prompts it
+// has a thread per 32 values, which stay in registers between the maximum and
+// the codes (reading them twice took 66 us where this takes FIXME); for a decode
+// step 128 threads, which one token leaves idle but a growing scale does not:
+// the page's older codes are then rewritten.
 #include <cfloat>
 
 #include "kv8_common.cuh"
@@ -30,7 +31,7 @@ int kv8_fault_flag()
     return (int)v;
 }
 
-constexpr int kKvThreads = 256;
+constexpr int kKvThreads = 256;  // of the read
 
 struct Kv8Append {
     Kv8View v;
@@ -39,7 +40,6 @@ struct Kv8Append {
     const void *x[2];
     int64_t stride[2];
     int bf16[2];
-    int items;
 };
 
 // Eight consecutive values as floats; NaN becomes 0 and infinities the largest
@@ -74,20 +74,28 @@ __device__ __forceinline__ int kv8_code(float x, float s, float inv)
     return (int)fminf(fmaxf(q, -127.f), 127.f);
 }
 
-template <int G>  // threads per (page, head, k or v): 32 or kKvThreads
-__global__ void __launch_bounds__(kKvThreads) k_kv8_append(const Kv8Append a)
+// rint(c * ratio), exactly, ratio = was / now.
+__device__ __forceinline__ int kv8_recode(int c, float ratio, double was, double now)
 {
-    __shared__ float red[kKvThreads / 32];
+    const float t = (float)c * ratio;
+    float q = rintf(t);
+    if (!(fabsf(t - q) <= 0.4999f)) q = (float)rint(c * was / now);
+    return (int)q;
+}
+
+// G threads; each keeps its first NC pieces of 8 values in registers and reads
+// further ones again.
+template <int G, int NC>
+__global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
+{
+    __shared__ float red[G / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
     const Kv8View &v = a.v;
-    const int64_t task = (int64_t)blockIdx.x * (kKvThreads / G) + threadIdx.x / G;
-    const int t = threadIdx.x % G;
-    const int h = (int)(task % v.H), which = (int)(task / v.H % 2);
-    const int64_t item = task / (2 * v.H);
-    if (item >= a.items) return;  // whole groups leave, so what follows is uniform in a group
-    // the item's sequence, and which of its touched pages
-    const int b = v.row_start ? kv8_find_seq(v, (int)item, v.P, 2) : (int)item;
+    const int t = threadIdx.x;
+    const int h = blockIdx.x % v.H, which = blockIdx.x / v.H % 2, item = blockIdx.x / (2 * v.H);
+    // the item's sequence, and which of its touched pages (all uniform in the CTA)
+    const int b = v.row_start ? kv8_find_seq_warp(v, item, v.P, 2) : item;
     if (b < 0) return;
     const Kv8Seq s = kv8_seq(v, b, &g_kv8_fault);
     const int nth = v.row_start ? (int)(item - (max(__ldg(v.row_start + b), 0) / v.P + 2 * (int64_t)b)) : 0;
@@ -95,62 +103,73 @@ __global__ void __launch_bounds__(kKvThreads) k_kv8_append(const Kv8Append a)
     const int64_t j64 = (int64_t)first / v.P + nth;
     if (s.n == 0 || j64 * v.P >= s.len) return;
     const int j = (int)j64;
-    const int page = kv8_page(v, b, j, &g_kv8_fault);
-    if (page < 0) return;
     const int lo = max(first, j * v.P), hi = min(s.len, (j + 1) * v.P);
     const int older = lo - j * v.P, D8 = v.D / 8, n8 = (hi - lo) * D8;
-    const int64_t r0 = s.r0 + (lo - p0);
-    const void *x = a.x[which];
-    const int64_t stride = a.stride[which];
-    const int bf16 = a.bf16[which];
-    int8_t *codes = a.codes[which] + ((int64_t)page * v.H + h) * v.P * v.D;
-    float *scale = a.scales[which] + (int64_t)page * v.H + h;
-
+    const int64_t stride = which ? a.stride[1] : a.stride[0], at0 = (s.r0 + (int64_t)(lo - p0)) * stride + (int64_t)h * v.D;
+    const void *x = which ? a.x[1] : a.x[0];
+    const int bf16 = which ? a.bf16[1] : a.bf16[0];
+    float f[NC][8];
     float top = 0.f;
-    for (int i = t; i < n8; i += G) {
-        float f[8];
-        kv8_load8(x, (r0 + i / D8) * stride + (int64_t)h * v.D + i % D8 * 8, bf16, f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[k]));
+    for (int c = 0; c < NC; ++c) {
+        const int i = t + c * G;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[c][k] = 0.f;
+        if (i < n8) kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, f[c]);
     }
+    const int page = kv8_page(v, b, j, &g_kv8_fault);
+    if (page < 0) return;
+    int8_t *codes = (which ? a.codes[1] : a.codes[0]) + ((int64_t)page * v.H + h) * v.P * v.D;
+    float *scale = (which ? a.scales[1] : a.scales[0]) + (int64_t)page * v.H + h;
     const float was = older ? fmaxf(*scale, 0.f) : 0.f;
-    top = warp_max_nonneg(top);
-    if constexpr (G > 32) {
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-        __syncthreads();
-        top = red[0];
 #pragma unroll
-        for (int i = 1; i < kKvThreads / 32; ++i) top = fmaxf(top, red[i]);
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[c][k]));
+    for (int i = t + NC * G; i < n8; i += G) {
+        float g[8];
+        kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(g[k]));
     }
+    top = warp_max_nonneg(top);
+    if ((t & 31) == 0) red[t >> 5] = top;
+    __syncthreads();  // also: every thread has read the old scale
+#pragma unroll
+    for (int i = 0; i < G / 32; ++i) top = fmaxf(top, red[i]);
     const float now = fmaxf(was, __fdiv_rn(top, 127.f));
     const float inv = now > 0.f ? __frcp_rn(now) : 0.f;
     if (now > was) {
-        const double wd = was, nd = now;
+        const float ratio = __fdiv_rn(was, now);
+#pragma unroll 4
         for (int i = t; i < older * v.D / 16; i += G) {
-            uint4 u = reinterpret_cast<const uint4 *>(codes)[i];
+            const uint4 u = reinterpret_cast<const uint4 *>(codes)[i];
             uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 uint32_t o = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = (int8_t)(w[k] >> (8 * e));
-                    o |= ((uint32_t)(int)rint(c * wd / nd) & 0xFFu) << (8 * e);
-                }
+                for (int e = 0; e < 4; ++e)
+                    o |= ((uint32_t)kv8_recode((int8_t)(w[k] >> (8 * e)), ratio, was, now) & 0xFFu) << (8 * e);
                 w[k] = o;
             }
             reinterpret_cast<uint4 *>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    for (int i = t; i < n8; i += G) {
-        float f[8];
-        kv8_load8(x, (r0 + i / D8) * stride + (int64_t)h * v.D + i % D8 * 8, bf16, f);
+    auto put = [&](int i, const float (&g)[8]) {
         uint32_t o[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k / 4] |= ((uint32_t)kv8_code(f[k], now, inv) & 0xFFu) << (8 * (k % 4));
+        for (int k = 0; k < 8; ++k) o[k / 4] |= ((uint32_t)kv8_code(g[k], now, inv) & 0xFFu) << (8 * (k % 4));
         reinterpret_cast<uint2 *>(codes)[older * D8 + i] = make_uint2(o[0], o[1]);
+    };
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+        if (t + c * G < n8) put(t + c * G, f[c]);
+    for (int i = t + NC * G; i < n8; i += G) {
+        float g[8];
+        kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, g);
+        put(i, g);
     }
-    __syncwarp();  // G = 32: every lane has read the old scale
     if (t == 0) *scale = now;
 }
 
@@ -167,16 +186,17 @@ lowbit_status kv8_append_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batc
     a.bf16[0] = k_type == LOWBIT_BF16; a.bf16[1] = v_type == LOWBIT_BF16;
     // touched pages, at most: see kv8_find_seq (n rows touch n / P + 2 or fewer)
     const int64_t items = b.row_start ? (int64_t)b.n_rows / c.page_tokens + 2 * (int64_t)b.n_seqs : b.n_seqs;
-    if (items >= (int64_t(1) << 31)) return LOWBIT_ERR_UNSUPPORTED_SHAPE;
-    a.items = (int)items;
-    const int64_t tasks = items * 2 * c.n_heads;
-    // one warp per page where a call brings few tokens per sequence
-    const bool few = b.n_rows <= 4 * (int64_t)b.n_seqs;
-    const int per = few ? kKvThreads / 32 : 1;
-    const int64_t grid = (tasks + per - 1) / per;
+    const int64_t grid = items * 2 * c.n_heads;
     if (grid >= (int64_t(1) << 31)) return LOWBIT_ERR_UNSUPPORTED_SHAPE;
-    const cudaError_t e = launch_pdl(few ? k_kv8_append<32> : k_kv8_append<kKvThreads>, dim3((unsigned)grid),
-                                     dim3(kKvThreads), 0, st, a);
+    // a decode step: about a token per sequence; else a thread per 32 values of a page
+    const bool few = b.n_rows <= 4 * (int64_t)b.n_seqs;
+    const int G = few ? 128 : c.page_tokens * c.head_dim / 32;
+    void (*kern)(const Kv8Append) = few        ? k_kv8_append<128, 1>
+                                    : G == 64  ? k_kv8_append<64, 4>
+                                    : G == 128 ? k_kv8_append<128, 4>
+                                    : G == 256 ? k_kv8_append<256, 4>
+                                               : k_kv8_append<512, 4>;
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), dim3(G), 0, st, a);
     return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 
@@ -185,54 +205,62 @@ struct Kv8Read {
     const int8_t *codes[2];
     const float *scales[2];
     void *out[2];
-    int bf16;
 };
 
-// One thread per 16 values of a row and head; blockIdx.y: keys or values.
+// One warp per row, of keys or of values (blockIdx.y): 4 values a lane, so that a
+// head's codes are read and its values written in one piece each; NU heads at a
+// time, so that as many loads are under way.
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kKvThreads) k_kv8_read(const Kv8Read a)
 {
+    constexpr int PER = 128 / D, NU = 8;  // heads a warp takes at once; times unrolled
     pdl_launch_dependents();
     pdl_wait_primary();
     const Kv8View &v = a.v;
-    const int which = blockIdx.y;
+    const int which = blockIdx.y, lane = threadIdx.x & 31;
     void *out = which ? a.out[1] : a.out[0];
-    if (!out) return;
+    const int r = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
+    if (!out || r >= v.n_rows) return;
     const int8_t *codes = which ? a.codes[1] : a.codes[0];
     const float *scales = which ? a.scales[1] : a.scales[0];
-    const int D16 = v.D / 16, per_row = v.H * D16;
-    const int64_t i = (int64_t)blockIdx.x * kKvThreads + threadIdx.x;
-    if (i >= (int64_t)v.n_rows * per_row) return;
-    const int r = (int)(i / per_row), c = (int)(i % per_row), h = c / D16;
-    const int b = v.row_start ? kv8_find_seq(v, r, 1, 0) : r;
+    const int b = v.row_start ? kv8_find_seq_warp(v, r, 1, 0) : r;
     if (b < 0) return;
     const Kv8Seq s = kv8_seq(v, b, &g_kv8_fault);
-    if (r >= s.r0 + s.n) return;  // behind the last sequence
+    if (r < s.r0 || r >= s.r0 + s.n) return;  // behind the last sequence
     const int pos = s.len - s.n + (r - s.r0);
-    uint4 u = make_uint4(0, 0, 0, 0);
-    float scale = 0.f;
     const int page = pos >= 0 ? kv8_page(v, b, pos / v.P, &g_kv8_fault) : -1;
-    if (page >= 0) {
-        const int64_t ph = (int64_t)page * v.H + h;
-        u = *reinterpret_cast<const uint4 *>(codes + (ph * v.P + pos % v.P) * v.D + c % D16 * 16);
-        scale = scales[ph];
-    }
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float f[16];
+    const int64_t ph = (int64_t)page * v.H;
+    const int own = lane * 4 / D, e = lane * 4 % D;  // this lane's head of a group, and entry
+    for (int h0 = own; h0 < v.H; h0 += PER * NU) {
+        uint32_t w[NU];
+        float sc[NU];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) f[k] = (float)(int8_t)(w[k / 4] >> (8 * (k % 4))) * scale;
-    const int64_t at = i * 16;
-    if (a.bf16) {
-        uint32_t o[8];
+        for (int u = 0; u < NU; ++u) {
+            const int h = h0 + PER * u;
+            w[u] = 0;
+            sc[u] = 0.f;
+            if (page >= 0 && h < v.H) {
+                w[u] = __ldg(reinterpret_cast<const uint32_t *>(codes + ((ph + h) * v.P + pos % v.P) * D + e));
+                sc[u] = __ldg(scales + ph + h);
+            }
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[k]) : "f"(f[2 * k + 1]), "f"(f[2 * k]));
-        uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at);
-        p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        p[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    } else {
-        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
+        for (int u = 0; u < NU; ++u) {
+            const int h = h0 + PER * u;
+            if (h >= v.H) break;
+            float f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) f[k] = (float)(int8_t)(w[u] >> (8 * k)) * sc[u];
+            const int64_t at = ((int64_t)r * v.H + h) * D + e;
+            if (BF16) {
+                uint2 o;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.x) : "f"(f[1]), "f"(f[0]));
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o.y) : "f"(f[3]), "f"(f[2]));
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) = o;
+            } else {
+                *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = make_float4(f[0], f[1], f[2], f[3]);
+            }
+        }
     }
 }
 
@@ -244,11 +272,11 @@ lowbit_status kv8_read_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     a.codes[0] = c.k; a.codes[1] = c.v;
     a.scales[0] = c.k_scales; a.scales[1] = c.v_scales;
     a.out[0] = k_out; a.out[1] = v_out;
-    a.bf16 = out_type == LOWBIT_BF16;
-    const int64_t threads = (int64_t)b.n_rows * c.n_heads * (c.head_dim / 16);
-    const int64_t grid = (threads + kKvThreads - 1) / kKvThreads;
-    if (grid >= (int64_t(1) << 31)) return LOWBIT_ERR_UNSUPPORTED_SHAPE;
-    const cudaError_t e = launch_pdl(k_kv8_read, dim3((unsigned)grid, 2), dim3(kKvThreads), 0, st, a);
+    const bool bf16 = out_type == LOWBIT_BF16;
+    void (*kern)(const Kv8Read) = c.head_dim == 128 ? (bf16 ? k_kv8_read<128, true> : k_kv8_read<128, false>)
+                                                    : (bf16 ? k_kv8_read<64, true> : k_kv8_read<64, false>);
+    const int64_t grid = ((int64_t)b.n_rows + kKvThreads / 32 - 1) / (kKvThreads / 32);
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)grid, 2), dim3(kKvThreads), 0, st, a);
     return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 

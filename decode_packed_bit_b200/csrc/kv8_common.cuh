@@ -75,4 +75,24 @@ __device__ __forceinline__ int kv8_find_seq(const Kv8View &v, int item, int T, i
     return lo;
 }
 
+// The same by a whole warp for one item: 32 sequences are looked at at once, so
+// that up to 32 take one memory latency, up to 1024 two.
+__device__ __forceinline__ int kv8_find_seq_warp(const Kv8View &v, int item, int T, int per)
+{
+    int lo = -1, hi = v.n_seqs - 1;
+    const int lane = threadIdx.x & 31;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, mid = lo + (lane + 1) * step;
+        bool at = false;
+        if (mid <= hi) at = max(__ldg(v.row_start + mid), 0) / T + (int64_t)per * mid <= item;
+        // they hold for the first lanes (where row_start does not fall; else any
+        // of them will do: what is found is checked)
+        const int n = __popc(__ballot_sync(0xffffffffu, at));
+        const int top = lo + n * step;
+        hi = n < 32 ? min(hi, top + step - 1) : hi;
+        lo = min(top, hi);
+    }
+    return lo;
+}
+
 }  // namespace lowbit
