@@ -42,8 +42,7 @@ struct Kv8Append {
     int bf16[2];
 };
 
-// Eight consecutive values as floats; NaN becomes 0 and infinities the largest
-// float.
+// Eight consecutive values as floats.
 __device__ __forceinline__ void kv8_load8(const void *base, int64_t at, int bf16, float (&v)[8])
 {
     if (bf16) {
@@ -60,27 +59,76 @@ __device__ __forceinline__ void kv8_load8(const void *base, int64_t at, int bf16
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
+}
+
+// NaN becomes 0 and infinities the largest float.
+__device__ __forceinline__ void kv8_finite8(float (&v)[8])
+{
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] == v[i] ? fminf(fmaxf(v[i], -FLT_MAX), FLT_MAX) : 0.f;
 }
 
-// rint(x / s), exactly; inv = 1 / s, or 0 where s = 0.
-__device__ __forceinline__ int kv8_code(float x, float s, float inv)
+// The largest magnitude's bits, which order like integers; from 0x7F800000 on
+// something is not finite.
+__device__ __forceinline__ uint32_t kv8_top8(const float (&v)[8], uint32_t top)
 {
-    const float t = x * inv;
-    float q = rintf(t);
-    // t is off by 1.5 ulp at most: 2e-5 below 127
-    if (!(fabsf(t - q) <= 0.4999f)) q = (float)rint((double)x / (double)s);
-    return (int)fminf(fmaxf(q, -127.f), 127.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return top;
 }
 
-// rint(c * ratio), exactly, ratio = was / now.
-__device__ __forceinline__ int kv8_recode(int c, float ratio, double was, double now)
+// Eight rint(x / s) as bytes, exactly; inv = 1 / s, or 0 where s = 0.  x * inv is off by
+// 1.5 ulp at most, 2e-5 below 127, so only a quotient within 1e-4 of a tie may be
+// rounded wrongly: then all eight are taken again in double.  Adding 1.5 * 2^23
+// rounds to an integer (ties to even) and leaves it in the low bits, in two's
+// complement.  |x| <= 127 s up to s's own rounding: no clamp.
+__device__ __forceinline__ uint2 kv8_codes8(const float (&x)[8], float s, float inv)
 {
-    const float t = (float)c * ratio;
-    float q = rintf(t);
-    if (!(fabsf(t - q) <= 0.4999f)) q = (float)rint(c * was / now);
-    return (int)q;
+    constexpr float kMagic = 12582912.f;
+    uint32_t c[8];
+    bool near = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float t = x[k] * inv, r = t + kMagic;
+        c[k] = __float_as_uint(r);
+        near |= !(fabsf(t - (r - kMagic)) <= 0.4999f);
+    }
+    if (near) {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            float v = x[0];
+#pragma unroll
+            for (int y = 1; y < 8; ++y) v = k == y ? x[y] : v;
+            const uint32_t q = (uint32_t)(int)rint((double)v / (double)s);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) c[y] = k == y ? q : c[y];
+        }
+    }
+    return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
+}
+
+// Four codes c as rint(c * was / now), exactly, the same way (ratio = was / now).
+__device__ __forceinline__ uint32_t kv8_recode4(uint32_t w, float ratio, float was, float now)
+{
+    constexpr float kMagic = 12582912.f;
+    uint32_t c[4];
+    bool near = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float t = (float)(int8_t)(w >> (8 * e)) * ratio, r = t + kMagic;
+        c[e] = __float_as_uint(r);
+        near |= !(fabsf(t - (r - kMagic)) <= 0.4999f);
+    }
+    if (near) {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t q = (uint32_t)(int)rint((double)(int8_t)(w >> (8 * e)) * (double)was / (double)now);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) c[y] = e == y ? q : c[y];
+        }
+    }
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
 // G threads; each keeps its first NC pieces of 8 values in registers and reads
@@ -88,7 +136,7 @@ __device__ __forceinline__ int kv8_recode(int c, float ratio, double was, double
 template <int G, int NC>
 __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
 {
-    __shared__ float red[G / 32];
+    __shared__ uint32_t red[G / 32];
     pdl_launch_dependents();
     pdl_wait_primary();
     const Kv8View &v = a.v;
@@ -109,7 +157,7 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
     const void *x = which ? a.x[1] : a.x[0];
     const int bf16 = which ? a.bf16[1] : a.bf16[0];
     float f[NC][8];
-    float top = 0.f;
+    uint32_t most = 0;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int i = t + c * G;
@@ -122,21 +170,32 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
     int8_t *codes = (which ? a.codes[1] : a.codes[0]) + ((int64_t)page * v.H + h) * v.P * v.D;
     float *scale = (which ? a.scales[1] : a.scales[0]) + (int64_t)page * v.H + h;
     const float was = older ? fmaxf(*scale, 0.f) : 0.f;
+    // the largest magnitude; where something is not finite (a CTA's decision),
+    // again over the finite values that stand for it
+    bool odd = false;
+    while (true) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c) {
+            if (odd) kv8_finite8(f[c]);
+            most = kv8_top8(f[c], most);
+        }
+        for (int i = t + NC * G; i < n8; i += G) {
+            float g[8];
+            kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, g);
+            if (odd) kv8_finite8(g);
+            most = kv8_top8(g, most);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if ((t & 31) == 0) red[t >> 5] = most;
+        __syncthreads();  // also: every thread has read the old scale
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(f[c][k]));
-    for (int i = t + NC * G; i < n8; i += G) {
-        float g[8];
-        kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(g[k]));
+        for (int i = 0; i < G / 32; ++i) most = max(most, red[i]);
+        if (most < 0x7F800000u) break;
+        odd = true;
+        most = 0;
+        __syncthreads();
     }
-    top = warp_max_nonneg(top);
-    if ((t & 31) == 0) red[t >> 5] = top;
-    __syncthreads();  // also: every thread has read the old scale
-#pragma unroll
-    for (int i = 0; i < G / 32; ++i) top = fmaxf(top, red[i]);
+    const float top = __uint_as_float(most);
     const float now = fmaxf(was, __fdiv_rn(top, 127.f));
     const float inv = now > 0.f ? __frcp_rn(now) : 0.f;
     if (now > was) {
@@ -146,29 +205,19 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
             const uint4 u = reinterpret_cast<const uint4 *>(codes)[i];
             uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t o = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o |= ((uint32_t)kv8_recode((int8_t)(w[k] >> (8 * e)), ratio, was, now) & 0xFFu) << (8 * e);
-                w[k] = o;
-            }
+            for (int k = 0; k < 4; ++k) w[k] = kv8_recode4(w[k], ratio, was, now);
             reinterpret_cast<uint4 *>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    auto put = [&](int i, const float (&g)[8]) {
-        uint32_t o[2] = {0, 0};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k / 4] |= ((uint32_t)kv8_code(g[k], now, inv) & 0xFFu) << (8 * (k % 4));
-        reinterpret_cast<uint2 *>(codes)[older * D8 + i] = make_uint2(o[0], o[1]);
-    };
+    uint2 *dst = reinterpret_cast<uint2 *>(codes) + older * D8;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-        if (t + c * G < n8) put(t + c * G, f[c]);
+        if (t + c * G < n8) dst[t + c * G] = kv8_codes8(f[c], now, inv);
     for (int i = t + NC * G; i < n8; i += G) {
         float g[8];
         kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, g);
-        put(i, g);
+        if (odd) kv8_finite8(g);
+        dst[i] = kv8_codes8(g, now, inv);
     }
     if (t == 0) *scale = now;
 }
