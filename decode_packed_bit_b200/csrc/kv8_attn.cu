@@ -56,7 +56,6 @@ struct Kv8Attn {
     uint16_t *out;
     int64_t q_stride, out_stride;
     int G;            // query heads per cache head
-    int page_log2;
     float scale_log2; // |scale| * log2(e)
     float limbs;      // 32512 with the sign of scale
     unsigned *counters;   // [CTAs], zero between calls
@@ -327,12 +326,12 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         present &= ~(1u << ld_slot);
         if (ld_more) {
             const int tok = ld_tile * kAtTile;
-            const int page = kv8_page(a.v, ld.b, tok >> a.page_log2, &g_at_fault);
+            const int page = kv8_page(a.v, ld.b, tok >> a.v.P_log2, &g_at_fault);
             ++ld_tile;
             if (page >= 0) {
                 present |= 1u << ld_slot;
                 ld_ph = (int64_t)page * a.v.H + ld.h;
-                const int64_t at = ((ld_ph << a.page_log2) + (tok & (a.v.P - 1))) * D + lane * 16;
+                const int64_t at = ((ld_ph << a.v.P_log2) + (tok & (a.v.P - 1))) * D + lane * 16;
                 const int8_t *src = a.k + at;
                 ld_v = a.vv + at;
                 const unsigned st = ring + ld_slot * S::kHalf + kdst;
@@ -741,8 +740,7 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     a.k = c.k; a.vv = c.v; a.ks = c.k_scales; a.vs = c.v_scales;
     a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
     a.G = q_heads / c.n_heads;
-    a.page_log2 = c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
-    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+        a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
     a.limbs = scale < 0.f ? -32512.f : 32512.f;
     const int ctas = attn_ctas();
     uint8_t *ws = static_cast<uint8_t *>(workspace);

@@ -55,7 +55,7 @@ struct Kv8AttnTc {
     uint16_t *out;
     int64_t q_stride, out_stride;
     int G, tokens;     // query heads per cache head; tokens of a tile: 128 / G
-    int page_log2, items;
+    int items;
     float scale_log2;  // |scale| * log2(e)
     float sign;        // of scale
 };
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
         float2 raw_info = make_float2(-1.f, 0.f);  // ks (-1: no page), vs
         auto pages_of = [&](int i) {
             const int tok = i * kAttTokens + (lane & 3) * 32;
-            return tok < seen ? kv8_page(a.v, b, tok >> a.page_log2, &g_att_range) : -1;
+            return tok < seen ? kv8_page(a.v, b, tok >> a.v.P_log2, &g_att_range) : -1;
         };
         const unsigned own = (unsigned)(8 * w + r7) * D + c4 * 16;  // of 32 tokens, this thread's first piece
         auto load = [&](const int8_t *codes, int i, int pages, uint4 (&raw)[NP]) {
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const int page = __shfl_sync(0xffffffffu, pages, y), slot = (i * kAttTokens + 32 * y) & (a.v.P - 1);
-                src[y] = page < 0 ? nullptr : codes + ((((int64_t)page * H + h) << a.page_log2) + slot) * D + own;
+                src[y] = page < 0 ? nullptr : codes + ((((int64_t)page * H + h) << a.v.P_log2) + slot) * D + own;
             }
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
@@ -677,8 +677,7 @@ lowbit_status kv8_attn_tc_launch(const lowbit_kv8_cache &c, const lowbit_kv8_bat
     a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
     a.G = q_heads / c.n_heads;
     a.tokens = kAttRows / a.G;
-    a.page_log2 = c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7;
-    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+        a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
     a.sign = scale < 0.f ? -1.f : 1.f;
     const int64_t units = attn_tc_units(c, b, q_heads);
     a.items = (int)(units / c.n_heads);

@@ -79,30 +79,28 @@ __device__ __forceinline__ uint32_t kv8_top8(const float (&v)[8], uint32_t top)
 
 // Eight rint(x / s) as bytes, exactly; inv = 1 / s, or 0 where s = 0.  x * inv is off by
 // 1.5 ulp at most, 2e-5 below 127, so only a quotient within 1e-4 of a tie may be
-// rounded wrongly: then all eight are taken again in double.  Adding 1.5 * 2^23
+// rounded wrongly: it is taken again in double.  Adding 1.5 * 2^23
 // rounds to an integer (ties to even) and leaves it in the low bits, in two's
 // complement.  |x| <= 127 s up to s's own rounding: no clamp.
 __device__ __forceinline__ uint2 kv8_codes8(const float (&x)[8], float s, float inv)
 {
     constexpr float kMagic = 12582912.f;
-    uint32_t c[8];
-    bool near = false;
+    uint32_t c[8], near = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const float t = x[k] * inv, r = t + kMagic;
         c[k] = __float_as_uint(r);
-        near |= !(fabsf(t - (r - kMagic)) <= 0.4999f);
+        if (!(fabsf(t - (r - kMagic)) <= 0.4999f)) near |= 1u << k;
     }
-    if (near) {
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-            float v = x[0];
+    while (near) {  // one in 600 pieces
+        const int k = __ffs(near) - 1;
+        near &= near - 1;
+        float v = x[0];
 #pragma unroll
-            for (int y = 1; y < 8; ++y) v = k == y ? x[y] : v;
-            const uint32_t q = (uint32_t)(int)rint((double)v / (double)s);
+        for (int y = 1; y < 8; ++y) v = k == y ? x[y] : v;
+        const uint32_t q = (uint32_t)(int)rint((double)v / (double)s);
 #pragma unroll
-            for (int y = 0; y < 8; ++y) c[y] = k == y ? q : c[y];
-        }
+        for (int y = 0; y < 8; ++y) c[y] = k == y ? q : c[y];
     }
     return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
                       __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
@@ -112,21 +110,19 @@ __device__ __forceinline__ uint2 kv8_codes8(const float (&x)[8], float s, float 
 __device__ __forceinline__ uint32_t kv8_recode4(uint32_t w, float ratio, float was, float now)
 {
     constexpr float kMagic = 12582912.f;
-    uint32_t c[4];
-    bool near = false;
+    uint32_t c[4], near = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float t = (float)(int8_t)(w >> (8 * e)) * ratio, r = t + kMagic;
         c[e] = __float_as_uint(r);
-        near |= !(fabsf(t - (r - kMagic)) <= 0.4999f);
+        if (!(fabsf(t - (r - kMagic)) <= 0.4999f)) near |= 1u << e;
     }
-    if (near) {
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t q = (uint32_t)(int)rint((double)(int8_t)(w >> (8 * e)) * (double)was / (double)now);
+    while (near) {
+        const int e = __ffs(near) - 1;
+        near &= near - 1;
+        const uint32_t q = (uint32_t)(int)rint((double)(int8_t)(w >> (8 * e)) * (double)was / (double)now);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) c[y] = e == y ? q : c[y];
-        }
+        for (int y = 0; y < 4; ++y) c[y] = e == y ? q : c[y];
     }
     return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
@@ -141,18 +137,19 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
     pdl_wait_primary();
     const Kv8View &v = a.v;
     const int t = threadIdx.x;
-    const int h = blockIdx.x % v.H, which = blockIdx.x / v.H % 2, item = blockIdx.x / (2 * v.H);
+    const int item = blockIdx.x, h = blockIdx.y, which = blockIdx.z;
     // the item's sequence, and which of its touched pages (all uniform in the CTA)
     const int b = v.row_start ? kv8_find_seq_warp(v, item, v.P, 2) : item;
     if (b < 0) return;
     const Kv8Seq s = kv8_seq(v, b, &g_kv8_fault);
-    const int nth = v.row_start ? (int)(item - (max(__ldg(v.row_start + b), 0) / v.P + 2 * (int64_t)b)) : 0;
+    const int nth = v.row_start ? item - ((max(__ldg(v.row_start + b), 0) >> v.P_log2) + 2 * b) : 0;
     const int p0 = s.len - s.n, first = max(p0, 0);
-    const int64_t j64 = (int64_t)first / v.P + nth;
-    if (s.n == 0 || j64 * v.P >= s.len) return;
-    const int j = (int)j64;
-    const int lo = max(first, j * v.P), hi = min(s.len, (j + 1) * v.P);
-    const int older = lo - j * v.P, D8 = v.D / 8, n8 = (hi - lo) * D8;
+    const int64_t j64 = (int64_t)(first >> v.P_log2) + nth;
+    if (s.n == 0 || j64 << v.P_log2 >= s.len) return;
+    const int j = (int)j64, start = j << v.P_log2;
+    const int lo = max(first, start), hi = min(s.len, start + v.P);
+    const int older = lo - start, d8 = v.D_log2 - 3, n8 = (hi - lo) << d8;
+    auto place = [&](int i, int64_t at, int64_t stride) { return at + (i >> d8) * stride + ((i & ((1 << d8) - 1)) << 3); };
     const int64_t stride = which ? a.stride[1] : a.stride[0], at0 = (s.r0 + (int64_t)(lo - p0)) * stride + (int64_t)h * v.D;
     const void *x = which ? a.x[1] : a.x[0];
     const int bf16 = which ? a.bf16[1] : a.bf16[0];
@@ -163,7 +160,7 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
         const int i = t + c * G;
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[c][k] = 0.f;
-        if (i < n8) kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, f[c]);
+        if (i < n8) kv8_load8(x, place(i, at0, stride), bf16, f[c]);
     }
     const int page = kv8_page(v, b, j, &g_kv8_fault);
     if (page < 0) return;
@@ -181,7 +178,7 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
         }
         for (int i = t + NC * G; i < n8; i += G) {
             float g[8];
-            kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, g);
+            kv8_load8(x, place(i, at0, stride), bf16, g);
             if (odd) kv8_finite8(g);
             most = kv8_top8(g, most);
         }
@@ -201,7 +198,7 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
     if (now > was) {
         const float ratio = __fdiv_rn(was, now);
 #pragma unroll 4
-        for (int i = t; i < older * v.D / 16; i += G) {
+        for (int i = t; i < older << (v.D_log2 - 4); i += G) {
             const uint4 u = reinterpret_cast<const uint4 *>(codes)[i];
             uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -209,13 +206,13 @@ __global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
             reinterpret_cast<uint4 *>(codes)[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
-    uint2 *dst = reinterpret_cast<uint2 *>(codes) + older * D8;
+    uint2 *dst = reinterpret_cast<uint2 *>(codes) + (older << d8);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
         if (t + c * G < n8) dst[t + c * G] = kv8_codes8(f[c], now, inv);
     for (int i = t + NC * G; i < n8; i += G) {
         float g[8];
-        kv8_load8(x, at0 + i / D8 * stride + i % D8 * 8, bf16, g);
+        kv8_load8(x, place(i, at0, stride), bf16, g);
         if (odd) kv8_finite8(g);
         dst[i] = kv8_codes8(g, now, inv);
     }
@@ -235,8 +232,7 @@ lowbit_status kv8_append_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batc
     a.bf16[0] = k_type == LOWBIT_BF16; a.bf16[1] = v_type == LOWBIT_BF16;
     // touched pages, at most: see kv8_find_seq (n rows touch n / P + 2 or fewer)
     const int64_t items = b.row_start ? (int64_t)b.n_rows / c.page_tokens + 2 * (int64_t)b.n_seqs : b.n_seqs;
-    const int64_t grid = items * 2 * c.n_heads;
-    if (grid >= (int64_t(1) << 31)) return LOWBIT_ERR_UNSUPPORTED_SHAPE;
+    if (items >= (int64_t(1) << 31)) return LOWBIT_ERR_UNSUPPORTED_SHAPE;
     // a decode step: about a token per sequence; else a thread per 32 values of a page
     const bool few = b.n_rows <= 4 * (int64_t)b.n_seqs;
     const int G = few ? 128 : c.page_tokens * c.head_dim / 32;
@@ -245,7 +241,7 @@ lowbit_status kv8_append_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batc
                                     : G == 128 ? k_kv8_append<128, 4>
                                     : G == 256 ? k_kv8_append<256, 4>
                                                : k_kv8_append<512, 4>;
-    const cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), dim3(G), 0, st, a);
+    const cudaError_t e = launch_pdl(kern, dim3((unsigned)items, c.n_heads, 2), dim3(G), 0, st, a);
     return e == cudaSuccess ? LOWBIT_OK : LOWBIT_ERR_CUDA;
 }
 
@@ -277,7 +273,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv8_read(const Kv8Read a)
     const Kv8Seq s = kv8_seq(v, b, &g_kv8_fault);
     if (r < s.r0 || r >= s.r0 + s.n) return;  // behind the last sequence
     const int pos = s.len - s.n + (r - s.r0);
-    const int page = pos >= 0 ? kv8_page(v, b, pos / v.P, &g_kv8_fault) : -1;
+    const int page = pos >= 0 ? kv8_page(v, b, pos >> v.P_log2, &g_kv8_fault) : -1;
     const int64_t ph = (int64_t)page * v.H;
     const int own = lane * 4 / D, e = lane * 4 % D;  // this lane's head of a group, and entry
     for (int h0 = own; h0 < v.H; h0 += PER * NU) {
@@ -289,7 +285,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv8_read(const Kv8Read a)
             w[u] = 0;
             sc[u] = 0.f;
             if (page >= 0 && h < v.H) {
-                w[u] = __ldg(reinterpret_cast<const uint32_t *>(codes + ((ph + h) * v.P + pos % v.P) * D + e));
+                w[u] = __ldg(reinterpret_cast<const uint32_t *>(codes + (((ph + h) << v.P_log2) + (pos & (v.P - 1))) * D + e));
                 sc[u] = __ldg(scales + ph + h);
             }
         }

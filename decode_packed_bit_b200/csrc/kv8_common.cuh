@@ -15,12 +15,14 @@ struct Kv8View {
     const int32_t *kv_len, *page_table, *row_start;
     int n_seqs, max_pages, n_rows;
     int n_pages, H, P, D;
+    int P_log2, D_log2;  // P is 32, 64 or 128, D 64 or 128: shifts in place of divisions
 };
 
 inline Kv8View kv8_view(const lowbit_kv8_cache &c, const lowbit_kv8_batch &b)
 {
     return Kv8View{b.kv_len, b.page_table, b.row_start, b.n_seqs, b.max_pages, b.n_rows,
-                   c.n_pages, c.n_heads, c.page_tokens, c.head_dim};
+                   c.n_pages, c.n_heads, c.page_tokens, c.head_dim,
+                   c.page_tokens == 32 ? 5 : c.page_tokens == 64 ? 6 : 7, c.head_dim == 64 ? 6 : 7};
 }
 
 // Sequence b: rows [r0, r0 + n), of which the first is position len - n.
