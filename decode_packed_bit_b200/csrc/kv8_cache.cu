@@ -130,7 +130,7 @@ __device__ __forceinline__ uint32_t kv8_recode4(uint32_t w, float ratio, float w
 // G threads; each keeps its first NC pieces of 8 values in registers and reads
 // further ones again.
 template <int G, int NC>
-__global__ void __launch_bounds__(G) k_kv8_append(const Kv8Append a)
+__global__ void __launch_bounds__(G, 768 / G) k_kv8_append(const Kv8Append a)
 {
     __shared__ uint32_t red[G / 32];
     pdl_launch_dependents();
