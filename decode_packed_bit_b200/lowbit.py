@@ -396,6 +396,15 @@ def _either(t, what):
     return _types[t.dtype]
 
 
+def _scratch(t, dev):
+    """Address and bytes of a workspace (None: none)."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "workspace", f"a contiguous tensor on cuda:{dev}")
+    return t.data_ptr(), t.nbytes
+
+
 def _ptrs(values):
     return (ctypes.c_void_p * len(values))(*values)
 
@@ -424,7 +433,7 @@ def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, works
         None if ranks is None else _dense(ranks, _int32, sl, "ranks", dev),
         None if scales is None else _dense(scales, _float32, sl, "scales", dev),
         _ptrs([_dense(t, _float32, sy, "base", dev) for t in base]), _ptrs([_dense(t, _float32, sy, "y", dev) for t in ys]),
-        R, M, N, K, rank, L, None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
+        R, M, N, K, rank, L, *_scratch(workspace, dev),
         _raw_stream(stream, dev)), "lowbit_lora_add_group")
 
 
@@ -568,5 +577,5 @@ def lowbit_kv8_attention(cache: KV8Cache, page_table, kv_len, q, out, scale, row
     qp, qs = _rows(q, _bfloat16, shape, "q", dev)
     op, os_ = _rows(out, _bfloat16, shape, "out", dev)
     _check(lib().lowbit_kv8_attention(cache._ref, ctypes.byref(batch), qp, qs, heads, scale, op, os_,
-                                      None if workspace is None else workspace.data_ptr(), _nbytes(workspace),
+                                      *_scratch(workspace, dev),
                                       _raw_stream(stream, dev)), "lowbit_kv8_attention")
