@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(G, 768 / G) k_kv8_append(const Kv8Append a)
     const int nth = v.row_start ? item - ((max(__ldg(v.row_start + b), 0) >> v.P_log2) + 2 * b) : 0;
     const int p0 = s.len - s.n, first = max(p0, 0);
     const int64_t j64 = (int64_t)(first >> v.P_log2) + nth;
-    if (s.n == 0 || j64 << v.P_log2 >= s.len) return;
+    if (s.n == 0 || nth < 0 || j64 << v.P_log2 >= s.len) return;  // nth < 0: row_start falls
     const int j = (int)j64, start = j << v.P_log2;
     const int lo = max(first, start), hi = min(s.len, start + v.P);
     const int older = lo - start, d8 = v.D_log2 - 3, n8 = (hi - lo) << d8;

@@ -87,8 +87,8 @@ __device__ __forceinline__ int kv8_find_seq_warp(const Kv8View &v, int item, int
         const int step = (hi - lo + 31) / 32, mid = lo + (lane + 1) * step;
         bool at = false;
         if (mid <= hi) at = max(__ldg(v.row_start + mid), 0) / T + (int64_t)per * mid <= item;
-        // they hold for the first lanes (where row_start does not fall; else any
-        // of them will do: what is found is checked)
+        // they hold for the first lanes where row_start does not fall; else what
+        // is found may begin after `item`, which the caller checks
         const int n = __popc(__ballot_sync(0xffffffffu, at));
         const int top = lo + n * step;
         hi = n < 32 ? min(hi, top + step - 1) : hi;

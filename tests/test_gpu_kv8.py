@@ -374,6 +374,29 @@ def test_rows_out_of_range_are_skipped(lb):
         assert lb.lowbit_fault_flags() == 16
 
 
+@pytest.mark.parametrize("rs", [[0, 500, 90, 600], [0, 500, 0, 500], [300, 600, 10, 20], [600, 500, 400, 0]])
+@pytest.mark.parametrize("G", [4, 8])  # on the integer tensor cores, on tcgen05
+def test_falling_row_starts_stay_inside(lb, G, rs):
+    """Not allowed, and read on the device: what comes out is not defined, but nothing outside is touched."""
+    P, H, D = 32, 2, 64
+    lens = [600, 600, 600]
+    n_pages, table = make_batch(9, lens, P)
+    rs, T = np.array(rs, np.int32), 600
+    cache = make_cache(lb, 9, n_pages, H, P, D)
+    used = {int(p) for p in table.ravel() if p < n_pages}
+    spare = [p for p in range(n_pages) if p not in used]
+    before = cache.k[spare].clone()
+    x = torch.randn((T, H, D), device="cuda")
+    lb.lowbit_kv8_append(cache, i32(table), i32(lens), x, x, row_start=i32(rs))
+    assert torch.equal(cache.k[spare], before)
+    y = torch.empty_like(x)
+    lb.lowbit_kv8_read(cache, i32(table), i32(lens), y, None, row_start=i32(rs))
+    q = torch.randn((T, H * G, D), device="cuda").bfloat16()
+    attend(lb, cache, table, lens, q, 0.1, rs)
+    assert lb.lowbit_fault_flags() == 16
+    assert lb.lowbit_fault_flags() == 0
+
+
 def test_attention_strides(lb):
     lens, P, H, G, D = [77, 200], 32, 2, 2, 64
     n_pages, table = make_batch(8, lens, P)
