@@ -740,7 +740,7 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     a.k = c.k; a.vv = c.v; a.ks = c.k_scales; a.vs = c.v_scales;
     a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
     a.G = q_heads / c.n_heads;
-        a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
     a.limbs = scale < 0.f ? -32512.f : 32512.f;
     const int ctas = attn_ctas();
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -749,7 +749,6 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     a.part_ml = reinterpret_cast<float *>(ws);
     ws += align256((size_t)2 * ctas * kAtMaxRT * 8 * 8);
     a.part_o = reinterpret_cast<float *>(ws);
-    if (!&g_at_fault) return LOWBIT_ERR_CUDA;
     // eight query rows per tile where that holds a sequence's rows, else sixteen
     // (each tile of keys and values is then read for twice the rows)
     const bool one = (int64_t)b.n_rows * a.G <= 8 * (int64_t)b.n_seqs;

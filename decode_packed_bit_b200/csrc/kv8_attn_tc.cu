@@ -677,7 +677,7 @@ lowbit_status kv8_attn_tc_launch(const lowbit_kv8_cache &c, const lowbit_kv8_bat
     a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
     a.G = q_heads / c.n_heads;
     a.tokens = kAttRows / a.G;
-        a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
+    a.scale_log2 = fabsf(scale) * 1.4426950408889634f;
     a.sign = scale < 0.f ? -1.f : 1.f;
     const int64_t units = attn_tc_units(c, b, q_heads);
     a.items = (int)(units / c.n_heads);

@@ -512,7 +512,7 @@ lowbit_status lowbit_rmsnorm_bf16(const float *a, const float *b, int M, int D, 
 static lowbit_status lora_shape_ok(int R, int M, int N, int K, int rank)
 {
     LB_CHECK(R >= 1 && R <= lora_max_group() && M >= 1 && N >= 1 && K >= 1 && rank >= 1, LOWBIT_ERR_INVALID_ARG);
-    LB_CHECK(K % 64 == 0 && rank % 8 == 0 && rank <= 128 && N <= (1 << 30) && M <= (1 << 30),
+    LB_CHECK(K % 64 == 0 && rank % 8 == 0 && rank <= 128 && N <= (1 << 25) && M <= (1 << 30),
              LOWBIT_ERR_UNSUPPORTED_SHAPE);
     LB_CHECK((int64_t)M * N < kMaxElems && (int64_t)M * K < kMaxElems, LOWBIT_ERR_UNSUPPORTED_SHAPE);
     return LOWBIT_OK;
@@ -540,6 +540,8 @@ lowbit_status lowbit_lora_add_group(const uint16_t *x, const int32_t *ids, const
         LB_CHECK(a[r] && b[r] && base[r] && y[r], LOWBIT_ERR_INVALID_ARG);
         LB_CHECK(aligned16(a[r]) && aligned16(b[r]) && aligned16(base[r]) && aligned16(y[r]), LOWBIT_ERR_MISALIGNED);
     }
+    for (int r = 0; r < R; ++r)  // the projections run side by side
+        for (int o = 0; o < R; ++o) LB_CHECK(o == r || (y[r] != y[o] && y[r] != base[o]), LOWBIT_ERR_INVALID_ARG);
     LB_CHECK(workspace_bytes >= lora_workspace_bytes(R, M, K, rank), LOWBIT_ERR_INVALID_ARG);
     return lora_launch(x, ids, a, b, ranks, scales, base, y, R, M, N, K, rank, n_adapters, workspace,
                        as_stream(stream));
@@ -617,7 +619,7 @@ static lowbit_status kv8_ok(const lowbit_kv8_cache *c, const lowbit_kv8_batch *b
                  (c->head_dim == 64 || c->head_dim == 128) && c->n_heads <= 1024,
              LOWBIT_ERR_UNSUPPORTED_SHAPE);
     LB_CHECK((int64_t)c->n_pages * c->n_heads < (int64_t(1) << 31) &&
-                 (int64_t)b->max_pages * c->page_tokens < (int64_t(1) << 31),
+                 (int64_t)b->max_pages * c->page_tokens <= (int64_t(1) << 30) && b->n_seqs <= (1 << 30),
              LOWBIT_ERR_UNSUPPORTED_SHAPE);
     LB_CHECK(b->row_start || b->n_rows == b->n_seqs, LOWBIT_ERR_INVALID_ARG);
     if (b->n_seqs == 0 || b->n_rows == 0) return LOWBIT_OK;

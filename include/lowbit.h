@@ -453,15 +453,17 @@ typedef enum {
  *   scales [n_adapters] fp32, or NULL (all 1)
  *   base   [M][N] fp32, the shared projection's output; may be y itself
  *   y      [M][N] fp32
- * Shapes: M >= 1, N >= 1, K >= 64 with K % 64 == 0, 8 <= rank <= 128 with
- * rank % 8 == 0, n_adapters >= 1, M * N, M * K and the adapters' elements
- * below 2^40.
- * t is held in fp32 and meets b as the sum of three bf16 numbers, which
- * carry all 24 bits of it; sums are fp32 in a fixed order, so the result is the same bits on every
- * run and does not depend on which other rows are in the call's batch beyond
- * the split that M chooses.
+ * Shapes: 1 <= M <= 2^30, 1 <= N <= 2^25, K >= 64 with K % 64 == 0, 8 <= rank
+ * <= 128 with rank % 8 == 0, n_adapters >= 1, M * N, M * K and the adapters'
+ * elements below 2^40.
+ * t is held in fp32 and meets b as the sum of three bf16 numbers, which carry
+ * all 24 bits of it (a t that is infinite makes its row NaN); sums are fp32 in
+ * a fixed order, so the result is the same bits on every run and does not
+ * depend on which other rows are in the call's batch beyond the split that M
+ * chooses.
  * Group form: R projections of one shape that read one x with one set of ids
- * (HOST arrays of R device pointers, 1 <= R <= 16).
+ * (HOST arrays of R device pointers, 1 <= R <= 16).  No y_r may be another's y
+ * or base.
  * workspace: lowbit_lora_workspace_bytes(R, M, N, K, rank) bytes; it needs no
  * initialisation.  Calls that share one must be ordered on one stream. */
 size_t lowbit_lora_workspace_bytes(int R, int M, int N, int K, int rank);
@@ -551,7 +553,8 @@ typedef struct {
  * zeros), rows outside [0, n_rows) are skipped; each sets bit 4 (value 16) of
  * lowbit_fault_flags().  A row whose position is negative (n_b > kv_len[b]) has no
  * place: it is not written, reads as zeros and attends to nothing.
- * n_seqs, n_rows >= 0 (0: no-op), max_pages >= 1, max_pages * page_tokens < 2^31. */
+ * 0 <= n_seqs <= 2^30, n_rows >= 0 (0: no-op), max_pages >= 1, max_pages *
+ * page_tokens <= 2^30. */
 typedef struct {
     const int32_t *kv_len;
     const int32_t *page_table;

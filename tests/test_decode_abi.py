@@ -119,6 +119,26 @@ def kv8(lb, cache=(), batch=()):
     return lb._KV8CacheC(**c), lb._KV8BatchC(**b)
 
 
+def test_sizes_whose_indices_would_wrap(lb):
+    assert lb.lowbit_lora_workspace_bytes(1, 1, (1 << 25) + 8, 64, 8) == 0   # more column ranges than a grid has
+    assert lb.lowbit_lora_workspace_bytes(1, 1, 1 << 25, 64, 8) > 0
+    L = lb.lib()
+    for batch in (dict(max_pages=(1 << 25) + 1), dict(n_seqs=(1 << 30) + 1)):
+        c, b = kv8(lb, batch=batch)
+        assert L.lowbit_kv8_read(ctypes.byref(c), ctypes.byref(b), FAKE, FAKE, 0, None) == 3
+        assert L.lowbit_kv8_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(b), 4) == 0
+
+
+def test_lora_group_outputs_are_apart(lb):
+    def arr(*p):
+        return ctypes.cast((ctypes.c_void_p * len(p))(*p), ctypes.c_void_p)
+
+    g, ab = lb.lib().lowbit_lora_add_group, arr(0x10000, 0x10000)
+    for base, y in ((arr(0x30000, 0x40000), arr(0x50000, 0x50000)),    # one output for two projections
+                    (arr(0x30000, 0x50000), arr(0x50000, 0x60000))):   # an output that is another's base
+        assert g(FAKE, FAKE, ab, ab, None, None, base, y, 2, 4, 64, 128, 16, 2, FAKE, BIG, None) == 1
+
+
 REFUSED = [
     (dict(k=None), {}, 1), (dict(v=None), {}, 1), (dict(k_scales=None), {}, 1), (dict(v_scales=None), {}, 1),
     (dict(k=0x10008), {}, 2), (dict(v_scales=0x10004), {}, 2), (dict(n_pages=0), {}, 1), (dict(n_heads=0), {}, 1),
