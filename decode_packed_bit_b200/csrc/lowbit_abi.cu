@@ -1,5 +1,7 @@
 // lowbit_abi.cu -- the extern "C" entry points declared in include/lowbit.h.
 // Every argument is validated here, on the host, before anything is enqueued.
+#include <cstring>
+
 #include "common.cuh"
 
 namespace lowbit {
@@ -111,6 +113,35 @@ static int per_byte(lowbit_format f)
     default: return 0;
     }
 }
+
+// The words of a block, one after the other.
+struct ArgBlock {
+    const int64_t *w;
+    int64_t word() { return *w++; }
+    int num() { return (int)*w++; }
+    float real()
+    {
+        double d;
+        memcpy(&d, w++, sizeof(d));
+        return (float)d;
+    }
+    template <typename T>
+    T *ptr()
+    {
+        return reinterpret_cast<T *>((uintptr_t)*w++);
+    }
+    lowbit_kv8_batch batch()
+    {
+        lowbit_kv8_batch b;
+        b.kv_len = ptr<const int32_t>();
+        b.page_table = ptr<const int32_t>();
+        b.row_start = ptr<const int32_t>();
+        b.n_seqs = num();
+        b.max_pages = num();
+        b.n_rows = num();
+        return b;
+    }
+};
 
 extern "C" {
 
@@ -693,6 +724,100 @@ lowbit_status lowbit_kv8_attention(const lowbit_kv8_cache *cache, const lowbit_k
     if (kv8_attn_tc_takes(*cache, *batch, q_heads))
         return kv8_attn_tc_launch(*cache, *batch, q, q_stride, q_heads, scale, out, out_stride, as_stream(stream));
     return kv8_attn_launch(*cache, *batch, q, q_stride, q_heads, scale, out, out_stride, workspace, as_stream(stream));
+}
+
+// ---------------------------------------------------------------------------
+// arguments in a block
+// ---------------------------------------------------------------------------
+
+lowbit_status lowbit_lora_add_group_args(const int64_t *args)
+{
+    LB_CHECK(args, LOWBIT_ERR_INVALID_ARG);
+    ArgBlock p{args};
+    const uint16_t *x = p.ptr<const uint16_t>();
+    const int32_t *ids = p.ptr<const int32_t>(), *ranks = p.ptr<const int32_t>();
+    const float *scales = p.ptr<const float>();
+    const int R = p.num(), M = p.num(), N = p.num(), K = p.num(), rank = p.num(), L = p.num();
+    void *workspace = p.ptr<void>();
+    const size_t bytes = (size_t)p.word();
+    void *stream = p.ptr<void>();
+    const uint16_t *a[16], *b[16];
+    const float *base[16];
+    float *y[16];
+    LB_CHECK(R >= 1 && R <= 16, LOWBIT_ERR_INVALID_ARG);
+    for (int r = 0; r < R; ++r) a[r] = p.ptr<const uint16_t>();
+    for (int r = 0; r < R; ++r) b[r] = p.ptr<const uint16_t>();
+    for (int r = 0; r < R; ++r) base[r] = p.ptr<const float>();
+    for (int r = 0; r < R; ++r) y[r] = p.ptr<float>();
+    return lowbit_lora_add_group(x, ids, a, b, ranks, scales, base, y, R, M, N, K, rank, L, workspace, bytes, stream);
+}
+
+lowbit_status lowbit_rope_args(const int64_t *args)
+{
+    LB_CHECK(args, LOWBIT_ERR_INVALID_ARG);
+    ArgBlock p{args};
+    const void *q = p.ptr<const void>();
+    const int64_t q_stride = p.word();
+    void *q_out = p.ptr<void>();
+    const int64_t q_out_stride = p.word();
+    const int q_heads = p.num();
+    const void *k = p.ptr<const void>();
+    const int64_t k_stride = p.word();
+    void *k_out = p.ptr<void>();
+    const int64_t k_out_stride = p.word();
+    const int kv_heads = p.num(), in_type = p.num(), out_type = p.num();
+    const int32_t *positions = p.ptr<const int32_t>();
+    const int64_t *phases = p.ptr<const int64_t>();
+    const int M = p.num(), head_dim = p.num(), rot = p.num(), interleaved = p.num();
+    const float magnitude = p.real();
+    return lowbit_rope(q, q_stride, q_out, q_out_stride, q_heads, k, k_stride, k_out, k_out_stride, kv_heads,
+                       (lowbit_dtype)in_type, (lowbit_dtype)out_type, positions, phases, M, head_dim, rot, interleaved,
+                       magnitude, p.ptr<void>());
+}
+
+lowbit_status lowbit_kv8_append_args(const int64_t *args)
+{
+    LB_CHECK(args, LOWBIT_ERR_INVALID_ARG);
+    ArgBlock p{args};
+    const lowbit_kv8_cache *cache = p.ptr<const lowbit_kv8_cache>();
+    const lowbit_kv8_batch batch = p.batch();
+    const void *k = p.ptr<const void>();
+    const int64_t k_stride = p.word();
+    const int k_type = p.num();
+    const void *v = p.ptr<const void>();
+    const int64_t v_stride = p.word();
+    const int v_type = p.num();
+    return lowbit_kv8_append(cache, &batch, k, k_stride, (lowbit_dtype)k_type, v, v_stride, (lowbit_dtype)v_type,
+                             p.ptr<void>());
+}
+
+lowbit_status lowbit_kv8_read_args(const int64_t *args)
+{
+    LB_CHECK(args, LOWBIT_ERR_INVALID_ARG);
+    ArgBlock p{args};
+    const lowbit_kv8_cache *cache = p.ptr<const lowbit_kv8_cache>();
+    const lowbit_kv8_batch batch = p.batch();
+    void *k_out = p.ptr<void>(), *v_out = p.ptr<void>();
+    const int out_type = p.num();
+    return lowbit_kv8_read(cache, &batch, k_out, v_out, (lowbit_dtype)out_type, p.ptr<void>());
+}
+
+lowbit_status lowbit_kv8_attention_args(const int64_t *args)
+{
+    LB_CHECK(args, LOWBIT_ERR_INVALID_ARG);
+    ArgBlock p{args};
+    const lowbit_kv8_cache *cache = p.ptr<const lowbit_kv8_cache>();
+    const lowbit_kv8_batch batch = p.batch();
+    const uint16_t *q = p.ptr<const uint16_t>();
+    const int64_t q_stride = p.word();
+    const int q_heads = p.num();
+    const float scale = p.real();
+    uint16_t *out = p.ptr<uint16_t>();
+    const int64_t out_stride = p.word();
+    void *workspace = p.ptr<void>();
+    const size_t bytes = (size_t)p.word();
+    return lowbit_kv8_attention(cache, &batch, q, q_stride, q_heads, scale, out, out_stride, workspace, bytes,
+                                p.ptr<void>());
 }
 
 }  // extern "C"

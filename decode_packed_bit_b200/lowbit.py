@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "liblowbit.so")
@@ -65,6 +66,11 @@ SYMBOLS = [
     ("lowbit_kv8_read", I32, [P, P, P, P, I32, P]),
     ("lowbit_kv8_attention_workspace_bytes", SZ, [P, P, I32]),
     ("lowbit_kv8_attention", I32, [P, P, P, I64, I32, F32, P, I64, P, SZ, P]),
+    ("lowbit_lora_add_group_args", I32, [P]),
+    ("lowbit_rope_args", I32, [P]),
+    ("lowbit_kv8_append_args", I32, [P]),
+    ("lowbit_kv8_read_args", I32, [P]),
+    ("lowbit_kv8_attention_args", I32, [P]),
 ]
 
 _lib = None
@@ -399,14 +405,18 @@ def _either(t, what):
 def _scratch(t, dev):
     """Address and bytes of a workspace (None: none)."""
     if t is None:
-        return None, 0
+        return 0, 0
     if t.get_device() != dev or not t.is_contiguous():
         _refuse(t, "workspace", f"a contiguous tensor on cuda:{dev}")
     return t.data_ptr(), t.nbytes
 
 
-def _ptrs(values):
-    return (ctypes.c_void_p * len(values))(*values)
+# The argument blocks of the calls below: 64-bit words in the order of the C parameters, 0 for NULL.
+_LORA_BLOCKS = {}  # by the number of projections
+_ROPE_BLOCK = struct.Struct("=18qdq").pack
+_APPEND_BLOCK = struct.Struct("=14q").pack
+_READ_BLOCK = struct.Struct("=11q").pack
+_ATTENTION_BLOCK = struct.Struct("=10qd5q").pack
 
 
 def lowbit_lora_workspace_bytes(R: int, M: int, N: int, K: int, rank: int) -> int:
@@ -427,14 +437,18 @@ def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, works
     L, rank, _ = a[0].shape
     N = b[0].shape[1]
     sa, sb, sy, sl = (L, rank, K), (L, N, rank), (M, N), (L,)
-    _check(lib().lowbit_lora_add_group(
+    block = _LORA_BLOCKS.get(R)
+    if block is None:
+        block = _LORA_BLOCKS[R] = struct.Struct(f"={13 + 4 * R}q").pack
+    ws, ws_bytes = _scratch(workspace, dev)
+    _check(lib().lowbit_lora_add_group_args(block(
         _bits16(x, (M, K), "x", dev), _dense(ids, _int32, (M,), "ids", dev),
-        _ptrs([_bits16(t, sa, "a", dev) for t in a]), _ptrs([_bits16(t, sb, "b", dev) for t in b]),
-        None if ranks is None else _dense(ranks, _int32, sl, "ranks", dev),
-        None if scales is None else _dense(scales, _float32, sl, "scales", dev),
-        _ptrs([_dense(t, _float32, sy, "base", dev) for t in base]), _ptrs([_dense(t, _float32, sy, "y", dev) for t in ys]),
-        R, M, N, K, rank, L, *_scratch(workspace, dev),
-        _raw_stream(stream, dev)), "lowbit_lora_add_group")
+        0 if ranks is None else _dense(ranks, _int32, sl, "ranks", dev),
+        0 if scales is None else _dense(scales, _float32, sl, "scales", dev),
+        R, M, N, K, rank, L, ws, ws_bytes, _raw_stream(stream, dev),
+        *[_bits16(t, sa, "a", dev) for t in a], *[_bits16(t, sb, "b", dev) for t in b],
+        *[_dense(t, _float32, sy, "base", dev) for t in base], *[_dense(t, _float32, sy, "y", dev) for t in ys])),
+        "lowbit_lora_add_group")
 
 
 def lowbit_lora_add(x, ids, a, b, base, y, ranks=None, scales=None, workspace=None, stream=None):
@@ -462,8 +476,7 @@ def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnit
     M, _, D = ref.shape
     half = phases.shape[0]
     ti, to = _either(ref, "input"), _either(ref_out, "output")
-    qp = qo = kp = ko = None
-    qs = qos = qh = ks = kos = kh = 0
+    qp = qo = kp = ko = qs = qos = qh = ks = kos = kh = 0
     if q is not None:
         qh = q.shape[1]
         qp, qs = _rows(q, ref.dtype, (M, qh, D), "q", dev)
@@ -472,10 +485,11 @@ def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnit
         kh = k.shape[1]
         kp, ks = _rows(k, ref.dtype, (M, kh, D), "k", dev)
         ko, kos = _rows(k_out, ref_out.dtype, (M, kh, D), "k_out", dev)
-    _check(lib().lowbit_rope(qp, qs, qo, qos, qh, kp, ks, ko, kos, kh, ti, to,
-                             _dense(positions, _int32, (M,), "positions", dev),
-                             _dense(phases, _int64, (half,), "phases", dev), M, D, 2 * half,
-                             1 if interleaved else 0, magnitude, _raw_stream(stream, dev)), "lowbit_rope")
+    _check(lib().lowbit_rope_args(_ROPE_BLOCK(qp, qs, qo, qos, qh, kp, ks, ko, kos, kh, ti, to,
+                                              _dense(positions, _int32, (M,), "positions", dev),
+                                              _dense(phases, _int64, (half,), "phases", dev), M, D, 2 * half,
+                                              1 if interleaved else 0, magnitude, _raw_stream(stream, dev))),
+           "lowbit_rope")
 
 
 # -- KV8 cache ----------------------------------------------------------------------
@@ -502,7 +516,7 @@ class KV8Cache:
                              _dense(v, _int8, (n_pages, heads, page, dim), "v", dev),
                              _dense(v_scales, _float32, (n_pages, heads), "v_scales", dev), n_pages, heads, page,
                              dim)
-        self._ref = ctypes.byref(self._c)
+        self._at = ctypes.addressof(self._c)
         self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
         self.n_pages, self.n_heads, self.page_tokens, self.head_dim, self.device = n_pages, heads, page, dim, dev
 
@@ -524,8 +538,8 @@ def _kv8_batch(cache, page_table, kv_len, row_start, rows, dev):
     B, width = page_table.shape
     if cache.device != dev:
         raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
-    return _KV8BatchC(_dense(kv_len, i32, (B,), "kv_len", dev), _dense(page_table, i32, (B, width), "page_table", dev),
-                      None if row_start is None else _dense(row_start, i32, (B + 1,), "row_start", dev), B, width, rows)
+    return (_dense(kv_len, i32, (B,), "kv_len", dev), _dense(page_table, i32, (B, width), "page_table", dev),
+            0 if row_start is None else _dense(row_start, i32, (B + 1,), "row_start", dev), B, width, rows)
 
 
 def lowbit_kv8_append(cache: KV8Cache, page_table, kv_len, k, v, row_start=None, stream=None):
@@ -539,7 +553,7 @@ def lowbit_kv8_append(cache: KV8Cache, page_table, kv_len, k, v, row_start=None,
     tk, tv = _either(k, "k"), _either(v, "v")
     kp, ks = _rows(k, k.dtype, shape, "k", dev)
     vp, vs = _rows(v, v.dtype, shape, "v", dev)
-    _check(lib().lowbit_kv8_append(cache._ref, ctypes.byref(batch), kp, ks, tk, vp, vs, tv, _raw_stream(stream, dev)),
+    _check(lib().lowbit_kv8_append_args(_APPEND_BLOCK(cache._at, *batch, kp, ks, tk, vp, vs, tv, _raw_stream(stream, dev))),
            "lowbit_kv8_append")
 
 
@@ -551,16 +565,16 @@ def lowbit_kv8_read(cache: KV8Cache, page_table, kv_len, k_out, v_out, row_start
     rows = ref.shape[0]
     shape = (rows, cache.n_heads, cache.head_dim)
     batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
-    _check(lib().lowbit_kv8_read(cache._ref, ctypes.byref(batch),
-                                 None if k_out is None else _dense(k_out, ref.dtype, shape, "k_out", dev),
-                                 None if v_out is None else _dense(v_out, ref.dtype, shape, "v_out", dev),
-                                 _either(ref, "output"), _raw_stream(stream, dev)), "lowbit_kv8_read")
+    _check(lib().lowbit_kv8_read_args(_READ_BLOCK(cache._at, *batch,
+                                                  0 if k_out is None else _dense(k_out, ref.dtype, shape, "k_out", dev),
+                                                  0 if v_out is None else _dense(v_out, ref.dtype, shape, "v_out", dev),
+                                                  _either(ref, "output"), _raw_stream(stream, dev))), "lowbit_kv8_read")
 
 
 def lowbit_kv8_attention_workspace_bytes(cache: KV8Cache, n_seqs: int, n_rows: int, q_heads: int) -> int:
     """Bytes for calls with this many sequences and rows (zero-fill them once)."""
     batch = _KV8BatchC(16, 16, 16, n_seqs, 1, n_rows)
-    return int(lib().lowbit_kv8_attention_workspace_bytes(cache._ref, ctypes.byref(batch), q_heads))
+    return int(lib().lowbit_kv8_attention_workspace_bytes(cache._at, ctypes.byref(batch), q_heads))
 
 
 def lowbit_kv8_attention(cache: KV8Cache, page_table, kv_len, q, out, scale, row_start=None, workspace=None,
@@ -576,6 +590,6 @@ def lowbit_kv8_attention(cache: KV8Cache, page_table, kv_len, q, out, scale, row
     batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
     qp, qs = _rows(q, _bfloat16, shape, "q", dev)
     op, os_ = _rows(out, _bfloat16, shape, "out", dev)
-    _check(lib().lowbit_kv8_attention(cache._ref, ctypes.byref(batch), qp, qs, heads, scale, op, os_,
-                                      *_scratch(workspace, dev),
-                                      _raw_stream(stream, dev)), "lowbit_kv8_attention")
+    ws, ws_bytes = _scratch(workspace, dev)
+    _check(lib().lowbit_kv8_attention_args(_ATTENTION_BLOCK(cache._at, *batch, qp, qs, heads, scale, op, os_, ws, ws_bytes,
+                                                            _raw_stream(stream, dev))), "lowbit_kv8_attention")

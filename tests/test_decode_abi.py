@@ -119,6 +119,60 @@ def kv8(lb, cache=(), batch=()):
     return lb._KV8CacheC(**c), lb._KV8BatchC(**b)
 
 
+def test_argument_blocks(lb):
+    """A block carries every parameter to its place: each one's refusal comes back through it as it does from the call."""
+    L = lb.lib()
+    at = 0x10000
+
+    def lora(x=at, ids=at, ranks=0, scales=0, R=1, M=4, N=64, K=128, rank=16, adapters=2, ws=at, n=BIG, a=at, b=at, base=at, y=at):
+        return L.lowbit_lora_add_group_args(lb._LORA_BLOCKS.setdefault(1, lb.struct.Struct("=17q").pack)(
+            x, ids, ranks, scales, R, M, N, K, rank, adapters, ws, n, 0, a, b, base, y))
+
+    for name in ("x", "ids", "a", "b", "base", "y"):
+        assert lora(**{name: 0}) == 1 and lora(**{name: at + 8}) == 2, name
+    assert lora(ranks=at + 8) == 2 and lora(scales=at + 8) == 2 and lora(ws=at + 8) == 2 and lora(ws=0) == 1
+    assert lora(R=0) == 1 and lora(R=17) == 1 and lora(M=0) == 1 and lora(N=0) == 1 and lora(K=96) == 3
+    assert lora(rank=12) == 3 and lora(adapters=0) == 1 and lora(n=16) == 1
+
+    names = "q qs qo qos qh k ks ko kos kh ti to pos ph M D rot inter mag stream".split()
+    base = dict(q=at, qs=256, qo=2 * at, qos=256, qh=2, k=at, ks=128, ko=2 * at, kos=128, kh=1, ti=0, to=1, pos=at, ph=at,
+                M=2, D=128, rot=64, inter=0, mag=1.0, stream=0)
+
+    def rope(**kw):
+        return L.lowbit_rope_args(lb._ROPE_BLOCK(*[{**base, **kw}[n] for n in names]))
+
+    for name in ("q", "qo", "k", "ko", "pos", "ph"):
+        assert rope(**{name: 0}) == 1 and rope(**{name: at + 8}) == 2, name
+    for name in ("qs", "qos", "ks", "kos"):
+        assert rope(**{name: 0}) == 1 and rope(**{name: 1 << 40}) == 3, name
+    assert rope(qh=-1) == 1 and rope(kh=-1) == 1 and rope(ti=2) == 1 and rope(to=2) == 1 and rope(M=0) == 1
+    assert rope(D=12) == 3 and rope(rot=63) == 3
+
+    c, b = kv8(lb)
+    cache, batch = ctypes.addressof(c), [at, at, at, 2, 4, 3]
+    append, read, attend = L.lowbit_kv8_append_args, L.lowbit_kv8_read_args, L.lowbit_kv8_attention_args
+    good = [at, 128, 0, at, 128, 0, 0]
+    for i, bad in ((0, at + 8), (1, 132), (3, at + 8), (4, 132)):
+        assert append(lb._APPEND_BLOCK(cache, *batch, *good[:i], bad, *good[i + 1:])) == 2
+    for i, bad in ((2, 2), (5, 2)):
+        assert append(lb._APPEND_BLOCK(cache, *batch, *good[:i], bad, *good[i + 1:])) == 1
+    assert read(lb._READ_BLOCK(cache, *batch, at + 8, 0, 0, 0)) == 2 and read(lb._READ_BLOCK(cache, *batch, 0, at + 8, 0, 0)) == 2
+    assert read(lb._READ_BLOCK(cache, *batch, at, 0, 5, 0)) == 1
+    good = [at, 256, 4, 0.1, at, 256, at, BIG, 0]
+    for i, bad, status in ((0, at + 8, 2), (1, 260, 2), (2, 3, 1), (3, float("nan"), 1), (4, at + 8, 2), (5, 260, 2), (6, at + 8, 2),
+                           (7, 16, 1)):
+        assert attend(lb._ATTENTION_BLOCK(cache, *batch, *good[:i], bad, *good[i + 1:])) == status, i
+    for i, bad, status in ((0, 0, 1), (1, at + 4, 2), (2, at + 4, 2), (3, -1, 1), (4, 0, 1), (5, -1, 1)):
+        broken = batch[:i] + [bad] + batch[i + 1:]
+        assert append(lb._APPEND_BLOCK(cache, *broken, at, 128, 0, at, 128, 0, 0)) == status
+        assert read(lb._READ_BLOCK(cache, *broken, at, at, 0, 0)) == status
+        assert attend(lb._ATTENTION_BLOCK(cache, *broken, *good)) == status
+    for f, n in ((append, 14), (read, 11), (attend, 16)):
+        assert f(lb.struct.pack(f"={n}q", 0, *batch, *[0] * (n - 7))) == 1
+        assert f(None) == 1
+    assert L.lowbit_lora_add_group_args(None) == 1 and L.lowbit_rope_args(None) == 1
+
+
 def test_sizes_whose_indices_would_wrap(lb):
     assert lb.lowbit_lora_workspace_bytes(1, 1, (1 << 25) + 8, 64, 8) == 0   # more column ranges than a grid has
     assert lb.lowbit_lora_workspace_bytes(1, 1, 1 << 25, 64, 8) > 0
