@@ -220,7 +220,9 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_few(const LoraArgs
     }
 }
 
-// Many rows: grid (blocks of 16 RB rows x slices, projections).
+// Many rows: grid (blocks of 16 RB rows x slices, projections, 2): z = 0 takes a
+// block's first adapter, z = 1 its others (with one CTA for
+// all, the blocks where prompts meet ended last: 4096 rows x 4096 25.8 us, so 20.5).
 // NT: rank / 8, rounded up to 2, 4, 8 or 16.
 template <int NT, int RB>
 __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink(const LoraArgs a)
@@ -237,7 +239,9 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink(const LoraArgs a)
     const int2 k = lora_range(a, slice, warp);
     float *tp = a.t + ((int64_t)target * a.slices + slice) * a.M * a.rank;
     const int half = a.rank / 2;
-    for (unsigned todo = lora_distinct(id, lane); todo; todo &= todo - 1) {
+    unsigned todo = lora_distinct(id, lane);
+    const unsigned first = todo & (0u - todo);
+    for (todo = blockIdx.z ? todo ^ first : first; todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1;
         const int i = __shfl_sync(0xffffffffu, id, src), rank = __shfl_sync(0xffffffffu, my_rank, src);
         const uint16_t *xp[RB][2];
@@ -310,13 +314,13 @@ struct LoraPieces {
     }
 };
 
-// acc += the block's rows of t (f: three bf16 numbers each) times a stage's 16
+// acc = the block's rows of t (f: their bf16 numbers, in NS fragments) times a stage's 16
 // columns of B.  Steps of 16 entries beyond the adapter's rank are left out (with
 // one or two steps the branch costs more than it saves: 94 against 85 us for
 // 4096 rows of rank 32), and in the step that it ends in the entries from the rank on are cleared: they
 // may hold anything.
-template <int KT, int RB>
-__device__ __forceinline__ void lora_mul(const uint32_t (&f)[RB][KT][3][4], unsigned src, int rank, int g, int t,
+template <int KT, int RB, int NS>
+__device__ __forceinline__ void lora_mul(const uint32_t (&f)[RB][KT][NS][4], unsigned src, int rank, int g, int t,
                                          float (&acc)[RB][2][4])
 {
 #pragma unroll
@@ -353,7 +357,7 @@ __device__ __forceinline__ void lora_mul(const uint32_t (&f)[RB][KT][3][4], unsi
             }
         }
 #pragma unroll
-        for (int s = 0; s < 3; ++s)
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
             for (int q = 0; q < RB; ++q)
 #pragma unroll
@@ -427,46 +431,33 @@ __device__ __forceinline__ void lora_acc(float4 &o, const float (&acc)[2][4], in
     o.x += acc[0][2 * h]; o.y += acc[0][2 * h + 1]; o.z += acc[1][2 * h]; o.w += acc[1][2 * h + 1];
 }
 
-// Few rows: grid (rows, column ranges, projections); the CTA of an adapter's
-// first row takes all its rows, 16 at a time; a row without an adapter is copied.
-// KT: rank / 16, rounded up to 1, 2, 4 or 8; VEC: rows of y are 16-byte aligned.
-template <int KT, bool VEC>
-__global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_expand_few(const LoraArgs a)
+// One adapter's rows over columns [c0, n_end).  SMALL: up to four rows, whose
+// three numbers lie in one fragment (rows 0-3 the first, 4-7 the second, 8-11
+// the third), a third of the MMAs; else 16 rows at a time.
+template <int KT, bool VEC, bool SMALL>
+__device__ __forceinline__ void lora_expand_rows(const LoraArgs &a, const LoraRows &own, const int *rows, uint4 *frag, unsigned ring,
+                                                 int c0, int n_end)
 {
     using S = LoraRing<KT, 1>;
-    extern __shared__ __align__(128) uint8_t ring_mem[];
-    __shared__ int rows[kLoraFewRows], warp_n[kLoraWarps];
-    __shared__ uint4 frag[KT * 3 * 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const unsigned ring = (unsigned)__cvta_generic_to_shared(ring_mem) + warp * S::kStages * S::kStage;
-    pdl_launch_dependents();
-    const int target = blockIdx.z;
-    const LoraRows own = lora_gather(a, blockIdx.x, rows, warp_n);
+    constexpr int NS = SMALL ? 1 : 3, NH = SMALL ? 1 : 2, kRows = SMALL ? 4 : 16, kStep = kLoraWarps * 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3, target = blockIdx.z;
     const float *base = a.base[target];
     float *y = a.y[target];
-    const int c0 = blockIdx.y * a.cols, n_end = min(a.N, c0 + a.cols);
-    if (own.n == 0) {
-        pdl_wait_primary();
-        if (own.id < 0 && y != base)
-            for (int n = c0 + threadIdx.x; n < n_end; n += kLoraThreads)
-                y[(int64_t)blockIdx.x * a.N + n] = base[(int64_t)blockIdx.x * a.N + n];
-        return;
-    }
-    constexpr int kStep = kLoraWarps * 16;
     LoraPieces<KT, 1> pieces;
     pieces.set(own.rank, a.rank, lane);
     const uint16_t *b = a.b[target] + (int64_t)own.id * a.N * a.rank + lane * 8;
-    for (int r0 = 0; r0 < own.n; r0 += 16) {
-        int64_t at[2];  // offsets of this thread's rows, -1 for none
+    for (int r0 = 0; r0 < own.n; r0 += kRows) {
+        int64_t at[NH];  // offsets of this thread's rows, -1 for none
 #pragma unroll
-        for (int h = 0; h < 2; ++h) at[h] = r0 + h * 8 + g < own.n ? (int64_t)rows[r0 + h * 8 + g] * a.N : -1;
+        for (int h = 0; h < NH; ++h)
+            at[h] = g < kRows && r0 + h * 8 + g < own.n ? (int64_t)rows[r0 + h * 8 + g] * a.N : -1;
         int n0 = c0 + warp * 16, ahead = n0, put = 0, get = 0;
         auto issue = [&]() {
             if (ahead < n_end) {
                 const unsigned st = ring + put * S::kStage;
                 if (VEC)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // row h * 8 + g, columns 4 t ..
+                    for (int h = 0; h < NH; ++h) {  // row h * 8 + g, columns 4 t ..
                         if (at[h] >= 0 && ahead + 4 * t < a.N)
                             lora_cp16(st + (h * 8 + g) * 64 + t * 16, base + at[h] + ahead + 4 * t);
                     }
@@ -486,22 +477,26 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
             const int k = e / 32, eg = (e & 31) >> 2, et = e & 3;
             uint32_t f[3][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NH; ++h) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r0 + h * 8 + eg < own.n)
-                    v = lora_t4(a, target, rows[r0 + h * 8 + eg], own.id, own.rank, k * 16 + 4 * et);
+                const int row = r0 + h * 8 + (SMALL ? eg & 3 : eg);
+                if (row < own.n) v = lora_t4(a, target, rows[row], own.id, own.rank, k * 16 + 4 * et);
                 lora_split(v, f, h);
             }
+            if (SMALL)
+                frag[e] = eg < 4 ? make_uint4(f[0][0], f[2][0], f[0][2], f[2][2]) : make_uint4(f[1][0], 0, f[1][2], 0);
+            else
 #pragma unroll
-            for (int s = 0; s < 3; ++s) frag[(k * 3 + s) * 32 + (e & 31)] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+                for (int s = 0; s < 3; ++s)
+                    frag[(k * 3 + s) * 32 + (e & 31)] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
         }
         __syncthreads();
-        uint32_t f[1][KT][3][4];
+        uint32_t f[1][KT][NS][4];
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
-                const uint4 u = frag[(k * 3 + s) * 32 + lane];
+            for (int s = 0; s < NS; ++s) {
+                const uint4 u = frag[(k * NS + s) * 32 + lane];
                 f[0][k][s][0] = u.x; f[0][k][s][1] = u.y; f[0][k][s][2] = u.z; f[0][k][s][3] = u.w;
             }
         for (; n0 < n_end; n0 += kStep) {
@@ -511,11 +506,17 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
             const unsigned st = ring + get * S::kStage;
             get = get + 1 == S::kStages ? 0 : get + 1;
             const int n = n0 + 4 * t;
-            float4 o[2];
+            float4 o[NH];
             float acc[1][2][4];
-            lora_mul<KT, 1>(f, st + S::kBase, own.rank, g, t, acc);
+            lora_mul<KT, 1, NS>(f, st + S::kBase, own.rank, g, t, acc);
+            if (SMALL)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)  // rows g and g + 4, then g + 8
+                        acc[0][j][c] += __shfl_xor_sync(0xffffffffu, acc[0][j][c], 16) + acc[0][j][2 + c];
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
                 if (VEC)
                     asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
                                  : "=f"(o[h].x), "=f"(o[h].y), "=f"(o[h].z), "=f"(o[h].w)
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
                     o[h] = lora_load4(base + (at[h] < 0 ? 0 : at[h]) + n, at[h] < 0 ? 0 : a.N - n);
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < NH; ++h) {
                 lora_acc(o[h], acc[0], h);
                 if (at[h] >= 0) lora_store4<VEC>(y + at[h] + n, a.N - n, o[h]);
             }
@@ -532,6 +533,37 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Few rows: grid (rows, column ranges, projections); the CTA of an adapter's
+// first row takes all its rows; a row without an adapter is copied.
+// KT: rank / 16, rounded up to 1, 2, 4 or 8; VEC: rows of y are 16-byte aligned.
+template <int KT, bool VEC>
+__global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_expand_few(const LoraArgs a)
+{
+    using S = LoraRing<KT, 1>;
+    extern __shared__ __align__(128) uint8_t ring_mem[];
+    __shared__ int rows[kLoraFewRows], warp_n[kLoraWarps];
+    __shared__ uint4 frag[KT * 3 * 32];
+    const unsigned ring = (unsigned)__cvta_generic_to_shared(ring_mem) + (threadIdx.x >> 5) * S::kStages * S::kStage;
+    pdl_launch_dependents();
+    const LoraRows own = lora_gather(a, blockIdx.x, rows, warp_n);
+    const int c0 = blockIdx.y * a.cols, n_end = min(a.N, c0 + a.cols);
+    if (own.n == 0) {
+        const float *base = a.base[blockIdx.z];
+        float *y = a.y[blockIdx.z];
+        pdl_wait_primary();
+        if (own.id < 0 && y != base)
+            for (int n = c0 + threadIdx.x; n < n_end; n += kLoraThreads)
+                y[(int64_t)blockIdx.x * a.N + n] = base[(int64_t)blockIdx.x * a.N + n];
+        return;
+    }
+    // (a rank of 16 has three MMAs to save, and two ways cost it registers: 12.9
+    // against 12.3 us for 16 rows of three 5120 x 5120 projections)
+    if (KT > 1 && own.n <= 4)
+        lora_expand_rows<KT, VEC, true>(a, own, rows, frag, ring, c0, n_end);
+    else
+        lora_expand_rows<KT, VEC, false>(a, own, rows, frag, ring, c0, n_end);
 }
 
 // Many rows: grid (blocks of 16 RB rows, column ranges, projections):
@@ -623,7 +655,7 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, RB>::kCtas) k_lora_
         int i = id0, rank = rank0;
         for (unsigned todo = distinct; todo;) {
             float acc[RB][2][4];
-            lora_mul<KT, RB>(f, st + S::kBase, rank, g, t, acc);
+            lora_mul<KT, RB, 3>(f, st + S::kBase, rank, g, t, acc);
 #pragma unroll
             for (int q = 0; q < RB; ++q)
 #pragma unroll
@@ -666,7 +698,8 @@ struct LoraPlan {
 // rb: rows per block / 16; 32 rows (each weight loaded for twice the rows) where
 // their fragments leave registers for two CTAs per SM.  Slices of K: about two
 // CTAs per SM in the first launch, of at least 64 k for each warp; a decode
-// batch counts as M / 2 adapters.
+// batch counts as M / 2 adapters (61 rows, rank 64, K = 5120 in 4 slices: with 2
+// the two launches take 58 us in place of 47, with 6 50.7, with 8 52.7).
 static LoraPlan lora_plan(int R, int M, int K, int rank)
 {
     LoraPlan p;
@@ -726,13 +759,17 @@ lowbit_status lora_launch(const uint16_t *x, const int32_t *ids, const uint16_t 
     g.slices = p.slices; g.kslice = p.kslice;
     const int64_t groups = p.few ? M : ((int64_t)M + 16 * p.rb - 1) / (16 * p.rb);
     // Columns per CTA of the second launch, in rounds of the CTA's warps: as few as
-    // fill the SMs at once, at most eight (CTAs with more adapters or a higher rank
-    // take longer; with 43 rounds each, half of the SMs' time was spent waiting for
-    // the last of them).
+    // fill the SMs at once (a decode batch counts as 3 / 4 M adapters: 10.5 us for 16
+    // rows of three 5120 x 5120 projections against 12.3 as M / 2 and 10.9 as M), at
+    // most 20 for few rows and 8 for many.  A CTA has 3 us to go before its first
+    // round, but those with more adapters or a higher rank take longer and the SMs
+    // wait for the last of them: 61 rows, rank 64, 17408 columns 51.6 us with 8,
+    // 47.1 with 20, 52.5 with 27; 4096 rows, rank 32, 11008 columns 93.6 us with 8,
+    // 98.3 with 12, 102 with 17.
     const int64_t rounds = (N + kLoraWarps * 16 - 1) / (kLoraWarps * 16), slots = (rank <= 16 && p.few ? 4 : rank <= 64 ? 2 : 1) * 148;
-    const int64_t each = (rounds * (p.few ? (groups + 1) / 2 : groups) * R + slots - 1) / slots;
-    g.cols = (int)std::min<int64_t>(std::max<int64_t>(each, 1), 8) * kLoraWarps * 16;
-    const dim3 gs((unsigned)(groups * p.slices), R), ge((unsigned)groups, (unsigned)((N + g.cols - 1) / g.cols), R);
+    const int64_t each = (rounds * (p.few ? (3 * groups + 3) / 4 : groups) * R + slots - 1) / slots;
+    g.cols = (int)std::min<int64_t>(std::max<int64_t>(each, 1), p.few ? 20 : 8) * kLoraWarps * 16;
+    const dim3 gs((unsigned)(groups * p.slices), R, p.few ? 1 : 2), ge((unsigned)groups, (unsigned)((N + g.cols - 1) / g.cols), R);
     const cudaError_t e = rank <= 16   ? lora_run<1>(p, gs, ge, g, st)
                           : rank <= 32 ? lora_run<2>(p, gs, ge, g, st)
                           : rank <= 64 ? lora_run<4>(p, gs, ge, g, st)
