@@ -1,4 +1,5 @@
-"""Build liblowbit.so (sm_100a) in-tree with nvcc.
+"""Build liblowbit.so (sm_100a) in-tree with nvcc, and the binding's compiled
+part (_marshal.so, csrc/marshal.cpp) with g++ against the installed torch.
 
 The library is rebuilt when the SHA-1 of its sources and flags changes, so a
 stale binary can never be loaded after the sources move on.  Usage:
@@ -10,10 +11,12 @@ from __future__ import annotations
 import argparse
 import glob
 import hashlib
+import importlib.metadata
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblowbit.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 STAMP = os.path.join(PKG, ".liblowbit.sha1")
 OBJDIR = os.path.join(ROOT, "_build", "lowbit")
 
@@ -72,10 +76,41 @@ def kernel_digest(files=None) -> str:
     return h.hexdigest()
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile csrc/marshal.cpp into the package."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    flags = ["-O2", "-std=c++17", "-shared", "-fPIC"]
+    h = hashlib.sha1(" ".join(flags + [importlib.metadata.version("torch"), sys.version]).encode())
+    with open(src, "rb") as f:
+        h.update(f.read())
+    stamp = os.path.join(PKG, ".marshal.sha1")
+    if not force and os.path.exists(MARSHAL) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == h.hexdigest():
+                return MARSHAL
+    import torch
+    home = os.path.dirname(torch.__file__)
+    include = [sysconfig.get_paths()["include"], os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include")]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), *flags, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *["-I" + d for d in include], src, "-L" + os.path.join(home, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {src}:\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    with open(stamp, "w") as f:
+        f.write(h.hexdigest() + "\n")
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, out: str | None = None, defines=()) -> str:
     """Compile every csrc/*.cu and link liblowbit.so.  `out` and `defines`
     (extra -D flags) build a variant elsewhere, e.g. for a tuning sweep; the
-    default is the in-tree library."""
+    default is the in-tree library, and the binding's compiled part beside it."""
+    if out is None:
+        build_marshal(force)
     lib = out or LIB
     stamp = STAMP if out is None else out + ".sha1"
     objdir = OBJDIR if out is None else out + ".objs"

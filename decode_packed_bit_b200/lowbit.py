@@ -11,7 +11,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "liblowbit.so")
@@ -344,15 +343,24 @@ LOWBIT_F32 = 0
 LOWBIT_BF16 = 1
 ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 _types = {}  # torch dtypes of the operands that may be either -> lowbit_dtype
-_float32 = _bfloat16 = _int32 = _int64 = _int16 = _int8 = None  # torch's, set on the first call (torch is imported late)
+_float32 = _bfloat16 = _int32 = _int64 = _int8 = None  # torch's, set on the first call (torch is imported late)
+_halves = None  # bf16 values, as such or as int16 bit patterns
+_dense = _rows = _scratch = _call = None  # csrc/marshal.cpp's: the checks of operands, and the call with a block of words
+_LORA = _ROPE = _APPEND = _READ = _ATTENTION = 0  # addresses of the entry points that take a block
 
 
 def _first_call():
     import torch
-    global _float32, _bfloat16, _int32, _int64, _int16, _int8, _device, _current_stream
+    from . import _marshal
+    global _float32, _bfloat16, _int32, _int64, _int8, _halves, _dense, _rows, _scratch, _call
+    global _LORA, _ROPE, _APPEND, _READ, _ATTENTION, _device, _current_stream
     torch.cuda.init()
     _float32, _bfloat16 = torch.float32, torch.bfloat16
-    _int32, _int64, _int16, _int8 = torch.int32, torch.int64, torch.int16, torch.int8
+    _int32, _int64, _int8, _halves = torch.int32, torch.int64, torch.int8, (torch.bfloat16, torch.int16)
+    _dense, _rows, _scratch, _call = _marshal.dense, _marshal.rows, _marshal.scratch, _marshal.call
+    _LORA, _ROPE, _APPEND, _READ, _ATTENTION = (
+        ctypes.cast(getattr(lib(), f"lowbit_{name}_args"), P).value
+        for name in ("lora_add_group", "rope", "kv8_append", "kv8_read", "kv8_attention"))
     _types.update({_float32: LOWBIT_F32, _bfloat16: LOWBIT_BF16})
     _device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     return _device()
@@ -368,55 +376,11 @@ def _raw_stream(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _refuse(t, what, expected):
-    raise ValueError(f"{what}: expected {expected}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
-def _dense(t, dtype, shape, what, dev):
-    """The address of t: a dense tensor of this type and shape on device dev."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(t, what, f"a contiguous {dtype} tensor of shape {shape} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _bits16(t, shape, what, dev):
-    """The same for bf16 values, as such or as int16 bit patterns."""
-    return _dense(t, _int16 if t.dtype is _int16 else _bfloat16, shape, what, dev)
-
-
-def _rows(t, dtype, shape, what, dev):
-    """Address and row stride of a [rows][heads][dim] tensor whose rows are dense and may lie apart."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _refuse(t, what, f"a {dtype} tensor of shape {shape} with dense rows on cuda:{dev}")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1] * shape[2]
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != shape[2] and shape[1] > 1):
-        _refuse(t, what, f"a {dtype} tensor of shape {shape} with dense rows on cuda:{dev}")
-    return t.data_ptr(), s0
-
-
 def _either(t, what):
-    if t.dtype not in _types:
-        _refuse(t, what, "float32 or bfloat16")
-    return _types[t.dtype]
-
-
-def _scratch(t, dev):
-    """Address and bytes of a workspace (None: none)."""
-    if t is None:
-        return 0, 0
-    if t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, "workspace", f"a contiguous tensor on cuda:{dev}")
-    return t.data_ptr(), t.nbytes
-
-
-# The argument blocks of the calls below: 64-bit words in the order of the C parameters, 0 for NULL.
-_LORA_BLOCKS = {}  # by the number of projections
-_ROPE_BLOCK = struct.Struct("=18qdq").pack
-_APPEND_BLOCK = struct.Struct("=14q").pack
-_READ_BLOCK = struct.Struct("=11q").pack
-_ATTENTION_BLOCK = struct.Struct("=10qd5q").pack
+    found = _types.get(t.dtype)
+    if found is None:
+        raise ValueError(f"{what}: expected float32 or bfloat16, got {t.dtype}")
+    return found
 
 
 def lowbit_lora_workspace_bytes(R: int, M: int, N: int, K: int, rank: int) -> int:
@@ -437,17 +401,14 @@ def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, works
     L, rank, _ = a[0].shape
     N = b[0].shape[1]
     sa, sb, sy, sl = (L, rank, K), (L, N, rank), (M, N), (L,)
-    block = _LORA_BLOCKS.get(R)
-    if block is None:
-        block = _LORA_BLOCKS[R] = struct.Struct(f"={13 + 4 * R}q").pack
     ws, ws_bytes = _scratch(workspace, dev)
-    _check(lib().lowbit_lora_add_group_args(block(
-        _bits16(x, (M, K), "x", dev), _dense(ids, _int32, (M,), "ids", dev),
+    _check(_call(
+        _LORA, _dense(x, _halves, (M, K), "x", dev), _dense(ids, _int32, (M,), "ids", dev),
         0 if ranks is None else _dense(ranks, _int32, sl, "ranks", dev),
         0 if scales is None else _dense(scales, _float32, sl, "scales", dev),
         R, M, N, K, rank, L, ws, ws_bytes, _raw_stream(stream, dev),
-        *[_bits16(t, sa, "a", dev) for t in a], *[_bits16(t, sb, "b", dev) for t in b],
-        *[_dense(t, _float32, sy, "base", dev) for t in base], *[_dense(t, _float32, sy, "y", dev) for t in ys])),
+        *[_dense(t, _halves, sa, "a", dev) for t in a], *[_dense(t, _halves, sb, "b", dev) for t in b],
+        *[_dense(t, _float32, sy, "base", dev) for t in base], *[_dense(t, _float32, sy, "y", dev) for t in ys]),
         "lowbit_lora_add_group")
 
 
@@ -485,11 +446,9 @@ def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnit
         kh = k.shape[1]
         kp, ks = _rows(k, ref.dtype, (M, kh, D), "k", dev)
         ko, kos = _rows(k_out, ref_out.dtype, (M, kh, D), "k_out", dev)
-    _check(lib().lowbit_rope_args(_ROPE_BLOCK(qp, qs, qo, qos, qh, kp, ks, ko, kos, kh, ti, to,
-                                              _dense(positions, _int32, (M,), "positions", dev),
-                                              _dense(phases, _int64, (half,), "phases", dev), M, D, 2 * half,
-                                              1 if interleaved else 0, magnitude, _raw_stream(stream, dev))),
-           "lowbit_rope")
+    _check(_call(_ROPE, qp, qs, qo, qos, qh, kp, ks, ko, kos, kh, ti, to, _dense(positions, _int32, (M,), "positions", dev),
+                 _dense(phases, _int64, (half,), "phases", dev), M, D, 2 * half, 1 if interleaved else 0, float(magnitude),
+                 _raw_stream(stream, dev)), "lowbit_rope")
 
 
 # -- KV8 cache ----------------------------------------------------------------------
@@ -553,8 +512,7 @@ def lowbit_kv8_append(cache: KV8Cache, page_table, kv_len, k, v, row_start=None,
     tk, tv = _either(k, "k"), _either(v, "v")
     kp, ks = _rows(k, k.dtype, shape, "k", dev)
     vp, vs = _rows(v, v.dtype, shape, "v", dev)
-    _check(lib().lowbit_kv8_append_args(_APPEND_BLOCK(cache._at, *batch, kp, ks, tk, vp, vs, tv, _raw_stream(stream, dev))),
-           "lowbit_kv8_append")
+    _check(_call(_APPEND, cache._at, *batch, kp, ks, tk, vp, vs, tv, _raw_stream(stream, dev)), "lowbit_kv8_append")
 
 
 def lowbit_kv8_read(cache: KV8Cache, page_table, kv_len, k_out, v_out, row_start=None, stream=None):
@@ -565,10 +523,9 @@ def lowbit_kv8_read(cache: KV8Cache, page_table, kv_len, k_out, v_out, row_start
     rows = ref.shape[0]
     shape = (rows, cache.n_heads, cache.head_dim)
     batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
-    _check(lib().lowbit_kv8_read_args(_READ_BLOCK(cache._at, *batch,
-                                                  0 if k_out is None else _dense(k_out, ref.dtype, shape, "k_out", dev),
-                                                  0 if v_out is None else _dense(v_out, ref.dtype, shape, "v_out", dev),
-                                                  _either(ref, "output"), _raw_stream(stream, dev))), "lowbit_kv8_read")
+    _check(_call(_READ, cache._at, *batch, 0 if k_out is None else _dense(k_out, ref.dtype, shape, "k_out", dev),
+                 0 if v_out is None else _dense(v_out, ref.dtype, shape, "v_out", dev), _either(ref, "output"),
+                 _raw_stream(stream, dev)), "lowbit_kv8_read")
 
 
 def lowbit_kv8_attention_workspace_bytes(cache: KV8Cache, n_seqs: int, n_rows: int, q_heads: int) -> int:
@@ -591,5 +548,5 @@ def lowbit_kv8_attention(cache: KV8Cache, page_table, kv_len, q, out, scale, row
     qp, qs = _rows(q, _bfloat16, shape, "q", dev)
     op, os_ = _rows(out, _bfloat16, shape, "out", dev)
     ws, ws_bytes = _scratch(workspace, dev)
-    _check(lib().lowbit_kv8_attention_args(_ATTENTION_BLOCK(cache._at, *batch, qp, qs, heads, scale, op, os_, ws, ws_bytes,
-                                                            _raw_stream(stream, dev))), "lowbit_kv8_attention")
+    _check(_call(_ATTENTION, cache._at, *batch, qp, qs, heads, float(scale), op, os_, ws, ws_bytes,
+                 _raw_stream(stream, dev)), "lowbit_kv8_attention")

@@ -1,6 +1,7 @@
 """Refusals and host-side parts of the decode-side entry points (adapters, rotary positions, KV8 cache).  CPU only:
 every case fails validation, is an empty no-op, or runs on the host."""
 import ctypes
+import functools
 import math
 
 import pytest
@@ -121,12 +122,16 @@ def kv8(lb, cache=(), batch=()):
 
 def test_argument_blocks(lb):
     """A block carries every parameter to its place: each one's refusal comes back through it as it does from the call."""
+    torch = pytest.importorskip("torch")
+    from decode_packed_bit_b200 import _marshal as m
     L = lb.lib()
     at = 0x10000
 
+    def call(name, *words):
+        return m.call(ctypes.cast(getattr(L, f"lowbit_{name}_args"), ctypes.c_void_p).value, *words)
+
     def lora(x=at, ids=at, ranks=0, scales=0, R=1, M=4, N=64, K=128, rank=16, adapters=2, ws=at, n=BIG, a=at, b=at, base=at, y=at):
-        return L.lowbit_lora_add_group_args(lb._LORA_BLOCKS.setdefault(1, lb.struct.Struct("=17q").pack)(
-            x, ids, ranks, scales, R, M, N, K, rank, adapters, ws, n, 0, a, b, base, y))
+        return call("lora_add_group", x, ids, ranks, scales, R, M, N, K, rank, adapters, ws, n, 0, a, b, base, y)
 
     for name in ("x", "ids", "a", "b", "base", "y"):
         assert lora(**{name: 0}) == 1 and lora(**{name: at + 8}) == 2, name
@@ -139,7 +144,7 @@ def test_argument_blocks(lb):
                 M=2, D=128, rot=64, inter=0, mag=1.0, stream=0)
 
     def rope(**kw):
-        return L.lowbit_rope_args(lb._ROPE_BLOCK(*[{**base, **kw}[n] for n in names]))
+        return call("rope", *[{**base, **kw}[n] for n in names])
 
     for name in ("q", "qo", "k", "ko", "pos", "ph"):
         assert rope(**{name: 0}) == 1 and rope(**{name: at + 8}) == 2, name
@@ -150,27 +155,49 @@ def test_argument_blocks(lb):
 
     c, b = kv8(lb)
     cache, batch = ctypes.addressof(c), [at, at, at, 2, 4, 3]
-    append, read, attend = L.lowbit_kv8_append_args, L.lowbit_kv8_read_args, L.lowbit_kv8_attention_args
+    append, read, attend = (functools.partial(call, n) for n in ("kv8_append", "kv8_read", "kv8_attention"))
     good = [at, 128, 0, at, 128, 0, 0]
     for i, bad in ((0, at + 8), (1, 132), (3, at + 8), (4, 132)):
-        assert append(lb._APPEND_BLOCK(cache, *batch, *good[:i], bad, *good[i + 1:])) == 2
+        assert append(cache, *batch, *good[:i], bad, *good[i + 1:]) == 2
     for i, bad in ((2, 2), (5, 2)):
-        assert append(lb._APPEND_BLOCK(cache, *batch, *good[:i], bad, *good[i + 1:])) == 1
-    assert read(lb._READ_BLOCK(cache, *batch, at + 8, 0, 0, 0)) == 2 and read(lb._READ_BLOCK(cache, *batch, 0, at + 8, 0, 0)) == 2
-    assert read(lb._READ_BLOCK(cache, *batch, at, 0, 5, 0)) == 1
+        assert append(cache, *batch, *good[:i], bad, *good[i + 1:]) == 1
+    assert read(cache, *batch, at + 8, 0, 0, 0) == 2 and read(cache, *batch, 0, at + 8, 0, 0) == 2
+    assert read(cache, *batch, at, 0, 5, 0) == 1
     good = [at, 256, 4, 0.1, at, 256, at, BIG, 0]
     for i, bad, status in ((0, at + 8, 2), (1, 260, 2), (2, 3, 1), (3, float("nan"), 1), (4, at + 8, 2), (5, 260, 2), (6, at + 8, 2),
                            (7, 16, 1)):
-        assert attend(lb._ATTENTION_BLOCK(cache, *batch, *good[:i], bad, *good[i + 1:])) == status, i
+        assert attend(cache, *batch, *good[:i], bad, *good[i + 1:]) == status, i
     for i, bad, status in ((0, 0, 1), (1, at + 4, 2), (2, at + 4, 2), (3, -1, 1), (4, 0, 1), (5, -1, 1)):
         broken = batch[:i] + [bad] + batch[i + 1:]
-        assert append(lb._APPEND_BLOCK(cache, *broken, at, 128, 0, at, 128, 0, 0)) == status
-        assert read(lb._READ_BLOCK(cache, *broken, at, at, 0, 0)) == status
-        assert attend(lb._ATTENTION_BLOCK(cache, *broken, *good)) == status
+        assert append(cache, *broken, at, 128, 0, at, 128, 0, 0) == status
+        assert read(cache, *broken, at, at, 0, 0) == status
+        assert attend(cache, *broken, *good) == status
     for f, n in ((append, 14), (read, 11), (attend, 16)):
-        assert f(lb.struct.pack(f"={n}q", 0, *batch, *[0] * (n - 7))) == 1
-        assert f(None) == 1
-    assert L.lowbit_lora_add_group_args(None) == 1 and L.lowbit_rope_args(None) == 1
+        assert f(None, *batch, *[0] * (n - 7)) == 1
+    for name in ("lora_add_group", "rope", "kv8_append", "kv8_read", "kv8_attention"):
+        assert getattr(L, f"lowbit_{name}_args")(None) == 1
+    # the module's own refusals
+    with pytest.raises(TypeError):
+        m.call(1, *[0] * 200)
+    with pytest.raises(TypeError):
+        m.call()
+    with pytest.raises(TypeError):
+        m.call(1, "x")
+    with pytest.raises(OverflowError):
+        m.call(1, 1 << 63)
+    t = torch.zeros((2, 3, 8))
+    for f in (m.dense, m.rows):
+        with pytest.raises(ValueError, match="x: expected .* on cuda:0, got torch.float32"):
+            f(t, torch.float32, (2, 3, 8), "x", 0)  # not on a GPU
+        with pytest.raises(TypeError):
+            f(None, torch.float32, (2, 3, 8), "x", 0)
+        with pytest.raises(TypeError):
+            f(t, torch.float32, [2, 3, 8], "x", 0)
+        with pytest.raises(TypeError):
+            f(t, torch.float32, (2, 3, 8), "x")
+    with pytest.raises(ValueError):
+        m.scratch(t, 0)
+    assert m.scratch(None, 0) == (0, 0)
 
 
 def test_sizes_whose_indices_would_wrap(lb):
