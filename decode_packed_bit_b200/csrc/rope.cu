@@ -95,6 +95,13 @@ __device__ __forceinline__ void rope_turns(const RopeArgs &a, int64_t m, float2 
     }
 }
 
+__device__ __forceinline__ void rope_turn(float &a, float &b, float c, float s)
+{
+    const float r = a * c - b * s;
+    b = b * c + a * s;
+    a = r;
+}
+
 // A piece's head: source and destination.
 template <typename TI, typename TO>
 __device__ __forceinline__ void rope_head(const RopeArgs &a, int64_t m, int h, const TI *&src, TO *&dst)
@@ -107,12 +114,14 @@ __device__ __forceinline__ void rope_head(const RopeArgs &a, int64_t m, int h, c
 
 // rot is a multiple of 16 (half layout) or 8 (interleaved): 16-byte pieces of
 // pairs.  A thread's first pieces are under way before the sines are computed
-// (loaded after them, 8191 rows took 43 us in place of 38).
+// (loaded after them, 8191 rows of 40 heads took 43 us in place of 38); 48
+// registers, five CTAs an SM, and three pieces (31.5 us, 5.3 TB/s) do better than
+// 64, four CTAs and four (36.3), or 40, six CTAs and two (32.1).
 template <typename TI, typename TO, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, 5) k_rope(const RopeArgs a)
 {
-    constexpr int U = INTER ? 4 : 2;
-    __shared__ float2 turn[kRopeMaxDim / 2];  // {cos, sin} * magnitude
+    constexpr int U = (INTER ? 2 : 1) + (sizeof(TI) == 2 ? 1 : 0);  // pieces under way
+    __shared__ __align__(16) float2 turn[kRopeMaxDim / 2];  // {cos, sin} * magnitude
     pdl_launch_dependents();
     pdl_wait_primary();
     const int64_t m = blockIdx.x;
@@ -123,6 +132,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a)
     const int turned = INTER ? a.rot / 8 : a.rot / 16, rest = a.D - a.rot;
     const unsigned pieces = turned + (INTER ? rest / 8 : (rest + 8) / 16), total = nh * pieces;
     bool first = true;
+    // piece and head of this thread's next piece, advanced without divisions
+    unsigned head = threadIdx.x / pieces, c = threadIdx.x % pieces;
+    const unsigned dh = kRopeThreads / pieces, dc = kRopeThreads % pieces;
     for (unsigned base = threadIdx.x; first || base < total; base += U * kRopeThreads) {
         RopeRaw<TI> u[U], v[U];
         const TI *src[U];
@@ -134,15 +146,22 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a)
             const unsigned i = base + k * kRopeThreads;
             pair[k] = -2;
             if (i >= total) continue;
-            const int c = i % pieces;
-            rope_head(a, m, h0 + (int)(i / pieces), src[k], dst[k]);
-            pair[k] = c < turned ? c * (INTER ? 4 : 8) : -1;
+            rope_head(a, m, h0 + (int)head, src[k], dst[k]);
+            const int p = (int)c;
+            const bool turn_it = p < turned;
+            pair[k] = turn_it ? p * (INTER ? 4 : 8) : -1;
             if (INTER) {
-                at[k][0] = c < turned ? c * 8 : a.rot + (c - turned) * 8;
+                at[k][0] = p * 8;  // rot is 8 turned ones
                 at[k][1] = -1;
             } else {
-                at[k][0] = c < turned ? c * 8 : a.rot + (c - turned) * 16;
-                at[k][1] = c < turned ? half + c * 8 : at[k][0] + 8 < a.D ? at[k][0] + 8 : -1;
+                at[k][0] = turn_it ? p * 8 : a.rot + (p - turned) * 16;
+                at[k][1] = turn_it ? half + p * 8 : at[k][0] + 8 < a.D ? at[k][0] + 8 : -1;
+            }
+            head += dh;
+            c += dc;
+            if (c >= pieces) {
+                c -= pieces;
+                ++head;
             }
             u[k].load(src[k] + at[k][0]);
             if (!INTER && at[k][1] >= 0) v[k].load(src[k] + at[k][1]);
@@ -160,21 +179,19 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a)
             if (INTER) {
                 if (pair[k] >= 0)
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        const float2 w = turn[pair[k] + p];
-                        const float r = x[2 * p] * w.x - x[2 * p + 1] * w.y;
-                        x[2 * p + 1] = x[2 * p + 1] * w.x + x[2 * p] * w.y;
-                        x[2 * p] = r;
+                    for (int p = 0; p < 4; p += 2) {
+                        const float4 w = *reinterpret_cast<const float4 *>(turn + pair[k] + p);
+                        rope_turn(x[2 * p], x[2 * p + 1], w.x, w.y);
+                        rope_turn(x[2 * p + 2], x[2 * p + 3], w.z, w.w);
                     }
             } else if (at[k][1] >= 0) {
                 v[k].get(y);
                 if (pair[k] >= 0)
 #pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        const float2 w = turn[pair[k] + p];
-                        const float r = x[p] * w.x - y[p] * w.y;
-                        y[p] = y[p] * w.x + x[p] * w.y;
-                        x[p] = r;
+                    for (int p = 0; p < 8; p += 2) {
+                        const float4 w = *reinterpret_cast<const float4 *>(turn + pair[k] + p);
+                        rope_turn(x[p], y[p], w.x, w.y);
+                        rope_turn(x[p + 1], y[p + 1], w.z, w.w);
                     }
                 rope_store8(dst[k] + at[k][1], y);
             }
