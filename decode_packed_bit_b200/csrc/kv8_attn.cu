@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sh_sum[W], sh_units[W];
     __shared__ int64_t sh_off;
-    __shared__ int sh_b, sh_last;
+    __shared__ int sh_b, sh_first[2], sh_n[2];
     // a warp's parts of cut units: the head is 2 warp, the tail 2 warp + 1
     __shared__ AttnPart parts[2 * W];
     __shared__ int order[2 * W], listed;
@@ -622,94 +622,163 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         return ri < u.n ? a.out + (int64_t)(u.r0 + ri) * a.out_stride + (int64_t)(u.h * a.G + r % a.G) * D + d4 * 4 : nullptr;
     };
     const int parts_n = listed;
+    // First what each part counts for: a warp has a row, a lane a part, so that a
+    // unit's maximum and sum are scans over its lanes (thread by thread, part
+    // after part, the join took 3 us of a short call's 11).
+    float *tops = reinterpret_cast<float *>(smem + S::kQ);  // q's fragments are done with
+    for (int row = warp; row < ROWS; row += W) {
+        const int ord = lane < parts_n ? order[lane] : 64, at = (ord & 63) * ROWS + row;
+        const unsigned begins = __ballot_sync(0xffffffffu, (ord & 64) != 0), upto = (2u << lane) - 1;
+        const int first = 31 - __clz(begins & upto), last = (begins & ~upto ? __ffs(begins & ~upto) - 1 : 32) - 1;
+        float m = -INFINITY, l = 0.f;
+        if (lane < parts_n) {
+            m = stat_m[at];
+            l = stat_l[at];
+        }
+        float top = m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, top, o);
+            if (lane - o >= first) top = fmaxf(top, x);
+        }
+        top = __shfl_sync(0xffffffffu, top, last);
+        const float f = at_exp2(m - at_ref(top));
+        l *= f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, l, o);
+            if (lane - o >= first) l += x;
+        }
+        l = __shfl_sync(0xffffffffu, l, last);
+        if (lane < parts_n) {
+            stat_m[at] = f;
+            stat_l[at] = l;
+            tops[at] = top;
+        }
+    }
+    __syncthreads();
     for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
         const int row = x / (D / 4), d4 = x % (D / 4);
-        float top = -INFINITY, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < parts_n; ++k) {
-            const int p = order[k] & 63;
-            const float m = stat_m[p * ROWS + row], l = stat_l[p * ROWS + row];
-            const float4 v = *reinterpret_cast<const float4 *>(
-                reinterpret_cast<const float *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart) +
-                row * S::kPitch + d4 * 4);
-            if (order[k] & 64) {
-                top = m;
-                sum = l;
-                o = v;
-            } else {
-                const float now = fmaxf(top, m), ref = at_ref(now), f0 = at_exp2(top - ref), f1 = at_exp2(m - ref);
-                top = now;
-                sum = sum * f0 + l * f1;
-                o.x = o.x * f0 + v.x * f1; o.y = o.y * f0 + v.y * f1; o.z = o.z * f0 + v.z * f1; o.w = o.w * f0 + v.w * f1;
-            }
-            if (order[k] & 128) {
-                const AttnPart &u = parts[p];
-                if (u.start >= w0 && u.start + u.tiles <= w1) {
-                    if (uint16_t *op = out_at(u, row, d4)) at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
-                } else {
-                    // the CTA's part: 0 of a unit that started before its range, else 1
-                    const int64_t pr = (2 * (int64_t)blockIdx.x + (u.start >= w0 ? 1 : 0)) * ROWS + row;
-                    reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
-                    if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(top, sum);
+        constexpr int kBatch = 4;
+        for (int k = 0; k < parts_n; k += kBatch) {
+            int ord[kBatch];
+            float f[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+                if (k + q < parts_n) {
+                    ord[q] = order[k + q];
+                    const int p = ord[q] & 63;
+                    f[q] = stat_m[p * ROWS + row];
+                    v[q] = *reinterpret_cast<const float4 *>(
+                        reinterpret_cast<const float *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart) +
+                        row * S::kPitch + d4 * 4);
                 }
-            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q)
+                if (k + q < parts_n) {
+                    if (ord[q] & 64) o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    o.x += v[q].x * f[q]; o.y += v[q].y * f[q]; o.z += v[q].z * f[q]; o.w += v[q].w * f[q];
+                    if (ord[q] & 128) {
+                        const int p = ord[q] & 63;
+                        const AttnPart &u = parts[p];
+                        const float sum = stat_l[p * ROWS + row];
+                        if (u.start >= w0 && u.start + u.tiles <= w1) {
+                            if (uint16_t *op = out_at(u, row, d4)) at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
+                        } else {
+                            // the CTA's part: 0 of a unit that started before its range, else 1
+                            const int64_t pr = (2 * (int64_t)blockIdx.x + (u.start >= w0 ? 1 : 0)) * ROWS + row;
+                            reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
+                            if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(tops[p * ROWS + row], sum);
+                        }
+                    }
+                }
         }
     }
     // ---- join the parts of units cut between CTAs: the first and the last unit ----
-    for (int k = 0; k < 2 && parts_n > 0; ++k) {
-        const AttnPart u = parts[order[k == 0 ? 0 : parts_n - 1] & 63];
-        if (k == 1 && u.start == parts[order[0] & 63].start) break;
-        if (u.start >= w0 && u.start + u.tiles <= w1) continue;
-        // the CTAs that share the unit: its first tile's to its last's
-        const int c0 = (int)(((u.start + 1) * C - 1) / total), c1 = (int)(((u.start + u.tiles) * C - 1) / total);
-        __syncthreads();  // the CTA's part is written; the counter's release carries it
-        if (tid == 0) {
-            unsigned seen;
-            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.counters + c0) : "memory");
-            sh_last = seen == (unsigned)(c1 - c0);
-            if (sh_last) a.counters[c0] = 0;
+    __syncthreads();  // the CTA's parts are written; the counters' release carries them
+    if (warp < 2 && lane == 0) {
+        int n = 0, c0 = 0;
+        if (parts_n > 0) {
+            const AttnPart &u = parts[order[warp == 0 ? 0 : parts_n - 1] & 63];
+            const bool again = warp == 1 && u.start == parts[order[0] & 63].start;
+            if (!again && !(u.start >= w0 && u.start + u.tiles <= w1)) {
+                // the CTAs that share the unit: its first tile's to its last's
+                c0 = (int)(((u.start + 1) * C - 1) / total);
+                const int c1 = (int)(((u.start + u.tiles) * C - 1) / total);
+                unsigned seen;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(seen) : "l"(a.counters + c0) : "memory");
+                if (seen == (unsigned)(c1 - c0)) {
+                    a.counters[c0] = 0;
+                    n = c1 - c0 + 1;
+                }
+            }
+        }
+        sh_first[warp] = c0;
+        sh_n[warp] = n;
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        const int n = sh_n[k], c0 = sh_first[k];
+        if (n == 0) continue;
+        const AttnPart &u = parts[order[k == 0 ? 0 : parts_n - 1] & 63];
+        // parts in CTA order; the first CTA's holds the unit's start
+        auto part = [&](int c, int row) { return (2 * (int64_t)(c0 + c) + (c == 0 ? 1 : 0)) * ROWS + row; };
+        const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
+        float *fac = reinterpret_cast<float *>(smem), *inv = fac + ROWS * n;  // over the ring
+        __syncthreads();
+        for (int row = warp; row < ROWS; row += W) {
+            const float2 s = lane < n ? __ldcg(ml + part(lane, row)) : make_float2(-INFINITY, 0.f);
+            float top = s.x;
+            for (int c = lane + 32; c < n; c += 32) top = fmaxf(top, __ldcg(ml + part(c, row)).x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float ref = at_ref(top), f = at_exp2(s.x - ref);
+            float sum = s.y * f;
+            if (lane < n) fac[row * n + lane] = f;
+            for (int c = lane + 32; c < n; c += 32) {
+                const float2 x = __ldcg(ml + part(c, row));
+                const float g = at_exp2(x.x - ref);
+                fac[row * n + c] = g;
+                sum += x.y * g;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0) inv[row] = sum == 0.f ? 0.f : 1.f / sum;
         }
         __syncthreads();
-        if (!sh_last) continue;
-        // parts in CTA order; the first CTA's holds the unit's start.  A batch's
-        // loads are all under way before the first is used.
-        const int n = c1 - c0 + 1;
-        constexpr int kBatch = 20;
-        const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
-        for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
-            const int row = x / (D / 4), d4 = x % (D / 4);
-            uint16_t *op = out_at(u, row, d4);
-            if (!op) continue;
-            float top = -INFINITY, sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < n; c += kBatch) {
-                float2 s[kBatch];
-                float4 v[kBatch];
+        // a batch's loads are all under way before the first is used
+        constexpr int kItems = ROWS * (D / 4), NI = (kItems + S::kThreads - 1) / S::kThreads, kBatch = 20 / NI;
+        float4 o[NI];
 #pragma unroll
-                for (int q = 0; q < kBatch; ++q)
-                    if (c + q < n) {
-                        const int64_t pr = (2 * (int64_t)(c0 + c + q) + (c + q == 0 ? 1 : 0)) * ROWS + row;
-                        s[q] = __ldcg(ml + pr);
-                        v[q] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + pr * D) + d4);
+        for (int i = 0; i < NI; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < n; c += kBatch) {
+            float4 v[NI][kBatch];
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    const int x = tid + i * S::kThreads;
+                    if (x < kItems && c + q < n)
+                        v[i][q] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + part(c + q, x / (D / 4)) * D) + x % (D / 4));
+                }
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int q = 0; q < kBatch; ++q) {
+                    const int x = tid + i * S::kThreads;
+                    if (x < kItems && c + q < n) {
+                        const float f = fac[x / (D / 4) * n + c + q];
+                        o[i].x += v[i][q].x * f; o[i].y += v[i][q].y * f; o[i].z += v[i][q].z * f; o[i].w += v[i][q].w * f;
                     }
-                float now = top;
+                }
+        }
 #pragma unroll
-                for (int q = 0; q < kBatch; ++q)
-                    if (c + q < n) now = fmaxf(now, s[q].x);
-                const float ref = at_ref(now), f0 = at_exp2(top - ref);
-                sum *= f0;
-                o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
-                top = now;
-#pragma unroll
-                for (int q = 0; q < kBatch; ++q)
-                    if (c + q < n) {
-                        const float f = at_exp2(s[q].x - ref);
-                        sum += s[q].y * f;
-                        o.x += v[q].x * f; o.y += v[q].y * f; o.z += v[q].z * f; o.w += v[q].w * f;
-                    }
-            }
-            at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
+        for (int i = 0; i < NI; ++i) {
+            const int x = tid + i * S::kThreads;
+            if (x < kItems)
+                if (uint16_t *op = out_at(u, x / (D / 4), x % (D / 4))) at_store4(op, o[i], inv[x / (D / 4)]);
         }
     }
 }
