@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     __shared__ int sh_b, sh_first[2], sh_n[2];
     // a warp's parts of cut units: the head is 2 warp, the tail 2 warp + 1
     __shared__ AttnPart parts[2 * W];
-    __shared__ int order[2 * W], listed;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -603,40 +602,25 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     __syncthreads();
 
     // ---- join the parts of units cut between warps ----
-    // The parts there are, in order; a unit's begin with the tail of the warp it
-    // starts in (or with the head of the CTA's first).
-    if (warp == 0) {
-        const bool there = lane < 2 * W && parts[min(lane, 2 * W - 1)].there;
-        const unsigned all = __ballot_sync(0xffffffffu, there);
-        const unsigned begins = __ballot_sync(0xffffffffu, there && ((lane & 1) || lane == 0));
-        if (there) {
-            const unsigned later = all & ~((2u << lane) - 1);
-            const bool ends = !later || (begins >> (__ffs(later) - 1) & 1);
-            order[__popc(all & ((1u << lane) - 1))] = lane | (begins >> lane & 1 ? 64 : 0) | (ends ? 128 : 0);
-        }
-        if (lane == 0) listed = __popc(all);
-    }
-    __syncthreads();
+    // Lane p is part p; a unit's begin with the tail of the warp it starts in (or
+    // with the head of the CTA's first).
+    const bool there = lane < 2 * W && parts[min(lane, 2 * W - 1)].there;
+    const unsigned all = __ballot_sync(0xffffffffu, there);
+    const unsigned begins = __ballot_sync(0xffffffffu, there && ((lane & 1) || lane == 0)), upto = (2u << lane) - 1;
+    const unsigned ends = __ballot_sync(0xffffffffu, there && (!(all & ~upto) || (begins >> (__ffs(all & ~upto) - 1) & 1)));
     auto out_at = [&](const AttnPart &u, int row, int d4) -> uint16_t * {  // null past the sequence's rows
         const int r = u.row0 + row, ri = r / a.G;
         return ri < u.n ? a.out + (int64_t)(u.r0 + ri) * a.out_stride + (int64_t)(u.h * a.G + r % a.G) * D + d4 * 4 : nullptr;
     };
-    const int parts_n = listed;
-    // First what each part counts for: a warp has a row, a lane a part, so that a
-    // unit's maximum and sum are scans over its lanes (thread by thread, part
-    // after part, the join took 3 us of a short call's 11).
+    // First what each part counts for: a warp has a row, so that a unit's maximum and
+    // sum are scans over its lanes.  (Loops that are not unrolled: this code runs
+    // once, and fetching it is most of its time.)
     float *tops = reinterpret_cast<float *>(smem + S::kQ);  // q's fragments are done with
     for (int row = warp; row < ROWS; row += W) {
-        const int ord = lane < parts_n ? order[lane] : 64, at = (ord & 63) * ROWS + row;
-        const unsigned begins = __ballot_sync(0xffffffffu, (ord & 64) != 0), upto = (2u << lane) - 1;
-        const int first = 31 - __clz(begins & upto), last = (begins & ~upto ? __ffs(begins & ~upto) - 1 : 32) - 1;
-        float m = -INFINITY, l = 0.f;
-        if (lane < parts_n) {
-            m = stat_m[at];
-            l = stat_l[at];
-        }
-        float top = m;
-#pragma unroll
+        const int first = 31 - __clz(begins & upto), at = lane * ROWS + row;
+        const int last = ends & ~(upto >> 1) ? __ffs(ends & ~(upto >> 1)) - 1 : 31;
+        float m = there ? stat_m[at] : -INFINITY, l = there ? stat_l[at] : 0.f, top = m;
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const float x = __shfl_up_sync(0xffffffffu, top, o);
             if (lane - o >= first) top = fmaxf(top, x);
@@ -644,65 +628,67 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
         top = __shfl_sync(0xffffffffu, top, last);
         const float f = at_exp2(m - at_ref(top));
         l *= f;
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const float x = __shfl_up_sync(0xffffffffu, l, o);
             if (lane - o >= first) l += x;
         }
         l = __shfl_sync(0xffffffffu, l, last);
-        if (lane < parts_n) {
+        if (there) {
             stat_m[at] = f;
             stat_l[at] = l;
             tops[at] = top;
         }
     }
     __syncthreads();
+#pragma unroll 1
     for (int x = tid; x < ROWS * (D / 4); x += S::kThreads) {
         const int row = x / (D / 4), d4 = x % (D / 4);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int kBatch = 4;
-        for (int k = 0; k < parts_n; k += kBatch) {
-            int ord[kBatch];
+#pragma unroll 1
+        for (unsigned todo = all; todo;) {
+            int p[kBatch];
             float f[kBatch];
             float4 v[kBatch];
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-                if (k + q < parts_n) {
-                    ord[q] = order[k + q];
-                    const int p = ord[q] & 63;
-                    f[q] = stat_m[p * ROWS + row];
+            for (int q = 0; q < kBatch; ++q) {
+                p[q] = __ffs(todo) - 1;
+                todo &= todo - 1;
+                if (p[q] >= 0) {
+                    f[q] = stat_m[p[q] * ROWS + row];
                     v[q] = *reinterpret_cast<const float4 *>(
-                        reinterpret_cast<const float *>(p & 1 ? smem + (p >> 1) * NH * S::kHalf : smem + S::kHead + (p >> 1) * S::kPart) +
+                        reinterpret_cast<const float *>(p[q] & 1 ? smem + (p[q] >> 1) * NH * S::kHalf : smem + S::kHead + (p[q] >> 1) * S::kPart) +
                         row * S::kPitch + d4 * 4);
                 }
+            }
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q)
-                if (k + q < parts_n) {
-                    if (ord[q] & 64) o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    o.x += v[q].x * f[q]; o.y += v[q].y * f[q]; o.z += v[q].z * f[q]; o.w += v[q].w * f[q];
-                    if (ord[q] & 128) {
-                        const int p = ord[q] & 63;
-                        const AttnPart &u = parts[p];
-                        const float sum = stat_l[p * ROWS + row];
-                        if (u.start >= w0 && u.start + u.tiles <= w1) {
-                            if (uint16_t *op = out_at(u, row, d4)) at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
-                        } else {
-                            // the CTA's part: 0 of a unit that started before its range, else 1
-                            const int64_t pr = (2 * (int64_t)blockIdx.x + (u.start >= w0 ? 1 : 0)) * ROWS + row;
-                            reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
-                            if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(tops[p * ROWS + row], sum);
-                        }
+            for (int q = 0; q < kBatch; ++q) {
+                if (p[q] < 0) break;
+                if (begins >> p[q] & 1) o = make_float4(0.f, 0.f, 0.f, 0.f);
+                o.x += v[q].x * f[q]; o.y += v[q].y * f[q]; o.z += v[q].z * f[q]; o.w += v[q].w * f[q];
+                if (ends >> p[q] & 1) {
+                    const AttnPart &u = parts[p[q]];
+                    const float sum = stat_l[p[q] * ROWS + row];
+                    if (u.start >= w0 && u.start + u.tiles <= w1) {
+                        if (uint16_t *op = out_at(u, row, d4)) at_store4(op, o, sum == 0.f ? 0.f : 1.f / sum);
+                    } else {
+                        // the CTA's part: 0 of a unit that started before its range, else 1
+                        const int64_t pr = (2 * (int64_t)blockIdx.x + (u.start >= w0 ? 1 : 0)) * ROWS + row;
+                        reinterpret_cast<float4 *>(a.part_o + pr * D)[d4] = o;
+                        if (d4 == 0) reinterpret_cast<float2 *>(a.part_ml)[pr] = make_float2(tops[p[q] * ROWS + row], sum);
                     }
                 }
+            }
         }
     }
     // ---- join the parts of units cut between CTAs: the first and the last unit ----
     __syncthreads();  // the CTA's parts are written; the counters' release carries them
     if (warp < 2 && lane == 0) {
         int n = 0, c0 = 0;
-        if (parts_n > 0) {
-            const AttnPart &u = parts[order[warp == 0 ? 0 : parts_n - 1] & 63];
-            const bool again = warp == 1 && u.start == parts[order[0] & 63].start;
+        if (all) {
+            const AttnPart &u = parts[warp == 0 ? __ffs(all) - 1 : 31 - __clz(all)];
+            const bool again = warp == 1 && u.start == parts[__ffs(all) - 1].start;
             if (!again && !(u.start >= w0 && u.start + u.tiles <= w1)) {
                 // the CTAs that share the unit: its first tile's to its last's
                 c0 = (int)(((u.start + 1) * C - 1) / total);
@@ -722,7 +708,7 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
     for (int k = 0; k < 2; ++k) {
         const int n = sh_n[k], c0 = sh_first[k];
         if (n == 0) continue;
-        const AttnPart &u = parts[order[k == 0 ? 0 : parts_n - 1] & 63];
+        const AttnPart &u = parts[k == 0 ? __ffs(all) - 1 : 31 - __clz(all)];
         // parts in CTA order; the first CTA's holds the unit's start
         auto part = [&](int c, int row) { return (2 * (int64_t)(c0 + c) + (c == 0 ? 1 : 0)) * ROWS + row; };
         const float2 *ml = reinterpret_cast<const float2 *>(a.part_ml);
