@@ -16,12 +16,14 @@
 // it waits for t.  Only rows of the adapter at hand are stored,
 // so what another adapter holds (infinities among it) cannot reach them.
 //
-// Which rows a CTA takes: up to kLoraFewRows rows (decode), all rows of one
-// adapter, gathered, so that each adapter's weights are read once; beyond that
+// Which rows a CTA takes: up to kLoraFewRows rows (decode), 16 rows of one
+// adapter, gathered, so that an adapter's weights are read once for them; beyond that
 // (prompts, where neighbours share an adapter) blocks of 16 or 32 rows in the
 // caller's order, with a pass for each adapter in the block.  Nothing is sorted.
 // Bound by the adapters' bytes for decode, by base and y (8 bytes an output)
-// for prompts.
+// for prompts.  Measured: 61 rows of two 5120 -> 17408 projections, ranks up to 64,
+// 47 us (first launch 17, second 30 at 4.9 TB/s); 4096 rows, 4096 -> 11008, rank 32,
+// 93.5 us (16 and 78, 4.6 TB/s); one row, 4096 -> 4096, rank 16, 5.5 us, latency.
 #include <algorithm>
 
 #include "common.cuh"
@@ -161,9 +163,10 @@ __device__ __forceinline__ int2 lora_range(const LoraArgs &a, int slice, int war
     return make_int2(k0, min(s1, k0 + sub));
 }
 
-// The rows of row m's adapter, in order, when m is the first of them: their
-// number, and rows[] filled; 0 for the others and for rows without an adapter.
-// Called by all threads of a CTA, M <= kLoraFewRows.
+// Up to 16 rows of row m's adapter, in order, when m is the first of its adapter,
+// or the 17th, 33rd ...: their number, and rows[] filled; 0 for the others and
+// for rows without an adapter.  Called by all threads of a CTA, M <=
+// kLoraFewRows; warp_n: a word per warp and one more.
 struct LoraRows {
     int id, n, rank;
 };
@@ -172,29 +175,33 @@ __device__ __forceinline__ LoraRows lora_gather(const LoraArgs &a, int m, int *r
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int mine = lora_id(a, tid), id = lora_id(a, m);
     const bool same = tid < a.M && mine == id && id >= 0;
-    const bool later = __syncthreads_or(same && tid < m);
-    const unsigned vote = __ballot_sync(0xffffffffu, same);
+    const unsigned vote = __ballot_sync(0xffffffffu, same), below = vote & ((1u << lane) - 1);
     if (lane == 0) warp_n[warp] = __popc(vote);
     __syncthreads();
-    int at = 0, n = 0;
+    int at = __popc(below), n = 0, to_m = 0;  // same rows before this thread's, in all, in the warps before m's
 #pragma unroll
     for (int w = 0; w < kLoraWarps; ++w) {
-        if (w < warp) at += warp_n[w];
-        n += warp_n[w];
+        const int x = warp_n[w];
+        if (w < warp) at += x;
+        if (w < m >> 5) to_m += x;
+        n += x;
     }
-    if (same) rows[at + __popc(vote & ((1u << lane) - 1))] = tid;
+    if (tid == m) warp_n[kLoraWarps] = at - to_m;
     __syncthreads();
-    return LoraRows{id, later ? 0 : n, lora_rank(a, id)};
+    const int from = to_m + warp_n[kLoraWarps];
+    if (same && at >= from && at < from + 16) rows[at - from] = tid;
+    __syncthreads();
+    return LoraRows{id, from % 16 ? 0 : min(16, n - from), lora_rank(a, id)};
 }
 
-// Few rows: grid (rows x slices, projections); the CTA of an adapter's first
-// row takes all its rows, the others leave.
+// Few rows: grid (rows x slices, projections); the CTA of an adapter's first row
+// takes 16 of its rows, that of the 17th the next, the others leave.
 template <int NT>
-__global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_few(const LoraArgs a)
+__global__ void __launch_bounds__(kLoraThreads, NT == 8 ? 2 : 1) k_lora_shrink_few(const LoraArgs a)
 {
     using S = LoraShrink<NT, 1>;
     extern __shared__ __align__(16) float red[];
-    __shared__ int rows[kLoraFewRows], warp_n[kLoraWarps];
+    __shared__ int rows[16], warp_n[kLoraWarps + 1];
     pdl_wait_primary();
     pdl_launch_dependents();  // after the wait: the next launch may read whatever came before this one
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -205,18 +212,15 @@ __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink_few(const LoraArgs
     const uint16_t *w = a.a[target] + ((int64_t)own.id * a.rank + g) * a.K + t * 8;
     float *tp = a.t + ((int64_t)target * a.slices + slice) * a.M * a.rank;
     const int half = a.rank / 2;
-    for (int r0 = 0; r0 < own.n; r0 += 16) {
-        const uint16_t *xp[1][2];
+    const uint16_t *xp[1][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            xp[0][h] = r0 + h * 8 + g < own.n ? a.x + (int64_t)rows[r0 + h * 8 + g] * a.K + t * 8 : nullptr;
-        lora_dot<NT, 1>(red + (warp * 16 + g) * S::kLd + 2 * t, xp, w, own.rank, a.K, k.x, k.y, g);
-        __syncthreads();
-        for (int e = threadIdx.x; e < min(16, own.n - r0) * half; e += kLoraThreads) {
-            const int row = e / half, r = e % half * 2;
-            *reinterpret_cast<float2 *>(tp + (int64_t)rows[r0 + row] * a.rank + r) = lora_warps_sum<NT, 1>(red, row, r);
-        }
-        __syncthreads();
+    for (int h = 0; h < 2; ++h)
+        xp[0][h] = h * 8 + g < own.n ? a.x + (int64_t)rows[h * 8 + g] * a.K + t * 8 : nullptr;
+    lora_dot<NT, 1>(red + (warp * 16 + g) * S::kLd + 2 * t, xp, w, own.rank, a.K, k.x, k.y, g);
+    __syncthreads();
+    for (int e = threadIdx.x; e < own.n * half; e += kLoraThreads) {
+        const int row = e / half, r = e % half * 2;
+        *reinterpret_cast<float2 *>(tp + (int64_t)rows[row] * a.rank + r) = lora_warps_sum<NT, 1>(red, row, r);
     }
 }
 
@@ -431,9 +435,9 @@ __device__ __forceinline__ void lora_acc(float4 &o, const float (&acc)[2][4], in
     o.x += acc[0][2 * h]; o.y += acc[0][2 * h + 1]; o.z += acc[1][2 * h]; o.w += acc[1][2 * h + 1];
 }
 
-// One adapter's rows over columns [c0, n_end).  SMALL: up to four rows, whose
+// One adapter's rows (16 at most) over columns [c0, n_end).  SMALL: up to four, whose
 // three numbers lie in one fragment (rows 0-3 the first, 4-7 the second, 8-11
-// the third), a third of the MMAs; else 16 rows at a time.
+// the third), a third of the MMAs.
 template <int KT, bool VEC, bool SMALL>
 __device__ __forceinline__ void lora_expand_rows(const LoraArgs &a, const LoraRows &own, const int *rows, uint4 *frag, unsigned ring,
                                                  int c0, int n_end)
@@ -446,104 +450,99 @@ __device__ __forceinline__ void lora_expand_rows(const LoraArgs &a, const LoraRo
     LoraPieces<KT, 1> pieces;
     pieces.set(own.rank, a.rank, lane);
     const uint16_t *b = a.b[target] + (int64_t)own.id * a.N * a.rank + lane * 8;
-    for (int r0 = 0; r0 < own.n; r0 += kRows) {
-        int64_t at[NH];  // offsets of this thread's rows, -1 for none
+    int64_t at[NH];  // offsets of this thread's rows, -1 for none
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
-            at[h] = g < kRows && r0 + h * 8 + g < own.n ? (int64_t)rows[r0 + h * 8 + g] * a.N : -1;
-        int n0 = c0 + warp * 16, ahead = n0, put = 0, get = 0;
-        auto issue = [&]() {
-            if (ahead < n_end) {
-                const unsigned st = ring + put * S::kStage;
-                if (VEC)
+    for (int h = 0; h < NH; ++h)
+        at[h] = g < kRows && h * 8 + g < own.n ? (int64_t)rows[h * 8 + g] * a.N : -1;
+    int n0 = c0 + warp * 16, ahead = n0, put = 0, get = 0;
+    auto issue = [&]() {
+        if (ahead < n_end) {
+            const unsigned st = ring + put * S::kStage;
+            if (VEC)
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {  // row h * 8 + g, columns 4 t ..
-                        if (at[h] >= 0 && ahead + 4 * t < a.N)
-                            lora_cp16(st + (h * 8 + g) * 64 + t * 16, base + at[h] + ahead + 4 * t);
-                    }
-                pieces.copy(st + S::kBase, b + (int64_t)ahead * a.rank, a.N - ahead);
-                ahead += kStep;
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            put = put + 1 == S::kStages ? 0 : put + 1;
-        };
+                for (int h = 0; h < NH; ++h) {  // row h * 8 + g, columns 4 t ..
+                    if (at[h] >= 0 && ahead + 4 * t < a.N)
+                        lora_cp16(st + (h * 8 + g) * 64 + t * 16, base + at[h] + ahead + 4 * t);
+                }
+            pieces.copy(st + S::kBase, b + (int64_t)ahead * a.rank, a.N - ahead);
+            ahead += kStep;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        put = put + 1 == S::kStages ? 0 : put + 1;
+    };
 #pragma unroll
-        for (int s = 0; s < S::kStages - 1; ++s) issue();
-        if (r0 == 0)
-            pdl_wait_primary();
+    for (int s = 0; s < S::kStages - 1; ++s) issue();
+    pdl_wait_primary();
+    for (int e = threadIdx.x; e < KT * 32; e += kLoraThreads) {
+        const int k = e / 32, eg = (e & 31) >> 2, et = e & 3;
+        uint32_t f[3][4];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int row = h * 8 + (SMALL ? eg & 3 : eg);
+            if (row < own.n) v = lora_t4(a, target, rows[row], own.id, own.rank, k * 16 + 4 * et);
+            lora_split(v, f, h);
+        }
+        if (SMALL)
+            frag[e] = eg < 4 ? make_uint4(f[0][0], f[2][0], f[0][2], f[2][2]) : make_uint4(f[1][0], 0, f[1][2], 0);
         else
-            __syncthreads();  // frag is free again
-        for (int e = threadIdx.x; e < KT * 32; e += kLoraThreads) {
-            const int k = e / 32, eg = (e & 31) >> 2, et = e & 3;
-            uint32_t f[3][4];
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int row = r0 + h * 8 + (SMALL ? eg & 3 : eg);
-                if (row < own.n) v = lora_t4(a, target, rows[row], own.id, own.rank, k * 16 + 4 * et);
-                lora_split(v, f, h);
-            }
-            if (SMALL)
-                frag[e] = eg < 4 ? make_uint4(f[0][0], f[2][0], f[0][2], f[2][2]) : make_uint4(f[1][0], 0, f[1][2], 0);
+            for (int s = 0; s < 3; ++s)
+                frag[(k * 3 + s) * 32 + (e & 31)] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+    }
+    __syncthreads();
+    uint32_t f[1][KT][NS][4];
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const uint4 u = frag[(k * NS + s) * 32 + lane];
+            f[0][k][s][0] = u.x; f[0][k][s][1] = u.y; f[0][k][s][2] = u.z; f[0][k][s][3] = u.w;
+        }
+    for (; n0 < n_end; n0 += kStep) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+        __syncwarp();
+        issue();  // into the stage read last
+        const unsigned st = ring + get * S::kStage;
+        get = get + 1 == S::kStages ? 0 : get + 1;
+        const int n = n0 + 4 * t;
+        float4 o[NH];
+        float acc[1][2][4];
+        lora_mul<KT, 1, NS>(f, st + S::kBase, own.rank, g, t, acc);
+        if (SMALL)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)  // rows g and g + 4, then g + 8
+                    acc[0][j][c] += __shfl_xor_sync(0xffffffffu, acc[0][j][c], 16) + acc[0][j][2 + c];
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+            if (VEC)
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(o[h].x), "=f"(o[h].y), "=f"(o[h].z), "=f"(o[h].w)
+                             : "r"(st + (h * 8 + g) * 64 + t * 16));
             else
-#pragma unroll
-                for (int s = 0; s < 3; ++s)
-                    frag[(k * 3 + s) * 32 + (e & 31)] = make_uint4(f[s][0], f[s][1], f[s][2], f[s][3]);
+                o[h] = lora_load4(base + (at[h] < 0 ? 0 : at[h]) + n, at[h] < 0 ? 0 : a.N - n);
         }
-        __syncthreads();
-        uint32_t f[1][KT][NS][4];
 #pragma unroll
-        for (int k = 0; k < KT; ++k)
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const uint4 u = frag[(k * NS + s) * 32 + lane];
-                f[0][k][s][0] = u.x; f[0][k][s][1] = u.y; f[0][k][s][2] = u.z; f[0][k][s][3] = u.w;
-            }
-        for (; n0 < n_end; n0 += kStep) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
-            __syncwarp();
-            issue();  // into the stage read last
-            const unsigned st = ring + get * S::kStage;
-            get = get + 1 == S::kStages ? 0 : get + 1;
-            const int n = n0 + 4 * t;
-            float4 o[NH];
-            float acc[1][2][4];
-            lora_mul<KT, 1, NS>(f, st + S::kBase, own.rank, g, t, acc);
-            if (SMALL)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)  // rows g and g + 4, then g + 8
-                        acc[0][j][c] += __shfl_xor_sync(0xffffffffu, acc[0][j][c], 16) + acc[0][j][2 + c];
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                if (VEC)
-                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                 : "=f"(o[h].x), "=f"(o[h].y), "=f"(o[h].z), "=f"(o[h].w)
-                                 : "r"(st + (h * 8 + g) * 64 + t * 16));
-                else
-                    o[h] = lora_load4(base + (at[h] < 0 ? 0 : at[h]) + n, at[h] < 0 ? 0 : a.N - n);
-            }
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                lora_acc(o[h], acc[0], h);
-                if (at[h] >= 0) lora_store4<VEC>(y + at[h] + n, a.N - n, o[h]);
-            }
-            __syncwarp();  // every lane has read the stage
+        for (int h = 0; h < NH; ++h) {
+            lora_acc(o[h], acc[0], h);
+            if (at[h] >= 0) lora_store4<VEC>(y + at[h] + n, a.N - n, o[h]);
         }
+        __syncwarp();  // every lane has read the stage
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // Few rows: grid (rows, column ranges, projections); the CTA of an adapter's
-// first row takes all its rows; a row without an adapter is copied.
+// first (17th, ...) row takes 16 of its rows; a row without an adapter is copied.
 // KT: rank / 16, rounded up to 1, 2, 4 or 8; VEC: rows of y are 16-byte aligned.
 template <int KT, bool VEC>
 __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_expand_few(const LoraArgs a)
 {
     using S = LoraRing<KT, 1>;
     extern __shared__ __align__(128) uint8_t ring_mem[];
-    __shared__ int rows[kLoraFewRows], warp_n[kLoraWarps];
+    __shared__ int rows[16], warp_n[kLoraWarps + 1];
     __shared__ uint4 frag[KT * 3 * 32];
     const unsigned ring = (unsigned)__cvta_generic_to_shared(ring_mem) + (threadIdx.x >> 5) * S::kStages * S::kStage;
     pdl_launch_dependents();
@@ -695,15 +694,20 @@ struct LoraPlan {
     int rb, slices, kslice;
 };
 
+// few: rows gathered by adapter, where an adapter of the pool has fewer than 16 of
+// them on average (4096 x 4096, rank 16, gathered against in blocks: 256 rows of
+// 32 adapters in any order 17.7 and 53.9 us, 16 rows of 4 6.6 and 9.4; 64 rows of 4
+// adapters in any order 9.5 and 9.9, one adapter after the other 9.6 and 6.1).
 // rb: rows per block / 16; 32 rows (each weight loaded for twice the rows) where
-// their fragments leave registers for two CTAs per SM.  Slices of K: about two
+// their fragments leave registers for two CTAs per SM (4096 rows of rank 32, 11008
+// columns: 86 us, with 16 rows 105).  Slices of K: about two
 // CTAs per SM in the first launch, of at least 64 k for each warp; a decode
 // batch counts as M / 2 adapters (61 rows, rank 64, K = 5120 in 4 slices: with 2
 // the two launches take 58 us in place of 47, with 6 50.7, with 8 52.7).
-static LoraPlan lora_plan(int R, int M, int K, int rank)
+static LoraPlan lora_plan(bool few, int R, int M, int K, int rank)
 {
     LoraPlan p;
-    p.few = M <= kLoraFewRows;
+    p.few = few;
     p.rb = rank <= 32 ? 2 : 1;
     const int64_t groups = p.few ? (M + 1) / 2 : (M + 16 * p.rb - 1) / (16 * p.rb), want = 2 * 148;
     const int most = std::max(1, K / (64 * kLoraWarps));
@@ -715,7 +719,9 @@ static LoraPlan lora_plan(int R, int M, int K, int rank)
 
 size_t lora_workspace_bytes(int R, int M, int K, int rank)
 {
-    return align256((size_t)R * lora_plan(R, M, K, rank).slices * M * rank * sizeof(float));
+    int slices = lora_plan(false, R, M, K, rank).slices;  // whatever the pool's size
+    if (M <= kLoraFewRows) slices = std::max(slices, lora_plan(true, R, M, K, rank).slices);
+    return align256((size_t)R * slices * M * rank * sizeof(float));
 }
 
 int lora_max_group() { return kLoraMaxGroup; }
@@ -748,7 +754,7 @@ lowbit_status lora_launch(const uint16_t *x, const int32_t *ids, const uint16_t 
                           const int32_t *ranks, const float *scales, const float *const *base, float *const *y, int R,
                           int M, int N, int K, int rank, int L, void *workspace, cudaStream_t st)
 {
-    const LoraPlan p = lora_plan(R, M, K, rank);
+    const LoraPlan p = lora_plan(M <= kLoraFewRows && M < 16 * (int64_t)L, R, M, K, rank);
     LoraArgs g = {};
     g.x = x; g.ids = ids; g.ranks = ranks; g.scales = scales;
     for (int r = 0; r < R; ++r) {
