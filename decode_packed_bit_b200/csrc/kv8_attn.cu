@@ -32,8 +32,8 @@
 // Measured: 64 sequences of up to 8192 tokens, 40 query heads on 8 cache heads of
 // 128, one row each 65 us, 5.2 TB/s over the whole launch (2 us until a CTA knows its
 // range, 60 for the tiles, 3 for a CTA's join and 2 for the last units'); one
-// sequence of 131071 tokens, four rows, 67.5 us, 4.0 TB/s (eight warps with 16 rows
-// each: issue and latency); 777 tokens 11 us, a chain of dependent loads and of
+// sequence of 131071 tokens, four rows, 63.4 us, 4.2 TB/s (two units for the 16 rows
+// and head read each tile, once from L2); 777 tokens 11 us, a chain of loads and of
 // code that is fetched and run once.
 #include <algorithm>
 #include <cfloat>

@@ -22,8 +22,8 @@
 // caller's order, with a pass for each adapter in the block.  Nothing is sorted.
 // Bound by the adapters' bytes for decode, by base and y (8 bytes an output)
 // for prompts.  Measured: 61 rows of two 5120 -> 17408 projections, ranks up to 64,
-// 47 us (first launch 17, second 30 at 4.9 TB/s); 4096 rows, 4096 -> 11008, rank 32,
-// 93.5 us (16 and 78, 4.6 TB/s); one row, 4096 -> 4096, rank 16, 5.5 us, latency.
+// 43 us (4.2 TB/s over both launches); 4096 rows, 4096 -> 11008, rank 32, 93.5 us
+// (16 and 78, 4.6 TB/s in the second); one row, 4096 -> 4096, rank 16, 5.5 us, latency.
 #include <algorithm>
 
 #include "common.cuh"

@@ -7,6 +7,7 @@
 #include <Python.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/DynamicTypes.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -61,6 +62,7 @@ bool fits(PyObject *const *args, Py_ssize_t n, const at::Tensor *&t, long long &
 
 PyObject *dense(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
+    HANDLE_TH_ERRORS  // a tensor without storage throws
     const at::Tensor *t;
     long long dev;
     bool error;
@@ -68,11 +70,13 @@ PyObject *dense(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (error) return nullptr;
     if (!ok || !t->is_contiguous()) return refuse(args[0], args[1], args[2], args[3], "(contiguous)", dev);
     return PyLong_FromUnsignedLongLong(reinterpret_cast<uintptr_t>(t->data_ptr()));
+    END_HANDLE_TH_ERRORS
 }
 
 // A [rows][heads][dim] tensor whose rows are dense and may lie apart: address and row stride.
 PyObject *rows(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
+    HANDLE_TH_ERRORS  // a tensor without storage throws
     const at::Tensor *t;
     long long dev;
     bool error;
@@ -92,11 +96,13 @@ PyObject *rows(PyObject *, PyObject *const *args, Py_ssize_t n)
     PyTuple_SET_ITEM(out, 0, PyLong_FromUnsignedLongLong(reinterpret_cast<uintptr_t>(t->data_ptr())));
     PyTuple_SET_ITEM(out, 1, PyLong_FromLongLong(stride));
     return out;
+    END_HANDLE_TH_ERRORS
 }
 
 // (t, device): address and bytes of a workspace, (0, 0) for None.
 PyObject *scratch(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
+    HANDLE_TH_ERRORS  // a tensor without storage throws
     if (n != 2 || (args[0] != Py_None && !THPVariable_Check(args[0]))) {
         PyErr_SetString(PyExc_TypeError, "workspace: expected a tensor or None");
         return nullptr;
@@ -118,6 +124,7 @@ PyObject *scratch(PyObject *, PyObject *const *args, Py_ssize_t n)
     PyTuple_SET_ITEM(out, 0, PyLong_FromUnsignedLongLong(at));
     PyTuple_SET_ITEM(out, 1, PyLong_FromUnsignedLongLong(bytes));
     return out;
+    END_HANDLE_TH_ERRORS
 }
 
 // (address of a function that takes a block, words...): integers, floats (as a double's bits), None (0).

@@ -197,6 +197,11 @@ def test_argument_blocks(lb):
             f(t, torch.float32, (2, 3, 8), "x")
     with pytest.raises(ValueError):
         m.scratch(t, 0)
+    for kind in (t.to_sparse(), t.to("meta")):
+        for f in (lambda x: m.dense(x, torch.float32, (2, 3, 8), "x", 0), lambda x: m.rows(x, torch.float32, (2, 3, 8), "x", 0),
+                  lambda x: m.scratch(x, 0)):
+            with pytest.raises((ValueError, RuntimeError)):
+                f(kind)
     assert m.scratch(None, 0) == (0, 0)
 
 
