@@ -32,9 +32,9 @@
 // Measured: 64 sequences of up to 8192 tokens, 40 query heads on 8 cache heads of
 // 128, one row each 65 us, 5.2 TB/s over the whole launch (2 us until a CTA knows its
 // range, 60 for the tiles, 3 for a CTA's join and 2 for the last units'); one
-// sequence of 131071 tokens, four rows, 63.4 us, 4.2 TB/s (two units for the 16 rows
-// and head read each tile, once from L2); 777 tokens 11 us, a chain of loads and of
-// code that is fetched and run once.
+// sequence of 131071 tokens, four rows, 67.4 us, 4.0 TB/s (eight warps with 16 rows
+// each: issue and latency); 777 tokens 11 us, a chain of loads and of code that is
+// fetched and run once.
 #include <algorithm>
 #include <cfloat>
 
@@ -812,14 +812,15 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     ws += align256((size_t)2 * ctas * kAtMaxRT * 8 * 8);
     a.part_o = reinterpret_cast<float *>(ws);
     // Eight query rows per tile where that holds a sequence's rows, or where there
-    // are few units and the cache is not far beyond L2, so that the units of the same
-    // tokens, side by side on neighbouring SMs, share them there (1 sequence x 4 rows x
-    // 131071 tokens, 268 MB, 62 us against 67 with sixteen; 32 x 2 rows x 1024 tokens 12.1
-    // against 22.9).  Else sixteen, so that a tile of keys and values is read for
-    // twice the rows: what L2 does not hold comes from HBM again with eight (9 x 4
-    // rows x 16384 tokens, 302 MB, 121 us against 190; 8 x 4 x 32768, 537 MB, 110
-    // against 151; many units, 64 x 4 x 4096, 113 against 172).
-    constexpr int64_t kShared = int64_t(280) << 20;
+    // are few units and L2 holds the cache, so that the units of the same tokens, side
+    // by side on neighbouring SMs, read it from HBM once (1 sequence x 4 rows x 8192
+    // tokens 17.4 us against 24 with sixteen, 32 x 2 rows x 1024 tokens 12.1 against
+    // 22.9).  Else sixteen, so that a tile of keys and values is read for twice the
+    // rows: what L2 does not hold comes from HBM again with eight (9 x 4 rows x 16384
+    // tokens, 302 MB, 121 us against 190; 8 x 4 x 32768, 537 MB, 110 against 151; many
+    // units, 64 x 4 x 4096, 113 against 172; 1 x 4 x 131071, 268 MB, by run 62-72
+    // against 67).
+    constexpr int64_t kShared = int64_t(128) << 20;
     const int64_t seqs = b.n_seqs, tiles = ((int64_t)b.n_rows * a.G + 8 * seqs - 1) / (8 * seqs);
     const int64_t bytes = std::min<int64_t>(c.n_pages, seqs * b.max_pages) * c.n_heads * c.page_tokens * c.head_dim * 2;
     const bool one = tiles <= 1 || (tiles * seqs * c.n_heads <= 2 * ctas && bytes <= kShared);

@@ -458,9 +458,9 @@ typedef enum {
  * elements below 2^40.
  * t is held in fp32 and meets b as the sum of three bf16 numbers, which carry
  * all 24 bits of it (a t that is infinite makes its row NaN); sums are fp32 in
- * a fixed order, so the result is the same bits on every run and does not
- * depend on which other rows are in the call's batch beyond the split that M
- * chooses.
+ * a fixed order, so the result is the same bits on every run.  That order
+ * depends on the shape, n_adapters and how many rows share the row's adapter;
+ * what other adapters hold never reaches a row.
  * Group form: R projections of one shape that read one x with one set of ids
  * (HOST arrays of R device pointers, 1 <= R <= 16).  No y_r may be another's y
  * or base.
