@@ -1,5 +1,5 @@
 // marshal.cpp -- what the Python binding of the decode-side calls does per
-// operand and per call, compiled: these calls take 2.7 to 10 us on the GPU, and
+// operand and per call, compiled: these calls take 2 to 10 us on the GPU, and
 // checking an operand from Python took 0.55 us, handing over 20 arguments
 // through ctypes 2.7.  The module checks a tensor and gives its address, and
 // calls an entry point that takes its arguments as a block of 64-bit words.

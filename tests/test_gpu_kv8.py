@@ -374,6 +374,25 @@ def test_rows_out_of_range_are_skipped(lb):
         assert lb.lowbit_fault_flags() == 16
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_sixteen_rows_a_tile(lb, D):
+    """So many units that tiles of sixteen query rows are taken: ragged rows and lengths, an idle slot, a row too many."""
+    g = np.random.default_rng(D)
+    H, G, P, B = 4, 4, 32, 48
+    rows = [int(x) for x in g.integers(3, 6, B)]
+    lens = [int(x) for x in g.integers(1, 150, B)]
+    rows[5], lens[5], lens[6], rows[6] = 0, 0, 3, 5
+    assert sum(rows) * G > 8 * B and -(-sum(rows) * G // (8 * B)) * B * H > 2 * 148
+    n_pages, table = make_batch(D + 1, lens, P)
+    cache = make_cache(lb, D + 2, n_pages, H, P, D)
+    q = torch.randn((sum(rows) + 2, H * G, D), device="cuda").bfloat16()
+    rs = starts(rows)
+    out = attend(lb, cache, table, lens, q, D ** -0.5, rs)
+    check_attention(cache, table, lens, q, D ** -0.5, rs, out)
+    assert torch.equal(out, attend(lb, cache, table, lens, q, D ** -0.5, rs))
+    assert lb.lowbit_fault_flags() == 0
+
+
 @pytest.mark.parametrize("rs", [[0, 500, 90, 600], [0, 500, 0, 500], [300, 600, 10, 20], [600, 500, 400, 0]])
 @pytest.mark.parametrize("G", [4, 8])  # on the integer tensor cores, on tcgen05
 def test_falling_row_starts_stay_inside(lb, G, rs):

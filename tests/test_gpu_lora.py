@@ -120,6 +120,24 @@ def test_padding_and_other_adapters_cannot_reach_a_row(lb):
     assert torch.equal(y[keep], z[keep])
 
 
+@pytest.mark.parametrize("M,L,used", [(40, 4, [1]), (250, 20, [3, 17]), (250, 20, [-1, 0, 5, 6, 7]), (33, 3, [2]), (64, 2, [0, 1]),
+                                      (256, 16, [9]), (256, 17, [9]), (16, 1, [0]), (15, 1, [0]), (20, 30, [4, 4, 4, 5])])
+@pytest.mark.parametrize("rank", [8, 40])
+def test_many_rows_of_an_adapter(lb, M, L, used, rank):
+    """More rows of one adapter than a tile holds, gathered or in blocks; exactly 16, and one more."""
+    N, K = 200, 128
+    x, _, a, b, base, ranks, scales = make(M + L, M, N, K, rank, L)
+    g = torch.Generator().manual_seed(M)
+    ids = torch.tensor(used, dtype=torch.int32)[torch.randint(0, len(used), (M,), generator=g)].cuda()
+    y = torch.full((M, N), float("nan"), device="cuda")
+    ws = workspace(lb, 1, M, N, K, rank)
+    lb.lowbit_lora_add(x, ids, a[0], b[0], base[0], y, ranks, scales, ws)
+    check(y, x, ids, a[0], b[0], base[0], ranks, scales, f"M={M} L={L} used={used} rank={rank}")
+    z = base[0].clone()
+    lb.lowbit_lora_add(x, ids, a[0], b[0], z, z, ranks, scales, ws)
+    assert torch.equal(y, z)
+
+
 def test_graph_follows_ids(lb):
     M, N, K, rank, L = 9, 128, 256, 16, 5
     x, ids, a, b, base, ranks, scales = make(8, M, N, K, rank, L)
