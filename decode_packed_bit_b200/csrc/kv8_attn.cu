@@ -500,12 +500,14 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     // the sums of limbs stay above INT_MIN
                     const float tm = top == INT_MIN ? -INFINITY : (float)top * f;
-                    // probabilities in parts of 1 / 65280 of the tile's largest
-                    const float ref = kAtLog2P - at_ref(tm);
+                    // probabilities in parts of 1 / 65280 of the tile's largest.  The difference
+                    // from it is taken in integers: exact, and the largest's own is 65280 at any
+                    // score.  (Taken in fp32, from scores of 2^16 on an ulp of tm is enough to
+                    // lift it past the 16 bits that the limbs hold.)  What wraps is masked.
                     uint32_t v[8], sum = 0;
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        v[x] = __float2uint_rn(at_exp2(fmaf((float)s[x], f, ref)));
+                        v[x] = __float2uint_rn(at_exp2(fmaf((float)(int)((unsigned)s[x] - (unsigned)top), f, kAtLog2P)));
                     }
                     if (masked) {
                         asm volatile("" ::: "memory");

@@ -598,7 +598,12 @@ lowbit_status lowbit_kv8_read(const lowbit_kv8_cache *cache, const lowbit_kv8_ba
  * Few rows per sequence (a decode step, tokens to be checked) run on the integer
  * tensor cores, split over the tokens; many rows (prompts: at least 64 rows x
  * query heads per cache head for each sequence, and 8192 of them in all) on
- * tcgen05.  Both keep sums and probabilities' statistics in fp32.
+ * tcgen05.  Both keep sums and probabilities' statistics in fp32, and are right for
+ * scores of any size that fp32 holds.  Roundings of q and of the probabilities:
+ * few rows take a row of q as multiples of 1 / 32512 of its largest magnitude
+ * (rounded; a single large entry makes the others' steps as large) and probabilities
+ * as multiples of 1 / 65280 of the largest in 32 tokens; prompts take both as f16
+ * after a power of two (q's, exactly but for entries below 2^-14 of the largest).
  * workspace: lowbit_kv8_attention_workspace_bytes(cache, batch, q_heads) bytes,
  * zero-filled before its first use (calls leave what they need zeroed).  Calls
  * that share one must be ordered on one stream; that holds for replays of
