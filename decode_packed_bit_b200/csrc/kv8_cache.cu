@@ -81,7 +81,9 @@ __device__ __forceinline__ uint32_t kv8_top8(const float (&v)[8], uint32_t top)
 // 1.5 ulp at most, 2e-5 below 127, so only a quotient within 1e-4 of a tie may be
 // rounded wrongly: it is taken again in double.  Adding 1.5 * 2^23
 // rounds to an integer (ties to even) and leaves it in the low bits, in two's
-// complement.  |x| <= 127 s up to s's own rounding: no clamp.
+// complement.  |x| <= 127 s (1 + 2^-23) where s is a normal number; a subnormal s
+// may be up to a half off (190 units of 2^-149 give s = 1), so quotients are held
+// to 127, in the branch that they all take: below 2^-128 inv is infinite.
 __device__ __forceinline__ uint2 kv8_codes8(const float (&x)[8], float s, float inv)
 {
     constexpr float kMagic = 12582912.f;
@@ -98,7 +100,7 @@ __device__ __forceinline__ uint2 kv8_codes8(const float (&x)[8], float s, float 
         float v = x[0];
 #pragma unroll
         for (int y = 1; y < 8; ++y) v = k == y ? x[y] : v;
-        const uint32_t q = (uint32_t)(int)rint((double)v / (double)s);
+        const uint32_t q = (uint32_t)(int)fmin(fmax(rint((double)v / (double)s), -127.0), 127.0);
 #pragma unroll
         for (int y = 0; y < 8; ++y) c[y] = k == y ? q : c[y];
     }

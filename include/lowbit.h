@@ -568,7 +568,8 @@ typedef struct {
  *     s' = max(s, fp32(max |new| / 127)), s taken as 0 unless the page already
  *          holds older tokens of the sequence
  *     an older token's code c becomes rint(c * s / s'); a new value's code is
- *     rint(x / s'), both rounded exactly, ties to even (0 where s' = 0);
+ *     rint(x / s'), held to [-127, 127] (which it exceeds only where s' is below
+ *     2^-128), both rounded exactly, ties to even (0 where s' = 0);
  * the slots after the last token are left as they were.  NaN counts as 0 and
  * infinities as the largest float.  A page's scale grows while the page fills,
  * and each growth rounds its older codes once more (half a step of the new
