@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(AttnShape<D, RT>::kThreads, 1) k_kv8_attn(cons
             bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 1) != 0;
             bad |= __shfl_xor_sync(0xffffffffu, (int)bad, 2) != 0;
             const float inv = top >= 0x1p-100f && !bad ? a.limbs / top : 0.f;
-            rowf[m] = bad && lim[m] > 0 ? NAN : top * (1.f / 32512.f) * a.scale_log2;
+            // a row that sees nothing gives zeros whatever it holds: `fac` below takes 0 * rowf
+            rowf[m] = lim[m] <= 0 ? 0.f : bad ? NAN : top * (1.f / 32512.f) * a.scale_log2;
             // 16-byte chunk t + 4 c of a key meets entries 64 c + 16 t ..: two
             // fragments of 8 entries each
 #pragma unroll

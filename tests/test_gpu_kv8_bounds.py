@@ -95,3 +95,25 @@ def test_equal_largest_scores(lb, rows, H, G, largest):
     # each weight within 2^-11 (f16) or 2^-17, fp32 sums, bf16
     tol = 2.0 ** -8 * want.abs() + 2.0 ** -10 * 1.27
     assert ((out - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan"), 3e38])
+@pytest.mark.parametrize("H,G,D,lens,rows", [(2, 4, 64, [2, 20, 100], [5, 30, 4]), (1, 8, 128, [1, 3], [2, 4]), (2, 4, 128, [1, 0, 33], [8, 1, 2]),
+                                             (4, 8, 128, [40, 150, 90], [200, 160, 91])])
+def test_rows_without_a_place_hold_anything(lb, H, G, D, lens, rows, bad):
+    """Rows before the first token share tiles with rows that have one: zeros, and the others as they were."""
+    n_pages, table = make_batch(D, lens, 32)
+    cache = make_cache(lb, D + 1, n_pages, H, 32, D)
+    rs = starts(rows)
+    q = queries(D + G, sum(rows), H * G, D)
+    clean = attend(lb, cache, table, lens, q, 0.1, rs)
+    check(cache, table, lens, q, 0.1, rs, clean)
+    for b, (n, r) in enumerate(zip(lens, rows)):
+        without = int(rs[b]) + max(r - n, 0)
+        q[int(rs[b]):without, :, 3] = bad
+        q[int(rs[b]):without, 0, :] = bad
+    for scale in (0.1, -0.1):
+        out = attend(lb, cache, table, lens, q, scale, rs)
+        check(cache, table, lens, q, scale, rs, out)
+        if scale > 0:
+            assert torch.equal(out, clean)
