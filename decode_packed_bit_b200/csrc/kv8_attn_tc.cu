@@ -156,8 +156,8 @@ __device__ __forceinline__ void att_st16(uint32_t addr, const uint32_t (&v)[16])
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void att_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// The same, and the values loaded may be used only after it.
+// The values that were loaded are operands of the wait: what uses them can then
+// not be moved before it (a volatile asm keeps its place among others of its kind only).
 __device__ __forceinline__ void att_wait_ld(uint32_t (&v)[16])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                     uint32_t v[32];
                     if (steps > 0) {
                         att_ld32(to + 32 * c, v);
-                        att_wait_ld();
+                        att_wait_ld(v);
                     } else {
 #pragma unroll
                         for (int y = 0; y < 32; ++y) v[y] = 0;
