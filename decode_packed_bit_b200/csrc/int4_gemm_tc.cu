@@ -117,6 +117,22 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
         : "r"(taddr));
 }
 
+// The wait for all loads under way.  The values that were loaded are operands of it,
+// or of the empty statement after it (volatile ones keep their order), so that
+// their use stays behind the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+}
+__device__ __forceinline__ void tmem_waited(uint32_t (&v)[16])
+{
+    asm volatile(""
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                   "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+}
+
 template <int NCH>  // 32-column chunks a thread drains (BM / 64)
 __device__ __forceinline__ void drain_group(uint32_t taddr, float d, float (&acc)[128])
 {
@@ -127,7 +143,10 @@ __device__ __forceinline__ void drain_group(uint32_t taddr, float d, float (&acc
 #pragma unroll
         for (int u = 0; u < D; ++u)
             if (c0 + u < 2 * NCH) tmem_ld16(taddr + 16u * (c0 + u), v[u]);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        tmem_wait_ld(v[0]);
+#pragma unroll
+        for (int u = 1; u < D; ++u)
+            if (c0 + u < 2 * NCH) tmem_waited(v[u]);
 #pragma unroll
         for (int u = 0; u < D; ++u)
             if (c0 + u < 2 * NCH)

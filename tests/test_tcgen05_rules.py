@@ -16,7 +16,7 @@ def waits(name):
         return re.findall(r'asm volatile\(\s*"tcgen05\.wait::ld[^;]*;"(.*?)\);', f.read(), re.S)
 
 
-@pytest.mark.parametrize("name", ["kv8_attn_tc.cu"])
+@pytest.mark.parametrize("name", ["kv8_attn_tc.cu", "int4_gemm_tc.cu"])
 def test_waits_for_tensor_memory_loads_tie_their_values(name):
     found = waits(name)
     assert found
