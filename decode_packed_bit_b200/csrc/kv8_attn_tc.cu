@@ -9,11 +9,15 @@
 //     by 2^-25 of it at most.  S = Q K^T is then exact but for fp32 sums; the
 //     row's power, the softmax scale and k's page scale multiply S.
 //   - v's page scale goes into the exponent: with x = s + log2(vs) a probability
-//     is exp2(x - m), m a running maximum of x, so P fits f16 (at most 2^8, off by
-//     2^-12 of itself) for any scales, O sums P times codes, and the row sum takes
-//     P / vs in fp32.
-// m follows the true maximum only when that is more than 8 ahead, which after
-// the first tiles is rare: only then O is rescaled in tensor memory.
+//     is exp2(x - m), m a reference 7 below a running maximum of x, so P fits f16 for
+//     any scales: at most 2^15, off by 2^-11 of itself, and normal down to 2^-21 of
+//     the largest, zero below 2^-32.  (m at the maximum itself left an f16 of 2^-24
+//     of it a single bit: where one token leads 4000 others by e^16.4 and has no
+//     value of its own, the output was a fifth off.)  O sums P times codes, and the row
+//     sum takes P / vs in fp32.
+// m follows the maximum only when that is more than 8 ahead, which after the first
+// tiles is rare (any reference gives the same quotient): only then O is rescaled
+// in tensor memory.
 //
 // A CTA takes two tiles of up to 128 rows (query tokens x the query heads that
 // share a cache head) of one sequence and cache head, which share K and V:
@@ -52,6 +56,9 @@ constexpr int kAttTokens = 128;  // tokens of a step
 constexpr int kAttConvWarp = 8, kAttMmaWarp = 12;
 constexpr int kAttThreads = 13 * 32;
 constexpr int kAttInfo = 4;  // steps of scales kept
+constexpr float kAttBelow = 7.f;        // the reference lies so far below the maximum it was taken from,
+constexpr float kAttAhead = 8.f;        // which may have grown by so much: P is at most 2^15
+constexpr float kAttUnit = 0x1p-7f;     // the row sum's unit: P / vs at the reference's own maximum
 
 struct Kv8AttnTc {
     Kv8View v;
@@ -73,7 +80,7 @@ struct AttnTc {
     static constexpr int kQ = 0;                           // [2]
     static constexpr int kK = 2 * kTile;                   // [2 stages]
     static constexpr int kV = 4 * kTile;                   // [2 stages]
-    static constexpr int kInfoAt = 6 * kTile;              // [kAttInfo][4 chunks] {ks or -1, log2 vs, 1 / vs, vs != 0}
+    static constexpr int kInfoAt = 6 * kTile;              // [kAttInfo][4 chunks] {ks or -1, log2 vs, kAttUnit / vs, vs != 0}
     static constexpr int kBars = kInfoAt + kAttInfo * 4 * 16;
     static constexpr int kBytes = kBars + 16 * 8 + 16 + 1024;
     static constexpr unsigned kTmem = 512;                 // S 0, S 1, O 0, O 1
@@ -210,7 +217,7 @@ __device__ __forceinline__ float att_top(const uint32_t (&v)[32], const float4 &
     return in.x >= 0.f && (!MASK || most > -INFINITY) ? fmaf(most, row_f * in.x, in.y) : -INFINITY;
 }
 
-// Their probabilities, two a word, and the sum over vs.
+// Their probabilities, two a word, and their sum over vs in parts of kAttUnit.
 template <bool MASK>
 __device__ __forceinline__ float att_probs(uint32_t (&p)[16], const uint32_t (&v)[32], const float4 &in, int left, float row_f,
                                            float ref)
@@ -432,9 +439,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                     x = fmaxf(x, masked ? att_top<true>(v, in, left - 32 * c, row_f) : att_top<false>(v, in, left - 32 * c, row_f));
                     __syncwarp();
                 }
-                const bool grow = x > m + 8.f;
+                const bool grow = x > m + (kAttBelow + kAttAhead);
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float now = grow ? x : m, f = grow ? att_exp2(m - now) : 1.f;
+                    const float now = grow ? x - kAttBelow : m, f = grow ? att_exp2(m - now) : 1.f;
                     m = now;
                     l *= f;
                     if (i > 0 && !rescale(i, f)) {
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
             if (ok && steps > 0) ok = att_wait(pvdone + tile, (steps - 1) & 1);
             tc_fence_after();
             if (ok) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = l == 0.f ? 0.f : kAttUnit / l;
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t v[32];
@@ -529,7 +536,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
                 // a page of zeros (its probabilities still count in the row's
                 // sum) stands with a scale that never leads the maximum
                 const float vs = raw_info.y, e = vs < 0x1p-100f ? 0x1p-60f : vs;
-                info[(i % kAttInfo) * 4 + lane] = make_float4(raw_info.x, log2f(e), 1.f / e, vs < 0x1p-100f ? 0.f : 1.f);
+                info[(i % kAttInfo) * 4 + lane] = make_float4(raw_info.x, log2f(e), kAttUnit / e, vs < 0x1p-100f ? 0.f : 1.f);
             }
         };
         auto store = [&](unsigned at, const uint4 (&raw)[NP]) {

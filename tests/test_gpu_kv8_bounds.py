@@ -117,3 +117,21 @@ def test_rows_without_a_place_hold_anything(lb, H, G, D, lens, rows, bad):
         check(cache, table, lens, q, scale, rs, out)
         if scale > 0:
             assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("lead", [8.0, 14.0, 16.4, 18.0])
+@pytest.mark.parametrize("rows,H,G,D", [(1, 2, 4, 128), (9, 1, 8, 64), (600, 2, 8, 128), (1100, 8, 1, 64)])
+def test_a_leading_token_without_value(lb, rows, H, G, D, lead):
+    """One token leads all others by `lead` and has values of zero, so that what is left is the others' part, which
+    weights of few bits would lose: the others have equal scores, and their roundings the same sign."""
+    P, n = 32, 4000
+    n_pages, table = make_batch(17, [n], P)
+    cache = make_cache(lb, 18, n_pages, H, P, D)
+    cache.k_scales[:] = 0.01
+    cache.k[:] = 0
+    first = int(table[0, 0])
+    cache.k[first, :, 0] = 100
+    cache.v[first, :, 0] = 0
+    q = torch.ones((rows, H * G, D), device="cuda").bfloat16()
+    out = attend(lb, cache, table, [n], q, lead / D, starts([rows]))
+    check(cache, table, [n], q, lead / D, starts([rows]), out)
