@@ -543,7 +543,7 @@ lowbit_status lowbit_rmsnorm_bf16(const float *a, const float *b, int M, int D, 
 static lowbit_status lora_shape_ok(int R, int M, int N, int K, int rank)
 {
     LB_CHECK(R >= 1 && R <= lora_max_group() && M >= 1 && N >= 1 && K >= 1 && rank >= 1, LOWBIT_ERR_INVALID_ARG);
-    LB_CHECK(K % 64 == 0 && rank % 8 == 0 && rank <= 128 && N <= (1 << 25) && M <= (1 << 30),
+    LB_CHECK(K % 64 == 0 && K <= (1 << 28) && rank % 8 == 0 && rank <= 128 && N <= (1 << 25) && M <= (1 << 30),
              LOWBIT_ERR_UNSUPPORTED_SHAPE);
     LB_CHECK((int64_t)M * N < kMaxElems && (int64_t)M * K < kMaxElems, LOWBIT_ERR_UNSUPPORTED_SHAPE);
     return LOWBIT_OK;

@@ -453,8 +453,8 @@ typedef enum {
  *   scales [n_adapters] fp32, or NULL (all 1)
  *   base   [M][N] fp32, the shared projection's output; may be y itself
  *   y      [M][N] fp32
- * Shapes: 1 <= M <= 2^30, 1 <= N <= 2^25, K >= 64 with K % 64 == 0, 8 <= rank
- * <= 128 with rank % 8 == 0, n_adapters >= 1, M * N, M * K and the adapters'
+ * Shapes: 1 <= M <= 2^30, 1 <= N <= 2^25, 64 <= K <= 2^28 with K % 64 == 0, 8 <=
+ * rank <= 128 with rank % 8 == 0, n_adapters >= 1, M * N, M * K and the adapters'
  * elements below 2^40.
  * t is held in fp32 and meets b as the sum of three bf16 numbers, which carry
  * all 24 bits of it (a t that is infinite makes its row NaN); sums are fp32 in
