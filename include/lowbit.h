@@ -616,11 +616,11 @@ lowbit_status lowbit_kv8_attention(const lowbit_kv8_cache *cache, const lowbit_k
                                    int64_t out_stride, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The same calls with their arguments in one block of 64-bit words, for bindings
- * that pay for each argument (a call of 20 costs 2.7 us through Python's ctypes, one block
- * 1.0): the parameters in order, pointers as addresses, a float as the bits of
- * the double it equals.  lowbit_lora_add_group's arrays follow the last
- * parameter in place of four of them: a[R], b[R], base[R], y[R]; a batch's
- * pointer becomes its six members. */
+ * that pay for each argument: the parameters in order, pointers as addresses, a
+ * float as the bits of the double it equals.  lowbit_lora_add_group's arrays
+ * follow the last parameter in place of four of them: a[R], b[R], base[R], y[R];
+ * a batch's pointer becomes its six members.  A number that its 32-bit parameter
+ * does not hold is LOWBIT_ERR_UNSUPPORTED_SHAPE. */
 lowbit_status lowbit_lora_add_group_args(const int64_t *args);
 lowbit_status lowbit_rope_args(const int64_t *args);
 lowbit_status lowbit_kv8_append_args(const int64_t *args);
