@@ -351,7 +351,11 @@ _LORA = _ROPE = _APPEND = _READ = _ATTENTION = 0  # addresses of the entry point
 
 def _first_call():
     import torch
-    from . import _marshal
+    try:
+        from . import _marshal
+    except ImportError as e:
+        raise RuntimeError(f"{os.path.join(PKG, '_marshal.so')} is missing or for another torch: build it with "
+                           "`python -m decode_packed_bit_b200.build` (it needs g++)") from e
     global _float32, _bfloat16, _int32, _int64, _int8, _halves, _dense, _rows, _scratch, _call
     global _LORA, _ROPE, _APPEND, _READ, _ATTENTION, _device, _current_stream
     torch.cuda.init()
