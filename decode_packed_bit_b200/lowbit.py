@@ -366,7 +366,8 @@ def _first_call():
         ctypes.cast(getattr(lib(), f"lowbit_{name}_args"), P).value
         for name in ("lora_add_group", "rope", "kv8_append", "kv8_read", "kv8_attention"))
     _types.update({_float32: LOWBIT_F32, _bfloat16: LOWBIT_BF16})
-    _device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    # _device last: from then on another thread takes all of these as set
+    _current_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     return _device()
 
 
@@ -399,11 +400,11 @@ def lowbit_lora_add_group(x, ids, a, b, base, ys, ranks=None, scales=None, works
     workspace: lowbit_lora_workspace_bytes(R, M, N, K, rank) bytes."""
     dev = _device()
     R = len(a)
-    if not 1 <= R == len(b) == len(base) == len(ys):
-        raise ValueError("lowbit_lora_add_group: lists of different lengths")
+    if not 1 <= R == len(b) == len(base) == len(ys) <= 16:
+        raise ValueError("lowbit_lora_add_group: expected lists of one length, 1 to 16")
     M, K = x.shape
     L, rank, _ = a[0].shape
-    N = b[0].shape[1]
+    _, N, _ = b[0].shape
     sa, sb, sy, sl = (L, rank, K), (L, N, rank), (M, N), (L,)
     ws, ws_bytes = _scratch(workspace, dev)
     _check(_call(
@@ -437,6 +438,8 @@ def lowbit_rope(q, q_out, k, k_out, positions, phases, interleaved=False, magnit
     """q [M][q_heads][D] -> q_out and k [M][kv_heads][D] -> k_out (either pair may be None), fp32 or bf16, rows dense
     and any stride (a multiple of 8) apart; positions int32 [M]; phases int64 [rot / 2].  In place where types match."""
     dev = _device()
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or q is k is None:
+        raise ValueError("lowbit_rope: expected q with q_out, k with k_out, or both")
     ref, ref_out = (q, q_out) if q is not None else (k, k_out)
     M, _, D = ref.shape
     half = phases.shape[0]
@@ -524,6 +527,8 @@ def lowbit_kv8_read(cache: KV8Cache, page_table, kv_len, k_out, v_out, row_start
     type, fp32 or bf16; either may be None)."""
     dev = _device()
     ref = k_out if k_out is not None else v_out
+    if ref is None:  # nothing is asked for
+        return
     rows = ref.shape[0]
     shape = (rows, cache.n_heads, cache.head_dim)
     batch = _kv8_batch(cache, page_table, kv_len, row_start, rows, dev)
