@@ -168,6 +168,10 @@ int lowbit_version(void) { return 100; }
 
 int lowbit_fault_flags(void)
 {
+    // the copies below wait for the legacy stream only, not for streams that do not
+    // block with it; a kernel on such a one could also set a flag just before it is
+    // cleared
+    if (cudaDeviceSynchronize() != cudaSuccess) return -1;
     const int f4 = i4tc_fault_flag(), fs = q1stack_fault_flag(), fg = smg_fault_flag();
     const int fk = kv8_fault_flag(), fa = kv8_attn_fault_flag(), ft = kv8_attn_tc_fault_flags();
     if (f4 < 0 || fs < 0 || fg < 0 || fk < 0 || fa < 0 || ft < 0) return -1;
