@@ -557,9 +557,8 @@ __global__ void __launch_bounds__(kLoraThreads, LoraRing<KT, 1>::kCtas) k_lora_e
                 y[(int64_t)blockIdx.x * a.N + n] = base[(int64_t)blockIdx.x * a.N + n];
         return;
     }
-    // (a rank of 16 has three MMAs to save, and two ways cost it registers: 12.9
-    // against 12.3 us for 16 rows of three 5120 x 5120 projections)
-    if (KT > 1 && own.n <= 4)
+    // (one row, rank 16, 4096 x 4096: 4.8 us against 5.5 with the form for 16 rows)
+    if (own.n <= 4)
         lora_expand_rows<KT, VEC, true>(a, own, rows, frag, ring, c0, n_end);
     else
         lora_expand_rows<KT, VEC, false>(a, own, rows, frag, ring, c0, n_end);
@@ -765,15 +764,15 @@ lowbit_status lora_launch(const uint16_t *x, const int32_t *ids, const uint16_t 
     g.slices = p.slices; g.kslice = p.kslice;
     const int64_t groups = p.few ? M : ((int64_t)M + 16 * p.rb - 1) / (16 * p.rb);
     // Columns per CTA of the second launch, in rounds of the CTA's warps: as few as
-    // fill the SMs at once (a decode batch counts as 3 / 4 M adapters: 10.5 us for 16
-    // rows of three 5120 x 5120 projections against 12.3 as M / 2 and 10.9 as M), at
+    // fill the SMs at once (a decode batch counts as M adapters: 10.3 us for 16 rows of
+    // three 5120 x 5120 projections against 10.9 as 3 / 4 M and 12.3 as M / 2), at
     // most 20 for few rows and 8 for many.  A CTA has 3 us to go before its first
     // round, but those with more adapters or a higher rank take longer and the SMs
-    // wait for the last of them: 61 rows, rank 64, 17408 columns 51.6 us with 8,
-    // 47.1 with 20, 52.5 with 27; 4096 rows, rank 32, 11008 columns 93.6 us with 8,
-    // 98.3 with 12, 102 with 17.
+    // wait for the last of them: 61 rows, rank 64, 17408 columns 47.2 us with 8,
+    // 44.4 with 12, 42.9 with 20, 47.3 with 27; 4096 rows, rank 32, 11008 columns 93.6
+    // us with 8, 98.3 with 12, 102 with 17.
     const int64_t rounds = (N + kLoraWarps * 16 - 1) / (kLoraWarps * 16), slots = (rank <= 16 && p.few ? 4 : rank <= 64 ? 2 : 1) * 148;
-    const int64_t each = (rounds * (p.few ? (3 * groups + 3) / 4 : groups) * R + slots - 1) / slots;
+    const int64_t each = (rounds * groups * R + slots - 1) / slots;
     g.cols = (int)std::min<int64_t>(std::max<int64_t>(each, 1), p.few ? 20 : 8) * kLoraWarps * 16;
     const dim3 gs((unsigned)(groups * p.slices), R, p.few ? 1 : 2), ge((unsigned)groups, (unsigned)((N + g.cols - 1) / g.cols), R);
     const cudaError_t e = rank <= 16   ? lora_run<1>(p, gs, ge, g, st)
