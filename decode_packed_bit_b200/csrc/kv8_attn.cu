@@ -817,12 +817,14 @@ lowbit_status kv8_attn_launch(const lowbit_kv8_cache &c, const lowbit_kv8_batch 
     // Eight query rows per tile where that holds a sequence's rows, or where there
     // are few units and L2 holds the cache, so that the units of the same tokens, side
     // by side on neighbouring SMs, read it from HBM once (1 sequence x 4 rows x 8192
-    // tokens 17.4 us against 24 with sixteen, 32 x 2 rows x 1024 tokens 12.1 against
-    // 22.9).  Else sixteen, so that a tile of keys and values is read for twice the
+    // tokens 17.7 us against 24.3 with sixteen, 32 x 2 rows x 1024 tokens 12.1 against
+    // 22.8).  Else sixteen, so that a tile of keys and values is read for twice the
     // rows: what L2 does not hold comes from HBM again with eight (9 x 4 rows x 16384
-    // tokens, 302 MB, 121 us against 190; 8 x 4 x 32768, 537 MB, 110 against 151; many
-    // units, 64 x 4 x 4096, 113 against 172; 1 x 4 x 131071, 268 MB, by run 62-72
-    // against 67).
+    // tokens, 302 MB, 119 us against 190; 8 x 4 x 32768, 537 MB, 109 against 148; many
+    // units, 64 x 4 x 4096, 111 against 173; 1 x 4 x 131071, 268 MB, by run 62-72
+    // against 67).  Lengths are on the device, so the rule takes what the cache and the
+    // page table could hold: a pool and a table of more than 128 MB get sixteen rows,
+    // however short the sequences are.
     constexpr int64_t kShared = int64_t(128) << 20;
     const int64_t seqs = b.n_seqs, tiles = ((int64_t)b.n_rows * a.G + 8 * seqs - 1) / (8 * seqs);
     const int64_t bytes = std::min<int64_t>(c.n_pages, seqs * b.max_pages) * c.n_heads * c.page_tokens * c.head_dim * 2;

@@ -2,7 +2,8 @@
 // cache, on the 5th-generation tensor cores (tcgen05.mma kind::f16).
 //
 // out[r] = sum_t softmax_t(scale q[r] . k[t]) v[t], t up to the row's position,
-// in one pass with a running maximum and sum per row.  Both products take the
+// in one pass with a running maximum and sum per row (Milakov and Gimelshein,
+// "Online normalizer calculation for softmax", 2018).  Both products take the
 // cache's codes as f16, which holds them exactly:
 //   - a row of q is scaled by a power of two to its own largest value and becomes
 //     f16: its bf16 mantissa fits, and entries below 2^-14 of the largest are off
@@ -32,7 +33,7 @@
 // At best bound by the exponentials (16 a clock and SM) and the tensor cores alike:
 // 128 x 128 scores take about 1024 clocks of either at D = 128.  Measured, three
 // prompts of 1900, 1866 and 797 rows over 8192, 1866 and 3509 tokens, 40 query
-// heads on 8: 510 us, 0.44 of the cuBLAS bf16 rate; a step of two tiles takes about
+// heads on 8: 511 us, 0.44 of the cuBLAS bf16 rate; a step of two tiles takes about
 // 5400 clocks, of which a tile waits 1700 for its scores, looks for their maximum
 // for 850 and makes its probabilities in 2600.  Leaving out the exponentials, or all
 // MMAs but one, changes a step by less than a tenth: it is a chain of latencies
@@ -194,8 +195,9 @@ __device__ __forceinline__ uint32_t att_f16x2(float lo, float hi)
     return r;
 }
 
-// Four int8 codes -> two words of exact f16: 0x6400 + u is 1024 + u for a byte u,
-// and u = code + 128.
+// Four int8 codes -> two words of exact f16: an f16 in [1024, 2048) has steps of 1, so the
+// bits 0x6400 + u are 1024 + u for a byte u (Kim, Henry, Fahim and Awadalla, "Who says
+// elephants can't run", 2022), and u = code + 128.
 __device__ __forceinline__ uint2 att_codes(uint32_t w)
 {
     const uint32_t u = w ^ 0x80808080u;
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) k_kv8_attn_tc(const Kv8AttnTc 
     if (a.v.n_seqs > 1 && a.items <= kAttThreads) {
         // between sequences it is not: every CTA ranks the items by their steps
         // (in the order of the rows, the longest sequence's could come last, and
-        // the SMs wait for them: 757 against 620 us for the three prompts below)
+        // the SMs wait for them: 624 against 511 us for the three prompts above)
         int *cost = reinterpret_cast<int *>(smem);
         if (threadIdx.x < kAttThreads) cost[threadIdx.x] = (int)threadIdx.x < a.items ? att_unit(a, threadIdx.x).steps : -1;
         __syncthreads();
@@ -675,10 +677,14 @@ static int64_t attn_tc_units(const lowbit_kv8_cache &c, const lowbit_kv8_batch &
 }
 
 // Which calls.  Time of the integer kernel over this one's: with 4096 rows (row,
-// query head) in all 0.65-0.87, 8192 0.90-1.30, 16384 1.16-1.66; 64 rows a
-// sequence and head (32 sequences x 16 rows, four heads a cache head) 1.16.  With
-// one sequence's 64 x 8 rows over 32768 tokens it is 0.29: eight units for 148
-// SMs, which the integer kernel cuts along the tokens and this one does not.
+// query head, over all cache heads) 0.50-0.53, 8192 0.98-0.99, 12288 1.46, 16384
+// 1.8-1.9, and 1.09 with 64 rows a sequence and head (32 sequences x 16 rows, four heads
+// a cache head).  Long contexts are among these (1 sequence, 64 heads on 8: 64 rows over
+// 32768 tokens 373 us against 741; 128 rows over 32768 729 against 745, over 131072 2844
+// against 2864; 192 rows over 32768 1090 against 746; 1024 rows of 8 heads on 1 over
+// 16384 374 against 380), although this kernel does not cut a unit along its tokens
+// and leaves most SMs idle there: the 8192 rows are 32 units.  Rows are averaged over the
+// call's sequences: a long prompt takes single rows beside it with it.
 bool kv8_attn_tc_takes(const lowbit_kv8_cache &c, const lowbit_kv8_batch &b, int q_heads)
 {
     const int64_t rows = (int64_t)b.n_rows * (q_heads / c.n_heads);

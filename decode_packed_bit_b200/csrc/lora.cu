@@ -22,8 +22,10 @@
 // caller's order, with a pass for each adapter in the block.  Nothing is sorted.
 // Bound by the adapters' bytes for decode, by base and y (8 bytes an output)
 // for prompts.  Measured: 61 rows of two 5120 -> 17408 projections, ranks up to 64,
-// 43 us (4.2 TB/s over both launches); 4096 rows, 4096 -> 11008, rank 32, 93.5 us
-// (16 and 78, 4.6 TB/s in the second); one row, 4096 -> 4096, rank 16, 5.5 us, latency.
+// 42.9 us (4.2 TB/s over both launches); 4096 rows, 4096 -> 11008, rank 32, 93.7 us
+// (16 and 78, 4.6 TB/s in the second); one row, 4096 -> 4096, rank 16, 4.8 us, latency.
+// The first launch moves its bytes at 1.7 to 2.3 TB/s only: its loads go straight
+// into registers, 64 contiguous bytes of a row at a time, two steps ahead.
 #include <algorithm>
 
 #include "common.cuh"
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kLoraThreads, NT == 8 ? 2 : 1) k_lora_shrink_f
 
 // Many rows: grid (blocks of 16 RB rows x slices, projections, 2): z = 0 takes a
 // block's first adapter, z = 1 its others (with one CTA for
-// all, the blocks where prompts meet ended last: 4096 rows x 4096 25.8 us, so 20.5).
+// all, the blocks where prompts meet ended last: 102 us for the prompts above, so 93.7).
 // NT: rank / 8, rounded up to 2, 4, 8 or 16.
 template <int NT, int RB>
 __global__ void __launch_bounds__(kLoraThreads) k_lora_shrink(const LoraArgs a)
@@ -320,7 +322,7 @@ struct LoraPieces {
 
 // acc = the block's rows of t (f: their bf16 numbers, in NS fragments) times a stage's 16
 // columns of B.  Steps of 16 entries beyond the adapter's rank are left out (with
-// one or two steps the branch costs more than it saves: 94 against 85 us for
+// one or two steps the branch costs more than it saves: 110 against 93.7 us for
 // 4096 rows of rank 32), and in the step that it ends in the entries from the rank on are cleared: they
 // may hold anything.
 template <int KT, int RB, int NS>
@@ -695,14 +697,18 @@ struct LoraPlan {
 
 // few: rows gathered by adapter, where an adapter of the pool has fewer than 16 of
 // them on average (4096 x 4096, rank 16, gathered against in blocks: 256 rows of
-// 32 adapters in any order 17.7 and 53.9 us, 16 rows of 4 6.6 and 9.4; 64 rows of 4
-// adapters in any order 9.5 and 9.9, one adapter after the other 9.6 and 6.1).
+// 32 adapters in any order 14.0 and 57.0 us, 16 rows of 4 5.4 and 8.9; 64 rows of 4
+// adapters in any order 9.9 and 10.0, one adapter after the other 9.9 and 6.1; 256 rows
+// of 4 14.9 and 11.7).  The rule sees the pool's size and not the ids, which are on the
+// device: 200 rows of 12 adapters in any order go in blocks and take 29 us, where
+// 13 adapters' are gathered and take 12.9; and beyond 256 rows all go in blocks, 512 rows of
+// 32 adapters 11.7 us in runs and 73 in any order.
 // rb: rows per block / 16; 32 rows (each weight loaded for twice the rows) where
 // their fragments leave registers for two CTAs per SM (4096 rows of rank 32, 11008
-// columns: 86 us, with 16 rows 105).  Slices of K: about two
+// columns: 93.7 us, with 16 rows 112).  Slices of K: about two
 // CTAs per SM in the first launch, of at least 64 k for each warp; a decode
-// batch counts as M / 2 adapters (61 rows, rank 64, K = 5120 in 4 slices: with 2
-// the two launches take 58 us in place of 47, with 6 50.7, with 8 52.7).
+// batch counts as M / 2 adapters (61 rows, rank 64, K = 5120 in 4 slices: 42.9 us for
+// both launches; in 2 51, 3 45.1, 6 46.8, 8 46.0).
 static LoraPlan lora_plan(bool few, int R, int M, int K, int rank)
 {
     LoraPlan p;
