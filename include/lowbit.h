@@ -35,12 +35,12 @@
  *     and keeps no state across calls besides the fault flags
  *     (lowbit_fault_flags) and the scratch array of the allocation-free
  *     entry point; entry points are safe to call from several host threads
- *     on different streams.  Only the Q1_0_g128 entry points take a
- *     caller-provided workspace, for the shapes whose kernel reads a
+ *     on different streams.  Of the products only the Q1_0_g128 entry points
+ *     take a caller-provided workspace, for the shapes whose kernel reads a
  *     prepared activation from global memory; its size comes from the
  *     matching *_workspace_bytes() query, which returns 0 for every shape a
  *     one-launch kernel takes (the activation is then built in shared
- *     memory).
+ *     memory).  The adapters and the KV8 attention always take one.
  *
  * Packed layouts (one row of a matrix is packed along K):
  *   Q1_0_g128  bits   [N][K/8]:   weight k is bit (k%8) of byte k/8; bit 1
@@ -574,7 +574,7 @@ typedef struct {
  * infinities as the largest float.  A page's scale grows while the page fills,
  * and each growth rounds its older codes once more (half a step of the new
  * scale at most).  The result is the same bits on every run.  A page may get
- * tokens of one sequence per call only. */
+ * tokens of one sequence per call only, and stand in that sequence's table once. */
 lowbit_status lowbit_kv8_append(const lowbit_kv8_cache *cache, const lowbit_kv8_batch *batch, const void *k,
                                 int64_t k_stride, lowbit_dtype k_type, const void *v, int64_t v_stride,
                                 lowbit_dtype v_type, void *stream);
@@ -605,6 +605,8 @@ lowbit_status lowbit_kv8_read(const lowbit_kv8_cache *cache, const lowbit_kv8_ba
  * (rounded; a single large entry makes the others' steps as large) and probabilities
  * as multiples of 1 / 65280 of the largest in 32 tokens; prompts take both as f16
  * after a power of two (q's, exactly but for entries below 2^-14 of the largest).
+ * Beside a page whose v_scales is 0, prompts are right where the others of its
+ * sequence and head lie within 2^-50 and 2^45.
  * workspace: lowbit_kv8_attention_workspace_bytes(cache, batch, q_heads) bytes,
  * zero-filled before its first use (calls leave what they need zeroed).  Calls
  * that share one must be ordered on one stream; that holds for replays of

@@ -23,8 +23,8 @@ Prompts (tcgen05):
           page's factor and the reference in fp32 as above: 2^-21 of |s_t - s_max| within the largest token's page,
           of |s_t| + |s_max| + |log vs| in others.  Exponentials: 2^-20.
   p       f16: 2^-11 of itself (half a step), or half of the smallest step 2^-24 where it is subnormal; the numerator
-          holds it rounded, the denominator not.  p is exp2(x - m + 7) with x = s + log2(vs) and m of at most the row's
-          largest x: half of that step is at most 2^-32 of exp(x_max - x_t) p_t.
+          holds it rounded, the denominator not.  p is exp2(x - m + 7) with x = s + log2(vs), vs = 2^-60 for a page
+          of zeros, and m of at most the row's largest x: half of that step is at most 2^-32 of exp(x_max - x_t) p_t.
 Both: fp32 sums over n tokens in tiles, 2^-24 (n / 32 + 64) sum_t p_t |v_t|; the output 2^-8 of itself (bf16)."""
 import numpy as np
 
@@ -107,10 +107,11 @@ def check(cache, table, lens, q, scale, row_start, out, untouched=-7.0, vacuous=
                 e = np.where(token // P == at // P, np.abs(fin - top), np.abs(fin) + np.abs(top) + lv + lv.max())
                 e = 2.0 ** -21 * e + 17 * D / 16 * 2.0 ** -23 * (size + np.take_along_axis(size, at, 1)) + 2.0 ** -20
                 e = np.where(token == at, 0.0, e)
-                # in units of x = s + ln vs, whose maximum the reference follows; pages of zeros have nothing to lose
-                x = np.where(vis & (vsn > 0)[None], s + np.log(np.where(vsn > 0, vsn, 1.0))[None], -np.inf)
+                # in units of x = s + ln vs, whose maximum the reference follows; a page of zeros stands with 2^-60 there,
+                # and has nothing to lose itself
+                x = np.where(vis, s + np.log(np.where(vsn > 2.0 ** -100, vsn, 2.0 ** -60))[None], -np.inf)
                 xm = x.max(1, keepdims=True)
-                lost = np.where(np.isfinite(x), np.minimum(xm, 1e300) - np.where(np.isfinite(x), x, 0.0), -np.inf)
+                lost = np.where(vis & (vsn > 2.0 ** -100)[None], xm - np.where(vis, x, xm), -np.inf)
                 d = np.where(vis, np.exp(np.minimum(lost + fin - top, 700.0)) / total * 2.0 ** -32, 0.0) + p * 2.0 ** -11
             else:
                 tiles = -(-n // 32)

@@ -135,3 +135,19 @@ def test_a_leading_token_without_value(lb, rows, H, G, D, lead):
     q = torch.ones((rows, H * G, D), device="cuda").bfloat16()
     out = attend(lb, cache, table, [n], q, lead / D, starts([rows]))
     check(cache, table, [n], q, lead / D, starts([rows]), out)
+
+
+@pytest.mark.parametrize("power", [-50, -20, 0, 20, 45])
+@pytest.mark.parametrize("rows,H,G", [(1, 2, 4), (9, 1, 8), (600, 2, 8)])
+def test_pages_of_zero_values(lb, rows, H, G, power):
+    """Pages whose values' scale is 0 (the first, some within, most of them) beside others of any usual magnitude."""
+    D, P, n = 64, 32, 1000
+    n_pages, table = make_batch(21, [n], P)
+    for zero in ([0], [0, 1, 2, 3, 7, 20], list(range(0, 30)), [31]):
+        cache = make_cache(lb, 22, n_pages, H, P, D)
+        cache.v_scales *= 2.0 ** power
+        cache.v_scales[table[0][zero].tolist()] = 0
+        q = queries(23, rows, H * G, D) * 2
+        out = attend(lb, cache, table, [n], q, 0.125, starts([rows]))
+        check(cache, table, [n], q, 0.125, starts([rows]), out)
+        assert out.any()
