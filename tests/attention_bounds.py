@@ -25,7 +25,8 @@ Prompts (tcgen05):
   p       f16: 2^-11 of itself (half a step), or half of the smallest step 2^-24 where it is subnormal; the numerator
           holds it rounded, the denominator not.  p is exp2(x - m + 7) with x = s + log2(vs), vs = 2^-60 for a page
           of zeros, and m of at most the row's largest x: half of that step is at most 2^-32 of exp(x_max - x_t) p_t.
-Both: fp32 sums over n tokens in tiles, 2^-24 (n / 32 + 64) sum_t p_t |v_t|; the output 2^-8 of itself (bf16)."""
+Both: fp32 sums over n tokens in tiles, 2^-24 (n / 32 + 64) sum_t p_t |v_t|; exponentials below 2^-126 are zero, n 2^-126 of
+the largest value; the output 2^-8 of itself (bf16), or half of its smallest step, 2^-134."""
 import numpy as np
 
 LN2 = float(np.log(2.0))
@@ -127,7 +128,7 @@ def check(cache, table, lens, q, scale, row_start, out, untouched=-7.0, vacuous=
             most = np.abs(vv).max()
             tol = (c @ np.abs(vv) + np.abs(o) * moved) / np.where(ok, 1 - moved, 1.0)
             tol = tol + 2.0 ** -24 * (n / 32 + 64) * (p @ np.abs(vv))
-            tol = tol * 1.01 + 2.0 ** -8 * np.abs(o) * 1.01 + 1e-44
+            tol = (tol + n * 2.0 ** -126 * most) * 1.01 + 2.0 ** -8 * np.abs(o) * 1.01 + 2.0 ** -134
             says = (ok & (tol <= vacuous * most + 1e-40)).all(1)
             n_rows, n_loose = n_rows + len(says), n_loose + int((~says).sum())
             diff = np.where(ok, np.abs(got - o), 0.0)
